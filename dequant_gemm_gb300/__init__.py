@@ -1,4 +1,6 @@
-"""GB300-native NF4 quantization and fused NF4-dequant matmul.
+"""GB300-native NF4 quantization and fused NF4-dequant matmul, with 8-bit
+floating point products (``fp8.py``) and the RMS norm between them
+(``norm.py``).
 
 A thin Python binding over the C ABI of ``libnf4gemm.so`` (declared in
 ``include/nf4gemm.h``): the functions below only allocate outputs with
@@ -31,6 +33,8 @@ STATUS = {
 # Every symbol the header declares, for load checks.
 EXPORTS = ("nf4_quantize", "nf4_quantize_ex", "nf4_dequantize", "nf4_dequantize_ex", "nf4_matmul_fwd",
            "nf4_matmul_bwd_dx", "nf4_matmul_fwd_ex", "nf4_matmul_bwd_dx_ex", "nf4_matmul_fwd_group",
+           "nf4_fp8_quantize", "nf4_fp8_dequantize", "nf4_fp8_matmul_fwd", "nf4_fp8_matmul_bwd_dx",
+           "nf4_rmsnorm_fwd", "nf4_rmsnorm_bwd", "nf4_rmsnorm_bwd_workspace",
            "nf4_poll_device_status", "nf4_poll_device_status_site", "nf4_codebook",
            "nf4_codebook_of", "nf4_set_mma_wait_limit", "nf4_last_cuda_error",
            "nf4_status_string")
@@ -58,6 +62,11 @@ class nf4_weight(ctypes.Structure):
                 ("dq_group", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class nf4_fp8_tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("block_rows", ctypes.c_int32)]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -65,6 +74,8 @@ _lib_lock = threading.Lock()
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -74,6 +85,8 @@ def lib() -> ctypes.CDLL:
             L = ctypes.CDLL(LIB_PATH)
             vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
             W = ctypes.POINTER(nf4_weight)
+            Q = ctypes.POINTER(nf4_fp8_tensor)
+            f32 = ctypes.c_float
             sig = {
                 "nf4_quantize": [vp, i64, i64, i32, vp, vp, vp, vp],
                 "nf4_quantize_ex": [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp],
@@ -84,6 +97,13 @@ def lib() -> ctypes.CDLL:
                 "nf4_matmul_fwd_ex": [vp, i32, i64, W, vp, i32, i32, vp],
                 "nf4_matmul_bwd_dx_ex": [vp, i32, i64, W, vp, i32, i32, vp],
                 "nf4_matmul_fwd_group": [vp, i32, i64, W, i32, vp, i32, i32, vp],
+                "nf4_fp8_quantize": [vp, i32, i64, i64, i32, vp, vp, vp],
+                "nf4_fp8_dequantize": [Q, vp, i32, vp],
+                "nf4_fp8_matmul_fwd": [Q, Q, vp, i32, i32, vp],
+                "nf4_fp8_matmul_bwd_dx": [Q, Q, vp, i32, i32, vp],
+                "nf4_rmsnorm_fwd": [vp, i32, vp, i32, vp, i32, i64, i64, f32, vp, vp, i32, vp, vp,
+                                    vp],
+                "nf4_rmsnorm_bwd": [vp, vp, vp, i32, vp, i32, vp, i64, i64, vp, vp, vp, i64, vp],
                 "nf4_poll_device_status": [vp],
                 "nf4_poll_device_status_site": [vp, vp],
                 "nf4_codebook": [vp],
@@ -94,6 +114,8 @@ def lib() -> ctypes.CDLL:
                 f = getattr(L, name)
                 f.argtypes = args
                 f.restype = ctypes.c_int32
+            L.nf4_rmsnorm_bwd_workspace.argtypes = [i64, i64]
+            L.nf4_rmsnorm_bwd_workspace.restype = i64
             L.nf4_status_string.argtypes = [ctypes.c_int32]
             L.nf4_status_string.restype = ctypes.c_char_p
             L.nf4_last_cuda_error.argtypes = []
@@ -117,6 +139,14 @@ def _ptr(t: torch.Tensor | None):
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _call_on(device: torch.device, fn, *args) -> int:
+    """fn(*args, stream) with `device` current; no switch where it already is."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, torch.cuda.current_stream(device).cuda_stream)
 
 
 @dataclass
@@ -400,3 +430,8 @@ def nf4_codebook(dtype: str = "nf4") -> torch.Tensor:
     buf = (ctypes.c_float * 16)()
     _check("nf4_codebook_of", lib().nf4_codebook_of(DTYPES[dtype], ctypes.cast(buf, ctypes.c_void_p)))
     return torch.tensor(list(buf), dtype=torch.float32)
+
+
+from .fp8 import (FP8_BLOCK, FP8Tensor, alloc_fp8, nf4_fp8_dequantize,  # noqa: E402
+                  nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd, nf4_fp8_quantize)
+from .norm import nf4_rmsnorm_bwd, nf4_rmsnorm_fwd  # noqa: E402

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "fp8.cuh"
 
 namespace {
 
@@ -210,6 +211,65 @@ nf4_status quantize(const void* W, int32_t w_elem, int64_t rows, int64_t cols, i
                                        absmax_scale, static_cast<cudaStream_t>(stream)));
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool valid_elem(int32_t e) { return e == NF4_F32 || e == NF4_BF16 || e == NF4_F16; }
+
+// Shape of a block-scaled e4m3 tensor (block_rows as the call needs it).
+nf4_status check_fp8(const nf4_fp8_tensor* t, int32_t block_rows) {
+  if (!t) return NF4_ERR_NULL;
+  if (t->block_rows != block_rows) return NF4_ERR_BLOCKSIZE;
+  if (t->rows < 0 || t->cols < 0 || (t->cols % 16) != 0) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+nf4_status check_fp8_ptrs(const nf4_fp8_tensor* t) {
+  if (!t->codes || !t->scale) return NF4_ERR_NULL;
+  if (!aligned16(t->codes) || !aligned4(t->scale)) return NF4_ERR_ALIGN;
+  return NF4_OK;
+}
+
+// The shared body of the e4m3 products.
+nf4_status fp8_matmul(bool dx, const nf4_fp8_tensor* a, const nf4_fp8_tensor* w, void* out,
+                      int32_t out_elem, int32_t flags, void* stream) {
+  if (nf4_status s = check_fp8(a, 1)) return s;
+  if (nf4_status s = check_fp8(w, nf4::kFp8Block)) return s;
+  if (out_elem != NF4_F32 && out_elem != NF4_BF16) return NF4_ERR_SHAPE;
+  if ((flags & ~NF4_ACCUMULATE) != 0) return NF4_ERR_SHAPE;
+  const int64_t red = dx ? w->rows : w->cols, out_cols = dx ? w->cols : w->rows;
+  if ((w->rows % 16) != 0 || a->cols != red) return NF4_ERR_SHAPE;
+  if (a->rows == 0 || out_cols == 0) return NF4_OK;
+  if (!out) return NF4_ERR_NULL;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (red == 0) {  // an empty reduction: the output is 0 (or unchanged when accumulating)
+    if ((flags & NF4_ACCUMULATE) != 0) return NF4_OK;
+    return launched(cudaMemsetAsync(
+        out, 0, static_cast<size_t>(a->rows) * out_cols * elem_bytes(out_elem), st));
+  }
+  if (nf4_status s = check_fp8_ptrs(a)) return s;
+  if (nf4_status s = check_fp8_ptrs(w)) return s;
+  if (!aligned16(out)) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  nf4::Fp8Call c;
+  c.dx = dx;
+  c.a = a->codes;
+  c.a_scale = a->scale;
+  c.w = w->codes;
+  c.w_scale = w->scale;
+  c.M = a->rows;
+  c.N = w->rows;
+  c.K = w->cols;
+  c.out = out;
+  c.out_bf16 = out_elem == NF4_BF16;
+  c.accumulate = (flags & NF4_ACCUMULATE) != 0;
+  c.num_sms = d->num_sms;
+  c.status = d->status;
+  c.wait_limit = g_mma_wait_limit.load(std::memory_order_relaxed);
+  c.device = d->ordinal;
+  c.st = st;
+  return launched(nf4::launch_fp8_matmul(c));
+}
+
 }  // namespace
 
 extern "C" {
@@ -268,6 +328,122 @@ nf4_status nf4_matmul_fwd_ex(const void* X, int32_t x_elem, int64_t M, const nf4
 nf4_status nf4_matmul_bwd_dx_ex(const void* dY, int32_t dy_elem, int64_t M, const nf4_weight* w,
                                 void* dX, int32_t dx_elem, int32_t flags, void* stream) {
   return matmul(true, dY, dy_elem, M, w, dX, dx_elem, flags, stream);
+}
+
+nf4_status nf4_fp8_quantize(const void* x, int32_t x_elem, int64_t rows, int64_t cols,
+                            int32_t block_rows, uint8_t* codes, float* scale, void* stream) {
+  if (block_rows != 1 && block_rows != nf4::kFp8Block) return NF4_ERR_BLOCKSIZE;
+  if (!valid_elem(x_elem) || rows < 0 || cols < 0 || (cols % 16) != 0) return NF4_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (!x || !codes || !scale) return NF4_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned4(scale)) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  return launched(nf4::launch_fp8_quantize(x, x_elem, rows, cols, block_rows, codes, scale,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+nf4_status nf4_fp8_dequantize(const nf4_fp8_tensor* q, void* out, int32_t out_elem, void* stream) {
+  if (!q) return NF4_ERR_NULL;
+  if (q->block_rows != 1 && q->block_rows != nf4::kFp8Block) return NF4_ERR_BLOCKSIZE;
+  if (nf4_status s = check_fp8(q, q->block_rows)) return s;
+  if (!valid_elem(out_elem)) return NF4_ERR_SHAPE;
+  if (q->rows == 0 || q->cols == 0) return NF4_OK;
+  if (nf4_status s = check_fp8_ptrs(q)) return s;
+  if (!out) return NF4_ERR_NULL;
+  if (!aligned16(out)) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  return launched(nf4::launch_fp8_dequantize(q->codes, q->scale, q->rows, q->cols, q->block_rows,
+                                             out, out_elem, static_cast<cudaStream_t>(stream)));
+}
+
+nf4_status nf4_fp8_matmul_fwd(const nf4_fp8_tensor* X, const nf4_fp8_tensor* W, void* Y,
+                              int32_t y_elem, int32_t flags, void* stream) {
+  return fp8_matmul(false, X, W, Y, y_elem, flags, stream);
+}
+
+nf4_status nf4_fp8_matmul_bwd_dx(const nf4_fp8_tensor* dY, const nf4_fp8_tensor* W, void* dX,
+                                 int32_t dx_elem, int32_t flags, void* stream) {
+  return fp8_matmul(true, dY, W, dX, dx_elem, flags, stream);
+}
+
+nf4_status nf4_rmsnorm_fwd(const void* x, int32_t x_elem, const void* residual, int32_t res_elem,
+                           const void* weight, int32_t w_elem, int64_t rows, int64_t cols,
+                           float eps, void* h, void* y, int32_t y_elem, float* scale, float* rstd,
+                           void* stream) {
+  if (!valid_elem(x_elem) || !valid_elem(w_elem)) return NF4_ERR_SHAPE;
+  if (residual && res_elem != x_elem && res_elem != NF4_F32) return NF4_ERR_SHAPE;
+  if (!scale && !valid_elem(y_elem)) return NF4_ERR_SHAPE;
+  if (!(eps >= 0.0f)) return NF4_ERR_SHAPE;
+  if (rows < 0 || rows > INT32_MAX || cols < 0 || (scale && (cols % 16) != 0)) return NF4_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (!x || !weight || !y || (residual ? !h : h != nullptr)) return NF4_ERR_NULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) ||
+      !aligned16(y) || !aligned4(scale) || !aligned4(rstd))
+    return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  nf4::NormFwdCall c;
+  c.x = x;
+  c.x_elem = x_elem;
+  c.residual = residual;
+  c.weight = weight;
+  c.w_elem = w_elem;
+  c.h = h;
+  c.h_elem = residual ? res_elem : x_elem;
+  c.y = y;
+  c.y_elem = y_elem;
+  c.y_fp8 = scale != nullptr;
+  c.scale = scale;
+  c.rstd = rstd;
+  c.rows = rows;
+  c.cols = cols;
+  c.eps = eps;
+  c.num_sms = d->num_sms;
+  c.st = static_cast<cudaStream_t>(stream);
+  return launched(nf4::launch_rmsnorm_fwd(c));
+}
+
+int64_t nf4_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return nf4::rmsnorm_bwd_parts(rows, cols) * cols * static_cast<int64_t>(sizeof(float));
+}
+
+nf4_status nf4_rmsnorm_bwd(const void* dy, const void* h, const void* dh, int32_t elem,
+                           const void* weight, int32_t w_elem, const float* rstd, int64_t rows,
+                           int64_t cols, void* dx, void* dweight, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  if (!valid_elem(elem) || !valid_elem(w_elem) || rows < 0 || rows > INT32_MAX || cols < 0)
+    return NF4_ERR_SHAPE;
+  if (cols == 0) return NF4_OK;
+  if (!dweight) return NF4_ERR_NULL;
+  if (!aligned16(dweight)) return NF4_ERR_ALIGN;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) return launched(cudaMemsetAsync(dweight, 0, cols * elem_bytes(w_elem), st));
+  if (!dy || !h || !weight || !rstd || !dx || !workspace) return NF4_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(dh) || !aligned16(weight) || !aligned4(rstd) ||
+      !aligned16(dx) || !aligned16(workspace))
+    return NF4_ERR_ALIGN;
+  if (workspace_bytes < nf4_rmsnorm_bwd_workspace(rows, cols)) return NF4_ERR_SHAPE;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  nf4::NormBwdCall c;
+  c.dy = dy;
+  c.h = h;
+  c.dh = dh;
+  c.elem = elem;
+  c.weight = weight;
+  c.w_elem = w_elem;
+  c.rstd = rstd;
+  c.dx = dx;
+  c.dweight = dweight;
+  c.partial = static_cast<float*>(workspace);
+  c.rows = rows;
+  c.cols = cols;
+  c.num_sms = d->num_sms;
+  c.st = st;
+  return launched(nf4::launch_rmsnorm_bwd(c));
 }
 
 nf4_status nf4_poll_device_status_site(void* stream, int32_t* site) {

@@ -48,8 +48,9 @@
  *
  * Conventions for every entry point:
  *  - Pointers marked "device" must be device-accessible (cudaMalloc'd or
- *    equivalent) and 16-byte aligned; the caller allocates and owns every
- *    buffer. The library allocates no device memory.
+ *    equivalent) and 16-byte aligned (4-byte where the declaration says so);
+ *    the caller allocates and owns every buffer. The library allocates no
+ *    device memory.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL means the legacy
  *    default stream) and do not synchronize, except nf4_poll_device_status.
  *  - Arguments are validated on the host before anything is launched; an
@@ -103,6 +104,9 @@ typedef enum nf4_elem {
 
 /* Most weights one nf4_matmul_fwd_group call takes. */
 #define NF4_GROUP_MAX 4
+
+/* Values along a row that share a scale of the 8-bit floating point format. */
+#define NF4_FP8_BLOCK 128
 
 /* A quantized weight (the QuantState of the bitsandbytes page, reduced to
  * plain device pointers). All arrays are device pointers owned by the
@@ -239,6 +243,98 @@ nf4_status nf4_matmul_bwd_dx_ex(const void* dY, int32_t dy_elem, int64_t M, cons
 nf4_status nf4_matmul_fwd_group(const void* X, int32_t x_elem, int64_t M, const nf4_weight* ws,
                                 int32_t count, void* const* Ys, int32_t y_elem, int32_t flags,
                                 void* stream);
+
+/* --------------------------------------------------------------------------
+ * 8-bit floating point operands with a scale for each block, and the RMS norm
+ * that produces them. These are this library's additions beside the formats
+ * above: the product runs on the tensor cores' 8-bit rate, and the norm in
+ * front of it writes codes and scales directly.
+ *
+ * Storage format (row-major, contiguous): codes are e4m3 (4 exponent bits, 3
+ * mantissa bits, largest value 448, no infinities); a block of 1 x 128 values
+ * (activations and gradients, block_rows = 1) or 128 x 128 values (weights,
+ * block_rows = 128) shares an fp32 scale. The last block of a row or a column
+ * may be short.
+ *   a = max |x| of the block, s = fl32(a / 448),
+ *   q = e4m3(fl32(x * fl32(1 / s))), to nearest even, saturating;
+ *   value = q * s.
+ * A block with a < 2^-117 has s = 0 and zero codes. A NaN or an infinity
+ * makes its whole block NaN. Scales given by the caller may be any fp32
+ * values; they multiply the block's products as they are.
+ * ------------------------------------------------------------------------ */
+typedef struct nf4_fp8_tensor {
+  const uint8_t* codes;         /* [rows * cols], 16-byte aligned                           */
+  const float* scale;           /* [ceil(rows / block_rows) * ceil(cols / 128)], 4-byte aligned */
+  int64_t rows;
+  int64_t cols;                 /* % 16 == 0                                                */
+  int32_t block_rows;           /* 1 or 128                                                 */
+} nf4_fp8_tensor;
+
+/* Quantize x [rows, cols] of x_elem (NF4_F32, NF4_BF16 or NF4_F16) in blocks
+ * of block_rows x 128.
+ *   codes device uint8 [rows * cols] (output)
+ *   scale device fp32 [ceil(rows / block_rows) * ceil(cols / 128)] (output, 4-byte aligned)
+ * cols % 16 != 0 or an unknown x_elem is NF4_ERR_SHAPE; block_rows other than
+ * 1 and 128 NF4_ERR_BLOCKSIZE. */
+nf4_status nf4_fp8_quantize(const void* x, int32_t x_elem, int64_t rows, int64_t cols,
+                            int32_t block_rows, uint8_t* codes, float* scale, void* stream);
+
+/* The values of q, each rounded once to out_elem (NF4_F32, NF4_BF16 or
+ * NF4_F16): out device [rows, cols]. */
+nf4_status nf4_fp8_dequantize(const nf4_fp8_tensor* q, void* out, int32_t out_elem, void* stream);
+
+/* Y = value(X) * value(W)^T: X [M, cols] with block_rows 1, W [rows, cols]
+ * with block_rows 128, Y device [M, rows] of y_elem NF4_F32 or NF4_BF16.
+ * flags: NF4_ACCUMULATE adds to Y's contents. Requires W.rows % 16 == 0 and
+ * X.cols == W.cols (NF4_ERR_SHAPE otherwise); block_rows otherwise is
+ * NF4_ERR_BLOCKSIZE. The products of a 128-block are summed in fp32 on the
+ * tensor cores, multiplied by the block's two scales in fp32 and added up in
+ * fp32; a bf16 Y is rounded once. Sums are taken in a fixed order: results
+ * are bitwise repeatable. */
+nf4_status nf4_fp8_matmul_fwd(const nf4_fp8_tensor* X, const nf4_fp8_tensor* W, void* Y,
+                              int32_t y_elem, int32_t flags, void* stream);
+
+/* The input gradient of the frozen weight, dX = value(dY) * value(W): dY
+ * [M, rows] with block_rows 1 (quantized along rows), W as above, dX device
+ * [M, cols] of dx_elem. Otherwise as nf4_fp8_matmul_fwd. */
+nf4_status nf4_fp8_matmul_bwd_dx(const nf4_fp8_tensor* dY, const nf4_fp8_tensor* W, void* dX,
+                                 int32_t dx_elem, int32_t flags, void* stream);
+
+/* Per row of x [rows, cols]:
+ *   h = x + residual, rounded to res_elem (residual NULL: h = x, not written)
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
+ *   x        device, x_elem NF4_F32, NF4_BF16 or NF4_F16
+ *   residual device [rows, cols] of res_elem = x_elem or NF4_F32, or NULL
+ *   weight   device [cols] of w_elem, any of the three
+ *   h        device [rows, cols] of res_elem (output; residual's buffer, or
+ *            x's where the types agree, may be given); NULL without a residual
+ *   y        device [rows, cols] of y_elem (output); with scale not NULL,
+ *            e4m3 codes in 1 x 128 blocks instead (y_elem is then ignored and
+ *            cols % 16 == 0 required)
+ *   scale    device fp32 [rows * ceil(cols / 128)] (output, 4-byte aligned), or NULL
+ *   rstd     device fp32 [rows] (output, 4-byte aligned), or NULL
+ * The statistics are fp32; y is rounded once, from h as rounded. Any cols. */
+nf4_status nf4_rmsnorm_fwd(const void* x, int32_t x_elem, const void* residual, int32_t res_elem,
+                           const void* weight, int32_t w_elem, int64_t rows, int64_t cols,
+                           float eps, void* h, void* y, int32_t y_elem, float* scale, float* rstd,
+                           void* stream);
+
+/* Bytes of device workspace that nf4_rmsnorm_bwd needs (host only). */
+int64_t nf4_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+
+/* The gradients of nf4_rmsnorm_fwd (an e4m3 y passes its gradient through):
+ *   dx = rstd * (dy w - xh * mean(dy w xh)) + dh,  xh = h * rstd
+ *   dweight = sum over rows of dy * xh
+ *   dy, h, dx device [rows, cols] of elem; dh the gradient that reaches h
+ *   from the residual stream, [rows, cols] of elem, or NULL; dx is the
+ *   gradient of x and of the residual alike, and may be dy's or dh's buffer
+ *   weight, dweight device [cols] of w_elem; rstd device fp32 [rows] (4-byte aligned)
+ *   workspace device, nf4_rmsnorm_bwd_workspace bytes (contents: any)
+ * rows = 0 gives dweight = 0. Sums are taken in a fixed order. */
+nf4_status nf4_rmsnorm_bwd(const void* dy, const void* h, const void* dh, int32_t elem,
+                           const void* weight, int32_t w_elem, const float* rstd, int64_t rows,
+                           int64_t cols, void* dx, void* dweight, void* workspace,
+                           int64_t workspace_bytes, void* stream);
 
 /* Synchronizes `stream`, then reports and clears the device status word of
  * the current device: NF4_ERR_DEVICE_TIMEOUT if any kernel's bounded wait ran
