@@ -16,6 +16,9 @@
 
 namespace nf4 {
 
+// Kernel numbers of report_status (see nf4_poll_device_status_site).
+constexpr uint32_t kSiteFp8Fwd = 4, kSiteFp8Dx = 5;
+
 constexpr int kFp8Block = NF4_FP8_BLOCK;      // 128
 constexpr float kE4m3Max = 448.0f;
 constexpr float kFp8MinAmax = 6.018531076210112e-36f;   // 2^-117

@@ -3,14 +3,434 @@
 //   input grad dX[m, k] = sum_b sy[m, b] sw[b, k / 128] sum_{n in b} qy[m, n] qw[n, k]
 // (b: the 128-wide blocks of the reduction; the weight is frozen, so there is
 // no weight gradient.)
+//
+// The inner sums run on the tensor cores (tcgen05, kind::f8f6f4, fp32
+// accumulators in tensor memory). The scales are fp32 and differ from block
+// to block along the reduction, so no accumulator can run on across blocks:
+// each block's sums go to a fresh tensor-memory buffer, and warps read them
+// back, multiply by the block's scales and add them into fp32 totals held in
+// registers, while the tensor cores fill the next buffer.
 #include <algorithm>
 
 #include "fp8.cuh"
+#include "tc.cuh"
 
 namespace nf4 {
 namespace {
 
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs, fp32 accumulate, K = 32; kCg
+// as for the 16-bit products.
+template <int kCg>
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kCg == 1) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// Instruction descriptor for kind::f8f6f4 with A and B e4m3 (format 0), fp32
+// D; fields as in the 16-bit kind's.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(uint32_t m, uint32_t n, bool a_mn_major,
+                                                    bool b_mn_major) {
+  return (1u << 4) | (a_mn_major ? (1u << 15) : 0u) | (b_mn_major ? (1u << 16) : 0u) |
+         ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// 32 consecutive 32-bit columns of this warp's lane quarter (no wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+        "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// acc += s * v, two at a time.
+template <int kN>
+__device__ __forceinline__ void scale_add(float* acc, const float (&v)[kN], float s) {
+  const float2 s2 = make_float2(s, s);
+#pragma unroll
+  for (int j = 0; j < kN; j += 2) {
+    const float2 r = __ffma2_rn(make_float2(v[j], v[j + 1]), s2, make_float2(acc[j], acc[j + 1]));
+    acc[j] = r.x;
+    acc[j + 1] = r.y;
+  }
+}
+
 struct MatmulArgs {
+  const float *a_scale, *w_scale;
+  void* out;
+  int64_t M, cols;         // out [M, cols]
+  int rb;                  // 128-blocks of the reduction
+  int64_t ws_col, ws_red;  // strides of w_scale along column and reduction blocks
+  int m_units, units;      // token tiles; all tiles
+  int out_bf16, accumulate;
+  int dx;
+  long long mma_wait_limit;
+  int* status;
+};
+
+// ------------------------------------------------------------ pair kernel --
+// Large token counts. A CTA pair (cta_group::2) computes 256 tokens x 256
+// columns: each CTA stages its 128 tokens and half of the weight tile (128
+// columns), and receives the sums of its tokens with all 256 columns, so that
+// a block's 32 KB of operands a CTA feed 512 cycles of MMA (a single CTA
+// with the same tile would stage 48 KB for them, more than shared memory
+// carries besides the tensor core's own reads).
+//   warp 0     copies: the block's activation and weight tiles, by TMA
+//   warp 1     even CTA: the four MMAs (K = 32 each) of a block into one of
+//              two 256-column buffers; odd CTA: tells the even one when its
+//              copies have landed
+//   warps 4-11 totals: a thread holds 128 columns of one token (lane quarter
+//              warp % 4, column half (warp - 4) / 4). The token's scale times
+//              the column half's is one factor a thread and block.
+// The 128 totals of a thread need more registers than the launch's even share
+// of 168: the first four warps give theirs up.
+// Persistent: a pair takes the tiles c, c + G, ... in turn, tokens fastest,
+// and the copies and MMAs of the next tile start while one is written out.
+constexpr int kPairStages = 6;
+constexpr int kPairBN = 256;
+constexpr int kTileBytes = 128 * 128;                  // 128 rows of one block
+constexpr int kPairStageBytes = 2 * kTileBytes;
+constexpr int kPairTotalWarps = 8;
+constexpr int kPairThreads = 32 * (4 + kPairTotalWarps);
+// registers a thread after the split: 128 x 56 + 256 x 224 = 384 x 168, the launch's own
+constexpr int kPairFewRegs = 56, kPairManyRegs = 224;
+static_assert(128 * kPairFewRegs + 256 * kPairManyRegs <= kPairThreads * 168, "register split");
+constexpr int kBoxBytes = 32 * 128;                    // a warp's 32 rows x 128 bytes of output
+constexpr int kPairOffBox = kPairStages * kPairStageBytes;
+constexpr int kPairOffBars = kPairOffBox + kPairTotalWarps * kBoxBytes;
+constexpr int kPairSmem = kPairOffBars + 256 + 1024;   // + alignment slack
+static_assert(kPairSmem <= 227 * 1024, "shared memory");
+
+// Where a thread reads the scales of its token and column half: ahead of
+// their use (a load takes longer than a block's MMAs), running on across tiles.
+struct ScaleCursor {
+  const float *as, *ws;    // next block's scales (as null outside the output)
+  int left, u;             // blocks left in the tile; tile
+};
+
+template <bool kDx>
+__global__ void __launch_bounds__(kPairThreads, 1)
+fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                const __grid_constant__ CUtensorMap tm_out, const MatmulArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t base = tc::smem_addr(smem), bars = base + kPairOffBars;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (kPairStages + s); };
+  auto sum_bar = [&](int b) { return bars + 8u * (2 * kPairStages + b); };       // buffer's sums done
+  auto read_bar = [&](int b) { return bars + 8u * (2 * kPairStages + 2 + b); };  // and read back
+  const uint32_t drain_bar = bars + 8u * (2 * kPairStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBars + 8 * (2 * kPairStages + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_ctarank();
+  const int cid = static_cast<int>(blockIdx.x >> 1), ncl = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      // the even CTA's stage is full once its own copies and the peer's have landed
+      tc::mbar_init(full_bar(s), rank == 0 ? 2 : 1);
+      tc::mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(sum_bar(b), 1);
+      tc::mbar_init(read_bar(b), 2 * kPairTotalWarps);
+    }
+    tc::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tensormap(&tm_a);
+    tc::prefetch_tensormap(&tm_w);
+    tc::prefetch_tensormap(&tm_out);
+  }
+  if (warp == 1) tc::tmem_alloc<2>(tc::smem_addr(tmem_slot), 512);
+  tc::fence_before_sync();
+  tc::cluster_sync();                  // the peer's barriers exist before any arrival
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&](uint32_t role) {
+    report_status(p.status, kStatusTimeout, kDx ? kSiteFp8Dx : kSiteFp8Fwd, role);
+    *abort_flag = 1;
+    const uint32_t peer = tc::mapa(tc::smem_addr(const_cast<int*>(abort_flag)), rank ^ 1u);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer), "r"(1u) : "memory");
+  };
+  auto tile_m = [&](int u) { return static_cast<int64_t>(u % p.m_units) * 256 + rank * 128; };
+  auto tile_c = [&](int u) { return static_cast<int64_t>(u / p.m_units) * kPairBN; };
+
+  if (warp < 4) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFewRegs));
+   if (warp == 0) {
+    // The whole warp runs the loops of warps 0 and 1 on uniform values and one
+    // elected lane issues, as in the 16-bit kernel.
+    int gs = 0, slot = 0;
+    uint32_t ph = 0;
+    bool stop = false;
+    for (int u = cid; u < p.units && !stop; u += ncl) {
+      const int32_t m = static_cast<int32_t>(tile_m(u));
+      const int32_t c = static_cast<int32_t>(tile_c(u)) + static_cast<int32_t>(rank) * 128;
+      for (int i = 0; i < p.rb; ++i, ++gs) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) { stop = true; break; }
+        int r = tc::mbar_wait_abortable(empty_bar(slot), ph ^ 1, abort_flag);
+        r = __shfl_sync(0xffffffffu, r, 0);
+        if (r != tc::kWaitDone) {
+          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleProducer);
+          stop = true;
+          break;
+        }
+        const uint32_t dst = base + slot * kPairStageBytes;
+        if (tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(full_bar(slot), kPairStageBytes);
+          tc::tma_load_2d(dst, &tm_a, i * 128, m, full_bar(slot));
+          if (kDx) tc::tma_load_2d(dst + kTileBytes, &tm_w, c, i * 128, full_bar(slot));
+          else tc::tma_load_2d(dst + kTileBytes, &tm_w, i * 128, c, full_bar(slot));
+        }
+        __syncwarp();
+        if (++slot == kPairStages) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // copies in flight after an abort land before the CTA exits: the even
+    // CTA's barrier also counts the peer's arrival, which may not come any more
+    // (then the wait runs to its limit)
+    if (*abort_flag && lane == 0)
+      for (int g = max(0, gs - kPairStages); g < gs; ++g)
+        tc::mbar_wait(full_bar(g % kPairStages), (g / kPairStages) & 1, 1ll << 24);
+   } else if (warp == 1) {
+    int slot = 0;
+    uint32_t ph = 0;
+    bool stop = false;
+    if (rank != 0) {
+      for (int u = cid; u < p.units && !stop; u += ncl)
+        for (int i = 0; i < p.rb; ++i) {
+          int r = tc::mbar_wait_abortable(full_bar(slot), ph, abort_flag);
+          r = __shfl_sync(0xffffffffu, r, 0);
+          if (r != tc::kWaitDone) {
+            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
+            stop = true;
+            break;
+          }
+          if (tc::elect_one()) tc::mbar_arrive_remote(tc::mapa(full_bar(slot), 0));
+          __syncwarp();
+          if (++slot == kPairStages) {
+            slot = 0;
+            ph ^= 1u;
+          }
+        }
+    } else {
+      const uint32_t idesc = idesc_f8_f32(256, kPairBN, false, kDx);
+      const uint64_t adesc0 = tc::sw128_kmajor_desc(base);
+      // input gradient: the weight tile's rows are the reduction, 128 columns
+      // (one swizzled atom wide) each, 8-row groups 1 KB apart
+      const uint64_t bdesc0 = kDx ? tc::sw128_mnmajor_desc(base + kTileBytes, 0, 1024)
+                                  : tc::sw128_kmajor_desc(base + kTileBytes);
+      constexpr uint32_t kBStep = kDx ? 32 * 128 / 16 : 2;   // 32 of the reduction
+      int g = 0;
+      for (int u = cid; u < p.units && !stop; u += ncl) {
+        for (int i = 0; i < p.rb; ++i, ++g) {
+          const int b = g & 1;
+          int r = tc::mbar_spin_abortable<true>(read_bar(b), ((g >> 1) & 1) ^ 1, abort_flag, 1ll << 31);
+          if (r == tc::kWaitDone)
+            r = tc::mbar_spin_abortable<true>(full_bar(slot), ph, abort_flag, p.mma_wait_limit);
+          r = __shfl_sync(0xffffffffu, r, 0);
+          if (r != tc::kWaitDone) {
+            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
+            stop = true;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint64_t off = static_cast<uint64_t>(slot * (kPairStageBytes >> 4));
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_f8_ss<2>(tmem + 256u * b, adesc0 + off + 2u * j, bdesc0 + off + kBStep * j, idesc,
+                           j != 0 ? 1u : 0u);
+            tc::mma_commit<2>(empty_bar(slot));
+            tc::mma_commit<2>(sum_bar(b));
+          }
+          __syncwarp();
+          if (++slot == kPairStages) {
+            slot = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (tc::elect_one()) tc::mma_commit<2>(drain_bar);
+      __syncwarp();
+      if (lane == 0 && !tc::mbar_wait(drain_bar, 0)) fail(kRoleMma);
+    }
+   }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairManyRegs));
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128u * half;
+    uint8_t* box = smem + kPairOffBox + (warp - 4) * kBoxBytes;
+    const uint32_t box_addr = tc::smem_addr(box);
+    const int row = 32 * q + lane;       // token of this thread within the CTA's 128
+    const int64_t col_blocks = (p.cols + 127) / 128;
+
+    ScaleCursor cur;
+    auto aim = [&](int u) {              // the cursor at tile u's first block
+      cur.u = u;
+      cur.left = p.rb;
+      const int64_t m = tile_m(u) + row, cb = tile_c(u) / 128 + half;
+      const bool in = u < p.units && m < p.M && cb < col_blocks;
+      cur.as = in ? p.a_scale + m * p.rb : nullptr;
+      cur.ws = p.w_scale + cb * p.ws_col;
+    };
+    // four blocks' scales in use and the next four on their way: a value is
+    // not touched until the chunk after the one that loads it
+    float now[4], sa[4], sw[4];
+    auto fetch = [&] {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sa[j] = sw[j] = 0.0f;
+        if (j < cur.left && cur.as) {
+          sa[j] = __ldg(cur.as + j);
+          sw[j] = __ldg(cur.ws + j * p.ws_red);
+        }
+      }
+      cur.left -= 4;
+      if (cur.left <= 0) {
+        aim(cur.u + ncl);
+      } else {
+        if (cur.as) cur.as += 4;
+        cur.ws += 4 * p.ws_red;
+      }
+    };
+    aim(cid);
+    fetch();
+
+    int g = 0;
+    bool stop = false;
+    for (int u = cid; u < p.units && !stop; u += ncl) {
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      for (int i = 0; i < p.rb; ++i, ++g) {
+        if ((i & 3) == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) now[j] = sa[j] * sw[j];
+          fetch();
+        }
+        const float s = now[0];
+        now[0] = now[1];
+        now[1] = now[2];
+        now[2] = now[3];
+        const int b = g & 1;
+        int r = tc::mbar_wait_abortable(sum_bar(b), (g >> 1) & 1, abort_flag);
+        r = __shfl_sync(0xffffffffu, r, 0);
+        if (r != tc::kWaitDone) {
+          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleCompute);
+          stop = true;
+          break;
+        }
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(src + 256u * b + 32u * c, v);
+          tc::tmem_wait_ld();
+          if (c == 3) {                  // the buffer is free once the last read is done
+            tc::fence_before_sync();
+            if (lane == 0) tc::mbar_arrive_remote(tc::mapa(read_bar(b), 0));
+          }
+          scale_add<32>(acc + 32 * c, v, s);
+        }
+      }
+      if (stop) break;
+      // out: 128 columns of 32 tokens a warp, in boxes of 128 bytes a row whose
+      // 16-byte chunks are swizzled by the row (no bank conflicts); rows and
+      // columns past the end are dropped by the copy
+      const int64_t m0 = tile_m(u) + 32 * q, m = m0 + lane, c0 = tile_c(u) + 128 * half;
+      if (m0 >= p.M || c0 >= p.cols) continue;
+      if (p.accumulate && m < p.M) {
+#pragma unroll
+        for (int j = 0; j < 128; j += 8) {
+          if (c0 + j >= p.cols) break;
+          float o[8];
+          if (p.out_bf16) load8<kElemBf16>(p.out, m * p.cols + c0 + j, o);
+          else load8<kElemF32>(p.out, m * p.cols + c0 + j, o);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) acc[j + t] += o[t];
+        }
+      }
+      auto send = [&](int64_t c) {
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && c < p.cols) {
+          tc::tma_store_2d(&tm_out, box_addr, static_cast<int32_t>(c), static_cast<int32_t>(m0));
+          tc::bulk_commit();
+        }
+      };
+      auto reuse = [&] {                 // the box's previous contents have been read
+        if (lane == 0) tc::bulk_wait_read_all();
+        __syncwarp();
+      };
+      uint4* rowp = reinterpret_cast<uint4*>(box + 128 * lane);
+      if (p.out_bf16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          reuse();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float* a = acc + 64 * h + 8 * j;
+            rowp[j ^ (lane & 7)] = make_uint4(pack2<kElemBf16>(a[0], a[1]), pack2<kElemBf16>(a[2], a[3]),
+                                              pack2<kElemBf16>(a[4], a[5]), pack2<kElemBf16>(a[6], a[7]));
+          }
+          send(c0 + 64 * h);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          reuse();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float* a = acc + 32 * h + 4 * j;
+            *reinterpret_cast<float4*>(&rowp[j ^ (lane & 7)]) = make_float4(a[0], a[1], a[2], a[3]);
+          }
+          send(c0 + 32 * h);
+        }
+      }
+    }
+    if (lane == 0) tc::bulk_wait_all();
+  }
+
+  // neither CTA frees its tensor memory or leaves before both are done
+  tc::fence_before_sync();
+  tc::cluster_sync();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc<2>(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------- simple kernel --
+struct SimpleArgs {
   const uint8_t *a, *w;
   const float *a_scale, *w_scale;
   int64_t M, red, cols;    // out [M, cols]
@@ -23,7 +443,7 @@ struct MatmulArgs {
 // 64 x 64 outputs a CTA, 4 x 4 a thread, one 128-wide block at a time staged
 // in shared memory as fp32 in two halves of 64.
 template <bool kDx>
-__global__ void __launch_bounds__(256) fp8_matmul_simple_kernel(const MatmulArgs p) {
+__global__ void __launch_bounds__(256) fp8_matmul_simple_kernel(const SimpleArgs p) {
   __shared__ float As[64][65], Bs[64][65];   // [reduction][token], [reduction][column]
   const int64_t m0 = blockIdx.y * 64ll, c0 = blockIdx.x * 64ll;
   const int tm = (threadIdx.x >> 4) * 4, tc = (threadIdx.x & 15) * 4;
@@ -91,20 +511,81 @@ __global__ void __launch_bounds__(256) fp8_matmul_simple_kernel(const MatmulArgs
     }
 }
 
+
+}  // namespace
+
+namespace {
+template <bool kDx>
+cudaError_t launch_pair(const Fp8Call& c, const MatmulArgs& args, int64_t red) {
+  MatmulArgs a = args;
+  const int64_t m_units = (c.M + 255) / 256, c_units = (a.cols + kPairBN - 1) / kPairBN;
+  a.m_units = static_cast<int>(m_units);
+  a.units = static_cast<int>(m_units * c_units);
+  CUtensorMap tm_a, tm_w, tm_out;
+  const uint64_t ur = static_cast<uint64_t>(red), um = static_cast<uint64_t>(c.M);
+  const uint64_t pitch = static_cast<uint64_t>(a.cols) * (c.out_bf16 ? 2 : 4);
+  if (!encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.a, ur, um, ur, 128, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w, static_cast<uint64_t>(c.K),
+                 static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.K), 128, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tm_out, c.out_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                 c.out, static_cast<uint64_t>(a.cols), um, pitch, c.out_bf16 ? 64 : 32, 32,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  static std::once_flag once[kOnceDevices];
+  once_per_device(once, c.device, [] {
+    cudaFuncSetAttribute(fp8_pair_kernel<kDx>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  });
+  const int64_t pairs = std::min<int64_t>(a.units, std::max(1, c.num_sms / 2));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = c.st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<kDx>, tm_a, tm_w, tm_out, a);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const Fp8Call& c) {
-  MatmulArgs a;
+  const int64_t red = c.dx ? c.N : c.K, cols = c.dx ? c.K : c.N;
+  const int64_t kb = (c.K + 127) / 128;
+  if (c.M > 128) {
+    MatmulArgs a = {};
+    a.a_scale = c.a_scale;
+    a.w_scale = c.w_scale;
+    a.out = c.out;
+    a.M = c.M;
+    a.cols = cols;
+    a.rb = static_cast<int>((red + 127) / 128);
+    a.ws_col = c.dx ? 1 : kb;
+    a.ws_red = c.dx ? kb : 1;
+    a.out_bf16 = c.out_bf16;
+    a.accumulate = c.accumulate;
+    a.dx = c.dx;
+    a.mma_wait_limit = c.wait_limit;
+    a.status = c.status;
+    return c.dx ? launch_pair<true>(c, a, red) : launch_pair<false>(c, a, red);
+  }
+  SimpleArgs a;
   a.a = c.a;
   a.w = c.w;
   a.a_scale = c.a_scale;
   a.w_scale = c.w_scale;
   a.M = c.M;
-  a.red = c.dx ? c.N : c.K;
-  a.cols = c.dx ? c.K : c.N;
+  a.red = red;
+  a.cols = cols;
   a.w_pitch = c.K;
   a.rb = static_cast<int>((a.red + 127) / 128);
-  a.kb = static_cast<int>((c.K + 127) / 128);
+  a.kb = static_cast<int>(kb);
   a.out = c.out;
   a.out_bf16 = c.out_bf16;
   a.accumulate = c.accumulate;

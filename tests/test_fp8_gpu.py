@@ -85,7 +85,7 @@ def test_quantize_of_extreme_values(block_rows):
     assert v[129].isnan().any() == (block_rows == 128) and not v[:128].isnan().any()
 
 
-SHAPES = [(1, 16, 16), (1, 512, 4096), (2, 144, 272), (5, 4096, 528), (16, 272, 1040), (17, 256, 128),
+SHAPES = [(1, 16, 16), (300, 16, 16), (1, 512, 4096), (2, 144, 272), (5, 4096, 528), (16, 272, 1040), (17, 256, 128),
           (33, 1040, 400), (64, 528, 2064), (65, 128, 144), (100, 2048, 640), (128, 272, 272),
           (129, 400, 528), (250, 512, 896), (300, 1040, 1552), (513, 2064, 1040), (1000, 784, 3600)]
 
