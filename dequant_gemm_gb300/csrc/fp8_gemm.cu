@@ -63,6 +63,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "memory");
 }
 
+// Arrive on an mbarrier of the cluster without ordering this thread's memory
+// accesses: what it hands over is tensor memory whose reads have completed
+// (tcgen05.wait::ld). The releasing form cost the reading warps 350 cycles a
+// block.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 // acc += s * v, two at a time.
 template <int kN>
 __device__ __forceinline__ void scale_add(float* acc, const float (&v)[kN], float s) {
@@ -99,6 +108,7 @@ struct MatmulArgs {
 //   warp 1     even CTA: the four MMAs (K = 32 each) of a block into one of
 //              two 256-column buffers; odd CTA: tells the even one when its
 //              copies have landed
+//   warps 2-3  scales: the tokens', transposed, and the weight's into shared memory
 //   warps 4-11 totals: a thread holds 128 columns of one token (lane quarter
 //              warp % 4, column half (warp - 4) / 4). The token's scale times
 //              the column half's is one factor a thread and block.
@@ -106,7 +116,7 @@ struct MatmulArgs {
 // of 168: the first four warps give theirs up.
 // Persistent: a pair takes the tiles c, c + G, ... in turn, tokens fastest,
 // and the copies and MMAs of the next tile start while one is written out.
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr int kPairBN = 256;
 constexpr int kTileBytes = 128 * 128;                  // 128 rows of one block
 constexpr int kPairStageBytes = 2 * kTileBytes;
@@ -117,16 +127,18 @@ constexpr int kPairFewRegs = 56, kPairManyRegs = 224;
 static_assert(128 * kPairFewRegs + 256 * kPairManyRegs <= kPairThreads * 168, "register split");
 constexpr int kBoxBytes = 32 * 128;                    // a warp's 32 rows x 128 bytes of output
 constexpr int kPairOffBox = kPairStages * kPairStageBytes;
-constexpr int kPairOffBars = kPairOffBox + kPairTotalWarps * kBoxBytes;
+// The tokens' scales, [block][token] for 16 blocks at a time, two chunks: read
+// along the rows they are stored in (a thread reading its own token's scales
+// touched a line a lane, and the eight warps' 256 lines a block took longer
+// than half of its MMAs). The pitch of 130 keeps both the transposed stores
+// (16 blocks x 2 tokens a warp) and the reads free of bank conflicts.
+constexpr int kScaleChunk = 16;
+constexpr int kScalePitch = 130;
+constexpr int kScaleBytes = kScaleChunk * kScalePitch * 4;
+constexpr int kPairOffScale = kPairOffBox + kPairTotalWarps * kBoxBytes;
+constexpr int kPairOffBars = kPairOffScale + 2 * kScaleBytes;
 constexpr int kPairSmem = kPairOffBars + 256 + 1024;   // + alignment slack
 static_assert(kPairSmem <= 227 * 1024, "shared memory");
-
-// Where a thread reads the scales of its token and column half: ahead of
-// their use (a load takes longer than a block's MMAs), running on across tiles.
-struct ScaleCursor {
-  const float *as, *ws;    // next block's scales (as null outside the output)
-  int left, u;             // blocks left in the tile; tile
-};
 
 template <bool kDx>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -140,8 +152,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   auto empty_bar = [&](int s) { return bars + 8u * (kPairStages + s); };
   auto sum_bar = [&](int b) { return bars + 8u * (2 * kPairStages + b); };       // buffer's sums done
   auto read_bar = [&](int b) { return bars + 8u * (2 * kPairStages + 2 + b); };  // and read back
-  const uint32_t drain_bar = bars + 8u * (2 * kPairStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBars + 8 * (2 * kPairStages + 5));
+  auto sfull_bar = [&](int b) { return bars + 8u * (2 * kPairStages + 4 + b); };   // scale chunk
+  auto sempty_bar = [&](int b) { return bars + 8u * (2 * kPairStages + 6 + b); };
+  const uint32_t drain_bar = bars + 8u * (2 * kPairStages + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBars + 8 * (2 * kPairStages + 9));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -157,6 +171,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(sum_bar(b), 1);
       tc::mbar_init(read_bar(b), 2 * kPairTotalWarps);
+      tc::mbar_init(sfull_bar(b), 2);
+      tc::mbar_init(sempty_bar(b), kPairTotalWarps);
     }
     tc::mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -178,6 +194,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer), "r"(1u) : "memory");
   };
   auto tile_m = [&](int u) { return static_cast<int64_t>(u % p.m_units) * 256 + rank * 128; };
+  const int64_t col_blocks = (p.cols + 127) / 128;
   auto tile_c = [&](int u) { return static_cast<int64_t>(u / p.m_units) * kPairBN; };
 
   if (warp < 4) {
@@ -253,9 +270,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       for (int u = cid; u < p.units && !stop; u += ncl) {
         for (int i = 0; i < p.rb; ++i, ++g) {
           const int b = g & 1;
-          int r = tc::mbar_spin_abortable<true>(read_bar(b), ((g >> 1) & 1) ^ 1, abort_flag, 1ll << 31);
+          // the operands first: the buffer is the one that is waited for
+          int r = tc::mbar_spin_abortable<true>(full_bar(slot), ph, abort_flag, p.mma_wait_limit);
           if (r == tc::kWaitDone)
-            r = tc::mbar_spin_abortable<true>(full_bar(slot), ph, abort_flag, p.mma_wait_limit);
+            r = tc::mbar_spin_abortable<true>(read_bar(b), ((g >> 1) & 1) ^ 1, abort_flag, 1ll << 31);
           r = __shfl_sync(0xffffffffu, r, 0);
           if (r != tc::kWaitDone) {
             if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
@@ -283,6 +301,42 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       __syncwarp();
       if (lane == 0 && !tc::mbar_wait(drain_bar, 0)) fail(kRoleMma);
     }
+   } else {
+    // lane: block j of two tokens a step, one token a half-warp
+    const int j = lane & 15, t0 = 2 * (warp - 2) + (lane >> 4);
+    int ch = 0;
+    bool stop = false;
+    for (int u = cid; u < p.units && !stop; u += ncl) {
+      const int64_t m0 = tile_m(u);
+      for (int i = 0; i < p.rb; i += kScaleChunk, ++ch) {
+        int r = tc::mbar_wait_abortable(sempty_bar(ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag);
+        r = __shfl_sync(0xffffffffu, r, 0);
+        if (r != tc::kWaitDone) {
+          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleProducer);
+          stop = true;
+          break;
+        }
+        float* dst = reinterpret_cast<float*>(smem + kPairOffScale + (ch & 1) * kScaleBytes) + j * kScalePitch;
+        const float* src = p.a_scale + m0 * p.rb + i + j;
+        const bool in = i + j < p.rb;
+#pragma unroll
+        for (int h = 0; h < 32; h += 8) {
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int t = t0 + 4 * (h + k);
+            v[k] = in && m0 + t < p.M ? __ldg(src + static_cast<int64_t>(t) * p.rb) : 0.0f;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[t0 + 4 * (h + k)] = v[k];
+        }
+        const int64_t cb = tile_c(u) / 128 + (lane >> 4);
+        if (warp == 2)
+          dst[128 + (lane >> 4)] = in && cb < col_blocks ? __ldg(p.w_scale + cb * p.ws_col + (i + j) * p.ws_red) : 0.0f;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sfull_bar(ch & 1));
+      }
+    }
    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairManyRegs));
@@ -291,75 +345,71 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     uint8_t* box = smem + kPairOffBox + (warp - 4) * kBoxBytes;
     const uint32_t box_addr = tc::smem_addr(box);
     const int row = 32 * q + lane;       // token of this thread within the CTA's 128
-    const int64_t col_blocks = (p.cols + 127) / 128;
+    const float* scales = reinterpret_cast<const float*>(smem + kPairOffScale);
 
-    ScaleCursor cur;
-    auto aim = [&](int u) {              // the cursor at tile u's first block
-      cur.u = u;
-      cur.left = p.rb;
-      const int64_t m = tile_m(u) + row, cb = tile_c(u) / 128 + half;
-      const bool in = u < p.units && m < p.M && cb < col_blocks;
-      cur.as = in ? p.a_scale + m * p.rb : nullptr;
-      cur.ws = p.w_scale + cb * p.ws_col;
-    };
-    // four blocks' scales in use and the next four on their way: a value is
-    // not touched until the chunk after the one that loads it
-    float now[4], sa[4], sw[4];
-    auto fetch = [&] {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sa[j] = sw[j] = 0.0f;
-        if (j < cur.left && cur.as) {
-          sa[j] = __ldg(cur.as + j);
-          sw[j] = __ldg(cur.ws + j * p.ws_red);
+    int ch = 0, in = 0, left = p.rb;     // the next scale: chunk, block within it; blocks left in its tile
+    int ahead = ((p.units - cid + ncl - 1) / ncl) * p.rb;   // scales not yet read
+    float s_next = 0.0f;
+    // the next block's factor, read a block ahead of its use
+    auto next_scale = [&] {
+      if (ahead-- <= 0) return true;
+      if (in == 0 && !__all_sync(0xffffffffu, tc::mbar_try_wait(sfull_bar(ch & 1), (ch >> 1) & 1))) {
+        const int r = __shfl_sync(
+            0xffffffffu, tc::mbar_wait_abortable(sfull_bar(ch & 1), (ch >> 1) & 1, abort_flag), 0);
+        if (r != tc::kWaitDone) {
+          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleCompute);
+          return false;
         }
       }
-      cur.left -= 4;
-      if (cur.left <= 0) {
-        aim(cur.u + ncl);
-      } else {
-        if (cur.as) cur.as += 4;
-        cur.ws += 4 * p.ws_red;
+      const float* sp = scales + (ch & 1) * (kScaleBytes / 4) + in * kScalePitch;
+      s_next = sp[row] * sp[128 + half];
+      --left;
+      if (++in == kScaleChunk || left == 0) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sempty_bar(ch & 1));
+        ++ch;
+        in = 0;
+        if (left == 0) left = p.rb;
       }
+      return true;
     };
-    aim(cid);
-    fetch();
 
-    int g = 0;
-    bool stop = false;
+    const uint32_t read_remote = tc::mapa(read_bar(0), 0);
+    uint32_t b = 0, sum_ph = 0;
+    bool stop = !next_scale();
     for (int u = cid; u < p.units && !stop; u += ncl) {
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-      for (int i = 0; i < p.rb; ++i, ++g) {
-        if ((i & 3) == 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) now[j] = sa[j] * sw[j];
-          fetch();
-        }
-        const float s = now[0];
-        now[0] = now[1];
-        now[1] = now[2];
-        now[2] = now[3];
-        const int b = g & 1;
-        int r = tc::mbar_wait_abortable(sum_bar(b), (g >> 1) & 1, abort_flag);
-        r = __shfl_sync(0xffffffffu, r, 0);
-        if (r != tc::kWaitDone) {
-          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleCompute);
-          stop = true;
-          break;
+      for (int i = 0; i < p.rb; ++i) {
+        const float s = s_next;
+        if (!__all_sync(0xffffffffu, tc::mbar_try_wait(sum_bar(b), sum_ph))) {
+          const int r = __shfl_sync(0xffffffffu, tc::mbar_wait_abortable(sum_bar(b), sum_ph, abort_flag), 0);
+          if (r != tc::kWaitDone) {
+            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleCompute);
+            stop = true;
+            break;
+          }
         }
         tc::fence_after_sync();
+        // the next 32 columns are on their way while the last are added
+        float v[2][32];
+        tmem_ld32(src + 256u * b, v[0]);
+        tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(src + 256u * b + 32u * c, v);
+        for (int c = 0; c < 3; ++c) {
+          tmem_ld32(src + 256u * b + 32u * (c + 1), v[(c + 1) & 1]);
+          scale_add<32>(acc + 32 * c, v[c & 1], s);
           tc::tmem_wait_ld();
-          if (c == 3) {                  // the buffer is free once the last read is done
-            tc::fence_before_sync();
-            if (lane == 0) tc::mbar_arrive_remote(tc::mapa(read_bar(b), 0));
-          }
-          scale_add<32>(acc + 32 * c, v, s);
+        }
+        tc::fence_before_sync();         // all read: the buffer is free
+        if (lane == 0) arrive_relaxed(read_remote + 8u * b);
+        scale_add<32>(acc + 96, v[1], s);
+        b ^= 1u;
+        sum_ph ^= b ^ 1u;
+        if (!next_scale()) {
+          stop = true;
+          break;
         }
       }
       if (stop) break;
