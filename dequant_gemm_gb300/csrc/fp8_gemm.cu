@@ -63,6 +63,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "memory");
 }
 
+// Shared-memory accesses by 32-bit address (through the realigned base pointer
+// the compiler would emit generic ones).
+__device__ __forceinline__ float lds(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 // Arrive on an mbarrier of the cluster without ordering this thread's memory
 // accesses: what it hands over is tensor memory whose reads have completed
 // (tcgen05.wait::ld). The releasing form cost the reading warps 350 cycles a
@@ -72,16 +87,22 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
                : "memory");
 }
 
-// acc += s * v, two at a time.
+// acc += s * v, two at a time. Volatile, so that the additions stay where they
+// are written, between the issue of one tensor-memory load and the wait for
+// it: the compiler otherwise gathers them behind the last wait.
 template <int kN>
 __device__ __forceinline__ void scale_add(float* acc, const float (&v)[kN], float s) {
-  const float2 s2 = make_float2(s, s);
 #pragma unroll
-  for (int j = 0; j < kN; j += 2) {
-    const float2 r = __ffma2_rn(make_float2(v[j], v[j + 1]), s2, make_float2(acc[j], acc[j + 1]));
-    acc[j] = r.x;
-    acc[j + 1] = r.y;
-  }
+  for (int j = 0; j < kN; j += 2)
+    asm volatile(
+        "{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %4};\n\t"
+        "mov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(acc[j]), "+f"(acc[j + 1])
+        : "f"(v[j]), "f"(v[j + 1]), "f"(s));
 }
 
 struct MatmulArgs {
@@ -307,7 +328,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     int ch = 0;
     bool stop = false;
     for (int u = cid; u < p.units && !stop; u += ncl) {
-      const int64_t m0 = tile_m(u);
+      const int64_t m0 = tile_m(u), cb = tile_c(u) / 128 + (lane >> 4);
+      const int tokens = static_cast<int>(min(p.M - m0, static_cast<int64_t>(128)));
+      const float* src = p.a_scale + (m0 + t0) * p.rb + j;
+      const float* wsrc = warp == 2 && cb < col_blocks ? p.w_scale + cb * p.ws_col + j * p.ws_red : nullptr;
       for (int i = 0; i < p.rb; i += kScaleChunk, ++ch) {
         int r = tc::mbar_wait_abortable(sempty_bar(ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag);
         r = __shfl_sync(0xffffffffu, r, 0);
@@ -316,23 +340,19 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           stop = true;
           break;
         }
-        float* dst = reinterpret_cast<float*>(smem + kPairOffScale + (ch & 1) * kScaleBytes) + j * kScalePitch;
-        const float* src = p.a_scale + m0 * p.rb + i + j;
-        const bool in = i + j < p.rb;
-#pragma unroll
-        for (int h = 0; h < 32; h += 8) {
+        const uint32_t dst = base + kPairOffScale + (ch & 1) * kScaleBytes + j * kScalePitch * 4;
+        const int n = i + j < p.rb ? tokens : 0;       // tokens to read in this lane's block
+        const float* at = src + i;
+#pragma unroll 1
+        for (int h = 0; h < 128; h += 32, at += 32ll * p.rb) {
           float v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int t = t0 + 4 * (h + k);
-            v[k] = in && m0 + t < p.M ? __ldg(src + static_cast<int64_t>(t) * p.rb) : 0.0f;
-          }
+          for (int k = 0; k < 8; ++k)
+            v[k] = t0 + h + 4 * k < n ? __ldg(at + 4ll * k * p.rb) : 0.0f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[t0 + 4 * (h + k)] = v[k];
+          for (int k = 0; k < 8; ++k) sts(dst + 4 * (t0 + h + 4 * k), v[k]);
         }
-        const int64_t cb = tile_c(u) / 128 + (lane >> 4);
-        if (warp == 2)
-          dst[128 + (lane >> 4)] = in && cb < col_blocks ? __ldg(p.w_scale + cb * p.ws_col + (i + j) * p.ws_red) : 0.0f;
+        if (warp == 2) sts(dst + 4 * (128 + (lane >> 4)), n > 0 && wsrc ? __ldg(wsrc + i * p.ws_red) : 0.0f);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(sfull_bar(ch & 1));
       }
@@ -342,10 +362,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairManyRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128u * half;
-    uint8_t* box = smem + kPairOffBox + (warp - 4) * kBoxBytes;
-    const uint32_t box_addr = tc::smem_addr(box);
+    const uint32_t box_addr = base + kPairOffBox + (warp - 4) * kBoxBytes;
     const int row = 32 * q + lane;       // token of this thread within the CTA's 128
-    const float* scales = reinterpret_cast<const float*>(smem + kPairOffScale);
+    const uint32_t scales = base + kPairOffScale;
 
     int ch = 0, in = 0, left = p.rb;     // the next scale: chunk, block within it; blocks left in its tile
     int ahead = ((p.units - cid + ncl - 1) / ncl) * p.rb;   // scales not yet read
@@ -361,8 +380,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           return false;
         }
       }
-      const float* sp = scales + (ch & 1) * (kScaleBytes / 4) + in * kScalePitch;
-      s_next = sp[row] * sp[128 + half];
+      const uint32_t sp = scales + (ch & 1) * kScaleBytes + in * (kScalePitch * 4);
+      s_next = lds(sp + 4 * row) * lds(sp + 4 * (128 + half));
       --left;
       if (++in == kScaleChunk || left == 0) {
         __syncwarp();
@@ -441,7 +460,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         if (lane == 0) tc::bulk_wait_read_all();
         __syncwarp();
       };
-      uint4* rowp = reinterpret_cast<uint4*>(box + 128 * lane);
+      const uint32_t rowp = box_addr + 128 * lane;
       if (p.out_bf16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -449,8 +468,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float* a = acc + 64 * h + 8 * j;
-            rowp[j ^ (lane & 7)] = make_uint4(pack2<kElemBf16>(a[0], a[1]), pack2<kElemBf16>(a[2], a[3]),
-                                              pack2<kElemBf16>(a[4], a[5]), pack2<kElemBf16>(a[6], a[7]));
+            sts128(rowp + 16 * (j ^ (lane & 7)), pack2<kElemBf16>(a[0], a[1]), pack2<kElemBf16>(a[2], a[3]),
+                   pack2<kElemBf16>(a[4], a[5]), pack2<kElemBf16>(a[6], a[7]));
           }
           send(c0 + 64 * h);
         }
@@ -461,7 +480,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float* a = acc + 32 * h + 4 * j;
-            *reinterpret_cast<float4*>(&rowp[j ^ (lane & 7)]) = make_float4(a[0], a[1], a[2], a[3]);
+            sts128(rowp + 16 * (j ^ (lane & 7)), __float_as_uint(a[0]), __float_as_uint(a[1]),
+                   __float_as_uint(a[2]), __float_as_uint(a[3]));
           }
           send(c0 + 32 * h);
         }
