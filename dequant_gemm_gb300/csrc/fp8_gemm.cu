@@ -48,19 +48,12 @@ __host__ __device__ constexpr uint32_t idesc_f8_f32(uint32_t m, uint32_t n, bool
          ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// 32 consecutive 32-bit columns of this warp's lane quarter (no wait).
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
-        "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
-        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr)
-      : "memory");
+// 16 consecutive 32-bit columns of this warp's lane quarter (no wait).
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  tc::tmem_ld16(taddr, r);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
 }
 
 // Shared-memory accesses by 32-bit address (through the realigned base pointer
@@ -366,42 +359,28 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     const int row = 32 * q + lane;       // token of this thread within the CTA's 128
     const uint32_t scales = base + kPairOffScale;
 
-    int ch = 0, in = 0, left = p.rb;     // the next scale: chunk, block within it; blocks left in its tile
-    int ahead = ((p.units - cid + ncl - 1) / ncl) * p.rb;   // scales not yet read
-    float s_next = 0.0f;
-    // the next block's factor, read a block ahead of its use
-    auto next_scale = [&] {
-      if (ahead-- <= 0) return true;
-      if (in == 0 && !__all_sync(0xffffffffu, tc::mbar_try_wait(sfull_bar(ch & 1), (ch >> 1) & 1))) {
-        const int r = __shfl_sync(
-            0xffffffffu, tc::mbar_wait_abortable(sfull_bar(ch & 1), (ch >> 1) & 1, abort_flag), 0);
-        if (r != tc::kWaitDone) {
-          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleCompute);
-          return false;
-        }
-      }
-      const uint32_t sp = scales + (ch & 1) * kScaleBytes + in * (kScalePitch * 4);
-      s_next = lds(sp + 4 * row) * lds(sp + 4 * (128 + half));
-      --left;
-      if (++in == kScaleChunk || left == 0) {
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sempty_bar(ch & 1));
-        ++ch;
-        in = 0;
-        if (left == 0) left = p.rb;
-      }
-      return true;
-    };
-
+    int ch = 0;
     const uint32_t read_remote = tc::mapa(read_bar(0), 0);
     uint32_t b = 0, sum_ph = 0;
-    bool stop = !next_scale();
+    bool stop = false;
     for (int u = cid; u < p.units && !stop; u += ncl) {
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
       for (int i = 0; i < p.rb; ++i) {
-        const float s = s_next;
+        const int in = i % kScaleChunk;
+        if (in == 0 && !__all_sync(0xffffffffu, tc::mbar_try_wait(sfull_bar(ch & 1), (ch >> 1) & 1))) {
+          const int r = __shfl_sync(
+              0xffffffffu, tc::mbar_wait_abortable(sfull_bar(ch & 1), (ch >> 1) & 1, abort_flag), 0);
+          if (r != tc::kWaitDone) {
+            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleCompute);
+            stop = true;
+            break;
+          }
+        }
+        // the scales arrive while the block's sums are waited for
+        const uint32_t sp = scales + (ch & 1) * kScaleBytes + in * (kScalePitch * 4);
+        const float sa = lds(sp + 4 * row), sw = lds(sp + 4 * (128 + half));
         if (!__all_sync(0xffffffffu, tc::mbar_try_wait(sum_bar(b), sum_ph))) {
           const int r = __shfl_sync(0xffffffffu, tc::mbar_wait_abortable(sum_bar(b), sum_ph, abort_flag), 0);
           if (r != tc::kWaitDone) {
@@ -411,25 +390,26 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
         tc::fence_after_sync();
-        // the next 32 columns are on their way while the last are added
-        float v[2][32];
-        tmem_ld32(src + 256u * b, v[0]);
+        // the next 16 columns are on their way while the last are added
+        float v[2][16];
+        tmem_ld16f(src + 256u * b, v[0]);
+        const float s = sa * sw;
+        if (in == kScaleChunk - 1 || i + 1 == p.rb) {
+          if (lane == 0) tc::mbar_arrive(sempty_bar(ch & 1));
+          ++ch;
+        }
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          tmem_ld32(src + 256u * b + 32u * (c + 1), v[(c + 1) & 1]);
-          scale_add<32>(acc + 32 * c, v[c & 1], s);
+        for (int c = 0; c < 7; ++c) {
+          tmem_ld16f(src + 256u * b + 16u * (c + 1), v[(c + 1) & 1]);
+          scale_add<16>(acc + 16 * c, v[c & 1], s);
           tc::tmem_wait_ld();
         }
         tc::fence_before_sync();         // all read: the buffer is free
         if (lane == 0) arrive_relaxed(read_remote + 8u * b);
-        scale_add<32>(acc + 96, v[1], s);
+        scale_add<16>(acc + 112, v[1], s);
         b ^= 1u;
         sum_ph ^= b ^ 1u;
-        if (!next_scale()) {
-          stop = true;
-          break;
-        }
       }
       if (stop) break;
       // out: 128 columns of 32 tokens a warp, in boxes of 128 bytes a row whose
