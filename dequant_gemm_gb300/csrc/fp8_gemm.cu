@@ -63,6 +63,14 @@ __device__ __forceinline__ float lds(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 lds128(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts(uint32_t a, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
@@ -78,6 +86,15 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
+}
+
+// The two halves of a cluster barrier that orders nothing: a CTA's shared
+// memory may be written by the others once it has started.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // acc += s * v, two at a time. Volatile, so that the additions stay where they
@@ -106,7 +123,6 @@ struct MatmulArgs {
   int64_t ws_col, ws_red;  // strides of w_scale along column and reduction blocks
   int m_units, units;      // token tiles; all tiles
   int out_bf16, accumulate;
-  int dx;
   long long mma_wait_limit;
   int* status;
 };
@@ -395,6 +411,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         tmem_ld16f(src + 256u * b, v[0]);
         const float s = sa * sw;
         if (in == kScaleChunk - 1 || i + 1 == p.rb) {
+          __syncwarp();
           if (lane == 0) tc::mbar_arrive(sempty_bar(ch & 1));
           ++ch;
         }
@@ -479,92 +496,338 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   }
 }
 
-// ----------------------------------------------------------- simple kernel --
-struct SimpleArgs {
-  const uint8_t *a, *w;
-  const float *a_scale, *w_scale;
-  int64_t M, red, cols;    // out [M, cols]
-  int64_t w_pitch;         // K
-  int rb, kb;              // blocks along the reduction and along K
-  void* out;
-  int out_bf16, accumulate;
+// ------------------------------------------------------------ rows kernel --
+// Few tokens: the weight is what has to be read. Its 128 output columns are
+// the MMA's 128 rows (A), the tokens its kBT columns (B, 16 to 128), so that
+// the tensor core's and the reading warps' work shrinks with the tokens and a
+// stage is a 16 KB weight tile plus kBT x 128 bytes. Tiles that do not fill
+// the GPU are split along the reduction over a cluster of up to 8 CTAs, whose
+// totals meet in distributed shared memory: each CTA owns kBT / S tokens,
+// receives the others' totals of them and adds the S contributions in rank
+// order (repeatable, no workspace, no zeroing pass).
+//   warp 0 copies, warp 1 MMAs into kBufs buffers of kBT columns, warps 2-3
+//   scales (token scale times the tile's weight scale, [block][token]),
+//   warps 4.. totals: a thread holds one output column for kBT / kGroups
+//   tokens, whose factors it reads as broadcasts.
+template <int kBT>
+struct RowsCfg {
+  static constexpr int kGroups = kBT >= 64 ? 2 : 1;      // token groups, four warps each
+  static constexpr int kCols = kBT / kGroups;            // tokens a thread
+  static constexpr int kTotalWarps = 4 * kGroups;
+  static constexpr int kThreads = 32 * (4 + kTotalWarps);
+  static constexpr int kStageBytes = kTileBytes + kBT * 128;
+  // what fits beside the inbox: 8 to 10 weight tiles in flight, far above the
+  // 35 KB an SM needs to keep HBM busy
+  static constexpr int kStages = kBT == 128 ? 4 : kBT == 64 ? 7 : kBT == 32 ? 8 : 10;
+  static constexpr int kBufs = kBT == 128 ? 4 : 8;
+  static constexpr int kTmemCols = kBufs * kBT;          // 128, 256, 512, 512
+  static constexpr int kPitch = kBT + 4;                 // scale row: 16-byte aligned
+  static constexpr int kChunkBytes = kScaleChunk * kPitch * 4;
+  static constexpr int kOffInbox = kStages * kStageBytes;
+  static constexpr int kOffScale = kOffInbox + kBT * 512;
+  static constexpr int kOffBars = kOffScale + 2 * kChunkBytes;
+  static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 4 + 1;
+  static constexpr int kSmem = kOffBars + 8 * kNumBars + 16 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kTmemCols <= 512, "tensor memory");
 };
 
-// 64 x 64 outputs a CTA, 4 x 4 a thread, one 128-wide block at a time staged
-// in shared memory as fp32 in two halves of 64.
-template <bool kDx>
-__global__ void __launch_bounds__(256) fp8_matmul_simple_kernel(const SimpleArgs p) {
-  __shared__ float As[64][65], Bs[64][65];   // [reduction][token], [reduction][column]
-  const int64_t m0 = blockIdx.y * 64ll, c0 = blockIdx.x * 64ll;
-  const int tm = (threadIdx.x >> 4) * 4, tc = (threadIdx.x & 15) * 4;
-  float acc[4][4] = {};
-  for (int b = 0; b < p.rb; ++b) {
-    float t[4][4] = {};
-    for (int half = 0; half < 2; ++half) {
-      const int64_t r0 = b * 128ll + half * 64;
-      __syncthreads();
-      for (int e = threadIdx.x; e < 64 * 32; e += 256) {
-        const int i = e >> 5, r = (e & 31) * 2;
-        float2 v = make_float2(0.f, 0.f);
-        if (m0 + i < p.M && r0 + r < p.red)
-          v = e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(p.a + (m0 + i) * p.red + r0 + r));
-        As[r][i] = v.x;
-        As[r + 1][i] = v.y;
-        float2 u = make_float2(0.f, 0.f);
-        if constexpr (kDx) {   // weight row r0 + i, columns c0 + r, + 1
-          if (r0 + i < p.red && c0 + r < p.cols)
-            u = e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(p.w + (r0 + i) * p.w_pitch + c0 + r));
-          Bs[i][r] = u.x;
-          Bs[i][r + 1] = u.y;
-        } else {
-          if (c0 + i < p.cols && r0 + r < p.red)
-            u = e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(p.w + (c0 + i) * p.w_pitch + r0 + r));
-          Bs[r][i] = u.x;
-          Bs[r + 1][i] = u.y;
-        }
-      }
-      __syncthreads();
-      for (int r = 0; r < 64; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) t[i][j] += As[r][tm + i] * Bs[r][tc + j];
+template <bool kDx, int kBT>
+__global__ void __launch_bounds__(RowsCfg<kBT>::kThreads, 1)
+fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                const MatmulArgs p) {
+  using C = RowsCfg<kBT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t base = tc::smem_addr(smem), bars = base + C::kOffBars;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (C::kStages + s); };
+  auto sum_bar = [&](int b) { return bars + 8u * (2 * C::kStages + b); };
+  auto read_bar = [&](int b) { return bars + 8u * (2 * C::kStages + C::kBufs + b); };
+  auto sfull_bar = [&](int b) { return bars + 8u * (2 * C::kStages + 2 * C::kBufs + b); };
+  auto sempty_bar = [&](int b) { return bars + 8u * (2 * C::kStages + 2 * C::kBufs + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (2 * C::kStages + 2 * C::kBufs + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBars + 8 * C::kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = static_cast<int>(gridDim.x);        // the cluster
+  const int rank = static_cast<int>(blockIdx.x);
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 128, m0 = static_cast<int64_t>(blockIdx.z) * kBT;
+  const int b0 = static_cast<int>(static_cast<int64_t>(p.rb) * rank / splits);
+  const int nb = static_cast<int>(static_cast<int64_t>(p.rb) * (rank + 1) / splits) - b0;   // blocks here
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      tc::mbar_init(full_bar(i), 1);
+      tc::mbar_init(empty_bar(i), 1);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + tm + i, c = c0 + tc + j;
-        if (m < p.M && c < p.cols) {
-          const float sw = kDx ? p.w_scale[static_cast<int64_t>(b) * p.kb + c / 128]
-                               : p.w_scale[c / 128 * p.kb + b];
-          acc[i][j] += p.a_scale[m * p.rb + b] * sw * t[i][j];
-        }
-      }
+    for (int i = 0; i < C::kBufs; ++i) {
+      tc::mbar_init(sum_bar(i), 1);
+      tc::mbar_init(read_bar(i), C::kTotalWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(sfull_bar(i), 2);
+      tc::mbar_init(sempty_bar(i), C::kTotalWarps);
+    }
+    tc::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tensormap(&tm_a);
+    tc::prefetch_tensormap(&tm_w);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + tm + i, c = c0 + tc + j;
-      if (m >= p.M || c >= p.cols) continue;
-      float v = acc[i][j];
-      if (p.out_bf16) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + m * p.cols + c;
-        if (p.accumulate) v += __bfloat162float(*o);
-        *o = __float2bfloat16_rn(v);
-      } else {
-        float* o = static_cast<float*>(p.out) + m * p.cols + c;
-        if (p.accumulate) v += *o;
-        *o = v;
+  if (warp == 1) tc::tmem_alloc<1>(tc::smem_addr(tmem_slot), C::kTmemCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  cluster_arrive();
+  const uint32_t tmem = *tmem_slot;
+
+  auto fail = [&](uint32_t role) {
+    report_status(p.status, kStatusTimeout, kDx ? kSiteFp8Dx : kSiteFp8Fwd, role);
+    *abort_flag = 1;
+  };
+  auto waited = [&](uint32_t bar, uint32_t parity, uint32_t role) {   // warp-uniform
+    const int r = __shfl_sync(0xffffffffu, tc::mbar_wait_abortable(bar, parity, abort_flag), 0);
+    if (r == tc::kWaitTimeout && lane == 0) fail(role);
+    return r == tc::kWaitDone;
+  };
+
+  float acc[C::kCols];
+  if (warp == 0) {
+    int slot = 0;
+    uint32_t ph = 0;
+    int i = 0;
+    for (; i < nb; ++i) {
+      if (!waited(empty_bar(slot), ph ^ 1, kRoleProducer)) break;
+      const uint32_t dst = base + slot * C::kStageBytes;
+      const int32_t k = (b0 + i) * 128;
+      if (tc::elect_one()) {
+        tc::mbar_arrive_expect_tx(full_bar(slot), C::kStageBytes);
+        if (kDx) tc::tma_load_2d(dst, &tm_w, static_cast<int32_t>(r0), k, full_bar(slot));
+        else tc::tma_load_2d(dst, &tm_w, k, static_cast<int32_t>(r0), full_bar(slot));
+        tc::tma_load_2d(dst + kTileBytes, &tm_a, k, static_cast<int32_t>(m0), full_bar(slot));
+      }
+      __syncwarp();
+      if (++slot == C::kStages) {
+        slot = 0;
+        ph ^= 1u;
       }
     }
+    if (*abort_flag && lane == 0)   // copies in flight land before the CTA exits
+      for (int g = max(0, i - C::kStages); g < i; ++g)
+        tc::mbar_wait(full_bar(g % C::kStages), (g / C::kStages) & 1, 1ll << 24);
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f8_f32(128, kBT, kDx, false);
+    const uint64_t adesc0 = kDx ? tc::sw128_mnmajor_desc(base, 0, 1024) : tc::sw128_kmajor_desc(base);
+    const uint64_t bdesc0 = tc::sw128_kmajor_desc(base + kTileBytes);
+    constexpr uint32_t kAStep = kDx ? 32 * 128 / 16 : 2;   // 32 of the reduction
+    int slot = 0;
+    uint32_t ph = 0, buf = 0, bph = 1;
+    for (int i = 0; i < nb; ++i) {
+      int r = tc::mbar_spin_abortable<false>(full_bar(slot), ph, abort_flag, p.mma_wait_limit);
+      if (r == tc::kWaitDone) r = tc::mbar_spin_abortable<false>(read_bar(buf), bph, abort_flag, 1ll << 31);
+      r = __shfl_sync(0xffffffffu, r, 0);
+      if (r != tc::kWaitDone) {
+        if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
+        break;
+      }
+      tc::fence_after_sync();
+      const uint64_t off = static_cast<uint64_t>(slot * (C::kStageBytes >> 4));
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_f8_ss<1>(tmem + buf * kBT, adesc0 + off + kAStep * j, bdesc0 + off + 2u * j, idesc,
+                       j != 0 ? 1u : 0u);
+        tc::mma_commit<1>(sum_bar(buf));
+        tc::mma_commit<1>(empty_bar(slot));
+      }
+      __syncwarp();
+      if (++slot == C::kStages) {
+        slot = 0;
+        ph ^= 1u;
+      }
+      if (++buf == C::kBufs) {
+        buf = 0;
+        bph ^= 1u;
+      }
+    }
+    if (tc::elect_one()) tc::mma_commit<1>(drain_bar);
+    __syncwarp();
+    if (lane == 0 && !tc::mbar_wait(drain_bar, 0)) fail(kRoleMma);
+  } else if (warp < 4) {
+    // lane: block j of two tokens a step, one token a half-warp
+    const int j = lane & 15, t0 = 2 * (warp - 2) + (lane >> 4);
+    const int tokens = static_cast<int>(min(p.M - m0, static_cast<int64_t>(kBT)));
+    const float* as = p.a_scale + (m0 + t0) * p.rb + b0 + j;
+    const float* ws = p.w_scale + (r0 / 128) * p.ws_col + (b0 + j) * p.ws_red;
+    for (int i = 0, ch = 0; i < nb; i += kScaleChunk, ++ch) {
+      if (!waited(sempty_bar(ch & 1), ((ch >> 1) & 1) ^ 1, kRoleProducer)) break;
+      const uint32_t dst = base + C::kOffScale + (ch & 1) * C::kChunkBytes + j * (C::kPitch * 4);
+      const int n = i + j < nb ? tokens : 0;
+      const float w = n > 0 ? __ldg(ws + i * p.ws_red) : 0.0f;
+      constexpr int kStep = kBT < 32 ? kBT / 4 : 8;
+#pragma unroll 1
+      for (int h = 0; h < kBT; h += 4 * kStep) {
+        float v[kStep];
+#pragma unroll
+        for (int k = 0; k < kStep; ++k)
+          v[k] = t0 + h + 4 * k < n ? __ldg(as + i + (h + 4ll * k) * p.rb) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) sts(dst + 4 * (t0 + h + 4 * k), v[k] * w);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(sfull_bar(ch & 1));
+    }
+  } else {
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kCols * part;
+    const uint32_t scales = base + C::kOffScale + 4 * C::kCols * part;
+    // read back into this CTA's own barrier, by its cluster address (the
+    // relaxed arrival costs half of the local releasing one)
+    const uint32_t read_remote = tc::mapa(read_bar(0), tc::cluster_ctarank());
+#pragma unroll
+    for (int j = 0; j < C::kCols; ++j) acc[j] = 0.0f;
+    uint32_t buf = 0, ph = 0;
+    for (int i = 0; i < nb; ++i) {
+      const int in = i % kScaleChunk, ch = i / kScaleChunk;
+      if (in == 0 && !waited(sfull_bar(ch & 1), (ch >> 1) & 1, kRoleCompute)) break;
+      if (!waited(sum_bar(buf), ph, kRoleCompute)) break;
+      tc::fence_after_sync();
+      const uint32_t sp = scales + (ch & 1) * C::kChunkBytes + in * (C::kPitch * 4);
+#pragma unroll
+      for (int c = 0; c < C::kCols; c += 16) {
+        float v[16];
+        tmem_ld16f(src + kBT * buf + c, v);
+        float4 f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] = lds128(sp + 4 * c + 16 * k);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[c + 4 * k] = fmaf(v[4 * k], f[k].x, acc[c + 4 * k]);
+          acc[c + 4 * k + 1] = fmaf(v[4 * k + 1], f[k].y, acc[c + 4 * k + 1]);
+          acc[c + 4 * k + 2] = fmaf(v[4 * k + 2], f[k].z, acc[c + 4 * k + 2]);
+          acc[c + 4 * k + 3] = fmaf(v[4 * k + 3], f[k].w, acc[c + 4 * k + 3]);
+        }
+      }
+      tc::fence_before_sync();
+      if (lane == 0) arrive_relaxed(read_remote + 8u * buf);
+      if (in == kScaleChunk - 1 || i + 1 == nb) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sempty_bar(ch & 1));
+      }
+      if (++buf == C::kBufs) {
+        buf = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+
+  // totals to the CTAs that own the tokens: inbox[source][token][column]
+  cluster_wait();                                  // every CTA of the cluster runs
+  const int own_log = 31 - __clz(kBT / splits), own = 1 << own_log;   // tokens a CTA owns
+  if (warp >= 4) {
+    const int part = (warp - 4) >> 2, col = 32 * (warp & 3) + lane;
+#pragma unroll
+    for (int j = 0; j < C::kCols; ++j) {
+      const int t = C::kCols * part + j;
+      const uint32_t at = base + C::kOffInbox + 4u * ((rank * own + (t & (own - 1))) * 128 + col);
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, t >> own_log)), "f"(acc[j])
+                   : "memory");
+    }
+  }
+  tc::fence_before_sync();
+  tc::cluster_sync();                              // every total has arrived
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc<1>(tmem, C::kTmemCols);
+  }
+  // own tokens x 128 columns, four columns a thread
+  for (int e = threadIdx.x; e < own * 32; e += C::kThreads) {
+    const int t = e >> 5, c = (e & 31) * 4;
+    const int64_t m = m0 + static_cast<int64_t>(rank) * own + t;
+    if (m >= p.M || r0 + c >= p.cols) continue;
+    const uint32_t at = base + C::kOffInbox + 4u * (t * 128 + c);
+    float4 y = lds128(at);
+    for (int k = 1; k < splits; ++k) {
+      const float4 z = lds128(at + 512u * own * k);
+      y.x += z.x;
+      y.y += z.y;
+      y.z += z.z;
+      y.w += z.w;
+    }
+    const int64_t o = m * p.cols + r0 + c;
+    if (p.out_bf16) {
+      uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o);
+      if (p.accumulate) {
+        const uint2 u = *out;
+        const float2 a = unpack2<kElemBf16>(u.x), b = unpack2<kElemBf16>(u.y);
+        y.x += a.x;
+        y.y += a.y;
+        y.z += b.x;
+        y.w += b.y;
+      }
+      *out = make_uint2(pack2<kElemBf16>(y.x, y.y), pack2<kElemBf16>(y.z, y.w));
+    } else {
+      float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
+      if (p.accumulate) {
+        const float4 a = *out;
+        y.x += a.x;
+        y.y += a.y;
+        y.z += a.z;
+        y.w += a.w;
+      }
+      *out = y;
+    }
+  }
 }
 
+template <bool kDx, int kBT>
+cudaError_t launch_rows(const Fp8Call& c, const MatmulArgs& a, int64_t red) {
+  using C = RowsCfg<kBT>;
+  const int64_t row_tiles = (a.cols + 127) / 128, m_tiles = (c.M + kBT - 1) / kBT;
+  // splits: the shortest makespan in blocks, a CTA's fixed cost (start, last
+  // block, reduction) counted as 8
+  int splits = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= 8 && s <= a.rb; s *= 2) {
+    const int64_t rounds = (row_tiles * m_tiles * s + c.num_sms - 1) / c.num_sms;
+    const int64_t cost = rounds * ((a.rb + s - 1) / s + 8);
+    if (cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  CUtensorMap tm_a, tm_w;
+  const uint64_t ur = static_cast<uint64_t>(red), um = static_cast<uint64_t>(c.M);
+  if (!encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.a, ur, um, ur, 128, kBT,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w, static_cast<uint64_t>(c.K),
+                 static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.K), 128, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  static std::once_flag once[kOnceDevices];
+  once_per_device(once, c.device, [] {
+    cudaFuncSetAttribute(fp8_rows_kernel<kDx, kBT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(row_tiles),
+                     static_cast<unsigned>(m_tiles));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = c.st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp8_rows_kernel<kDx, kBT>, tm_a, tm_w, a);
+}
 
-}  // namespace
-
-namespace {
 template <bool kDx>
 cudaError_t launch_pair(const Fp8Call& c, const MatmulArgs& args, int64_t red) {
   MatmulArgs a = args;
@@ -603,46 +866,31 @@ cudaError_t launch_pair(const Fp8Call& c, const MatmulArgs& args, int64_t red) {
   return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<kDx>, tm_a, tm_w, tm_out, a);
 }
 
-}  // namespace
-
-cudaError_t launch_fp8_matmul(const Fp8Call& c) {
-  const int64_t red = c.dx ? c.N : c.K, cols = c.dx ? c.K : c.N;
-  const int64_t kb = (c.K + 127) / 128;
-  if (c.M > 128) {
-    MatmulArgs a = {};
-    a.a_scale = c.a_scale;
-    a.w_scale = c.w_scale;
-    a.out = c.out;
-    a.M = c.M;
-    a.cols = cols;
-    a.rb = static_cast<int>((red + 127) / 128);
-    a.ws_col = c.dx ? 1 : kb;
-    a.ws_red = c.dx ? kb : 1;
-    a.out_bf16 = c.out_bf16;
-    a.accumulate = c.accumulate;
-    a.dx = c.dx;
-    a.mma_wait_limit = c.wait_limit;
-    a.status = c.status;
-    return c.dx ? launch_pair<true>(c, a, red) : launch_pair<false>(c, a, red);
-  }
-  SimpleArgs a;
-  a.a = c.a;
-  a.w = c.w;
+template <bool kDx>
+cudaError_t launch_any(const Fp8Call& c) {
+  const int64_t red = kDx ? c.N : c.K, kb = (c.K + 127) / 128;
+  MatmulArgs a = {};
   a.a_scale = c.a_scale;
   a.w_scale = c.w_scale;
-  a.M = c.M;
-  a.red = red;
-  a.cols = cols;
-  a.w_pitch = c.K;
-  a.rb = static_cast<int>((a.red + 127) / 128);
-  a.kb = static_cast<int>(kb);
   a.out = c.out;
+  a.M = c.M;
+  a.cols = kDx ? c.K : c.N;
+  a.rb = static_cast<int>((red + 127) / 128);
+  a.ws_col = kDx ? 1 : kb;
+  a.ws_red = kDx ? kb : 1;
   a.out_bf16 = c.out_bf16;
   a.accumulate = c.accumulate;
-  const dim3 grid(static_cast<unsigned>((a.cols + 63) / 64), static_cast<unsigned>((a.M + 63) / 64));
-  if (c.dx) fp8_matmul_simple_kernel<true><<<grid, 256, 0, c.st>>>(a);
-  else fp8_matmul_simple_kernel<false><<<grid, 256, 0, c.st>>>(a);
-  return cudaGetLastError();
+  a.mma_wait_limit = c.wait_limit;
+  a.status = c.status;
+  if (c.M <= 16) return launch_rows<kDx, 16>(c, a, red);
+  if (c.M <= 32) return launch_rows<kDx, 32>(c, a, red);
+  if (c.M <= 64) return launch_rows<kDx, 64>(c, a, red);
+  if (c.M <= 128) return launch_rows<kDx, 128>(c, a, red);
+  return launch_pair<kDx>(c, a, red);
 }
+
+}  // namespace
+
+cudaError_t launch_fp8_matmul(const Fp8Call& c) { return c.dx ? launch_any<true>(c) : launch_any<false>(c); }
 
 }  // namespace nf4
