@@ -24,12 +24,15 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kFp8MinAmax = 6.018531076210112e-36f;   // 2^-117
 
 // Scale of a block from its largest magnitude, and the factor its values are
-// multiplied by.
+// multiplied by (a NaN or an infinity passes through). The division by 448
+// is div_by_const's, checked against the exact quotient for every significand
+// (results are normal, so the exponent does not matter).
 __device__ __forceinline__ float fp8_scale(float amax) {
-  return amax < kFp8MinAmax ? 0.0f : __fdiv_rn(amax, kE4m3Max);
+  const float s = div_by_const<448>(amax);
+  return amax < kFp8MinAmax ? 0.0f : amax <= 3.402823466e38f ? s : amax;
 }
 __device__ __forceinline__ float fp8_inverse(float scale) {
-  return scale == 0.0f ? 0.0f : __fdiv_rn(1.0f, scale);
+  return scale == 0.0f ? 0.0f : __frcp_rn(scale);
 }
 
 // max that returns NaN if either operand is NaN (fmaxf drops it).

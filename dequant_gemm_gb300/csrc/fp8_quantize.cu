@@ -16,9 +16,11 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 4;
 
-template <int kElem>
+// kWhole: rows of whole blocks, which then lie one after another and need no
+// row index (the 64-bit division by kb took longer than the block's bytes).
+template <int kElem, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads)
-fp8_quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols, int kb,
+fp8_quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols, uint32_t kb,
                          uint8_t* __restrict__ codes, float* __restrict__ scale) {
   const int sub = threadIdx.x & 15;
   const int64_t groups = rows * kb;
@@ -27,9 +29,14 @@ fp8_quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols,
   int64_t at[kRowUnroll];
 #pragma unroll
   for (int u = 0; u < kRowUnroll; ++u) {
-    const int64_t g = g0 + u, r = g / kb;
-    const int64_t c = (g - r * kb) * kFp8Block + 8 * sub;
-    at[u] = g < groups && c < cols ? r * cols + c : -1;
+    const int64_t g = g0 + u;
+    if (kWhole) {
+      at[u] = g < groups ? g * kFp8Block + 8 * sub : -1;
+    } else {
+      const int64_t r = groups <= UINT32_MAX ? static_cast<uint32_t>(g) / kb : g / kb;
+      const int64_t c = (g - r * kb) * kFp8Block + 8 * sub;
+      at[u] = g < groups && c < cols ? r * cols + c : -1;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
     if (at[u] >= 0) load8<kElem>(x, at[u], v[u]);
@@ -124,9 +131,13 @@ cudaError_t launch_fp8_quantize(const void* x, int x_elem, int64_t rows, int64_t
     constexpr int kElem = decltype(elem)::value;
     if (block_rows == 1) {
       const int64_t per_cta = kRowThreads / 16 * kRowUnroll;
-      fp8_quantize_rows_kernel<kElem>
-          <<<static_cast<unsigned>((rows * kb + per_cta - 1) / per_cta), kRowThreads, 0, st>>>(
-              x, rows, cols, static_cast<int>(kb), codes, scale);
+      const unsigned grid = static_cast<unsigned>((rows * kb + per_cta - 1) / per_cta);
+      if (cols % kFp8Block == 0)
+        fp8_quantize_rows_kernel<kElem, true>
+            <<<grid, kRowThreads, 0, st>>>(x, rows, cols, static_cast<uint32_t>(kb), codes, scale);
+      else
+        fp8_quantize_rows_kernel<kElem, false>
+            <<<grid, kRowThreads, 0, st>>>(x, rows, cols, static_cast<uint32_t>(kb), codes, scale);
     } else {
       const int64_t rb = (rows + kFp8Block - 1) / kFp8Block;
       fp8_quantize_tiles_kernel<kElem><<<static_cast<unsigned>(rb * kb), kTileThreads, 0, st>>>(

@@ -117,6 +117,68 @@ __device__ __forceinline__ void write_y(const FwdArgs& p, int64_t row, int64_t c
   if (in) store_any<kVec>(p.y, p.y_elem, i, y);
 }
 
+// One CTA a row, held in registers between the sum and the output: x and the
+// residual are read once, h and y written once. A thread holds kNC runs of
+// kVec elements, blockDim.x runs apart (8 elements, so that 16 lanes hold a
+// block of the 8-bit output; single elements where the row's length leaves
+// rows unaligned).
+template <int kX, int kRes, int kVec, int kNC>
+__global__ void __launch_bounds__(1024)
+rmsnorm_fwd_kernel(const FwdArgs p) {
+  __shared__ float part[32];
+  constexpr int kH = kRes == 2 ? kElemF32 : kX;    // the stream's type
+  const int64_t row = blockIdx.x, row0 = row * p.cols;
+  const int cols = static_cast<int>(p.cols), step = blockDim.x * kVec;
+  float v[kNC][kVec];
+#pragma unroll
+  for (int i = 0; i < kNC; ++i) {
+    const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[i][j] = 0.0f;
+    if (c < cols) load_any<kVec>(p.x, kX, row0 + c, v[i]);
+  }
+  if constexpr (kRes != 0) {
+    float r[kNC][kVec];
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+      const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) r[i][j] = 0.0f;
+      if (c < cols) load_any<kVec>(p.residual, kH, row0 + c, r[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kNC; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[i][j] = round_to(v[i][j] + r[i][j], kH);
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNC; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) ss += v[i][j] * v[i][j];
+  if constexpr (kRes != 0) {
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+      const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
+      if (c < cols) store_any<kVec>(p.h, kH, row0 + c, v[i]);
+    }
+  }
+  const float rstd = rsqrtf(block_sum(ss, part) / static_cast<float>(cols) + p.eps);
+  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < kNC; ++i) {
+    const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
+    const bool in = c < cols;
+    if (in) {
+      float w[kVec];
+      load_any<kVec>(p.weight, p.w_elem, c, w);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * rstd * w[j];
+    }
+    write_y<kVec>(p, row, c, in, v[i]);
+  }
+}
+
 // One CTA a row of any length, read twice: the second time h comes from where
 // the first pass wrote it (each thread reads back its own elements).
 template <int kVec>
@@ -156,7 +218,7 @@ __global__ void __launch_bounds__(512) rmsnorm_fwd_long_kernel(const FwdArgs p) 
 struct BwdArgs {
   const void *dy, *h, *dh, *weight;
   const float* rstd;
-  void* dx;
+  void *dx, *dweight;
   float* partial;
   int64_t rows, cols;
   int elem, w_elem;
@@ -203,21 +265,205 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_long_kernel(const BwdArgs p) 
   }
 }
 
-// dw = the sum of the partial rows, in their order.
-__global__ void __launch_bounds__(128)
-rmsnorm_dweight_kernel(const float* __restrict__ partial, int64_t parts, int64_t cols,
-                       void* __restrict__ dweight, int w_elem) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-  if (c >= cols) return;
-  float s = 0.0f;
-  for (int64_t i = 0; i < parts; ++i) s += partial[i * cols + c];
-  const float v[1] = {s};
-  store_any<1>(dweight, w_elem, c, v);
+// kVec elements as they lie in memory (16 or 32 bytes, or one element), so
+// that a row on its way costs no more registers than it has bytes.
+template <int kElem, int kVec>
+struct Raw {
+  static constexpr int kWords = kVec == 8 ? 2 * Elem<kElem>::kBytes : 1;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = 0u;
+  }
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (kVec == 8) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * Elem<kElem>::kBytes);
+#pragma unroll
+      for (int j = 0; j < kWords / 4; ++j) {
+        const uint4 u = q[j];
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+      }
+    } else if constexpr (kElem == kElemF32) {
+      w[0] = static_cast<const uint32_t*>(p)[i];
+    } else {
+      w[0] = static_cast<const uint16_t*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (kElem == kElemF32) return __uint_as_float(w[j]);
+    const float2 f = unpack2<kElem>(w[j >> 1]);
+    return (j & 1) ? f.y : f.x;
+  }
+};
+
+// Rows of up to kNC runs a thread, in registers: gridDim.x CTAs take the rows
+// in turn, the next row's loads under way while this one is reduced (kAhead),
+// each thread's share of dw in registers until the CTA is done. One CTA alone
+// writes dw itself.
+template <int kElem, int kVec, int kNC, bool kAhead>
+__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const BwdArgs p) {
+  using R = Raw<kElem, kVec>;
+  __shared__ float part[2][32];
+  const int cols = static_cast<int>(p.cols), step = blockDim.x * kVec;
+  const int c0 = static_cast<int>(threadIdx.x) * kVec;
+  float w[kNC][kVec], acc[kNC][kVec];
+#pragma unroll
+  for (int i = 0; i < kNC; ++i) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) w[i][j] = acc[i][j] = 0.0f;
+    if (c0 + i * step < cols) load_any<kVec>(p.weight, p.w_elem, c0 + i * step, w[i]);
+  }
+  R dy[kNC], h[kNC], dh[kNC];
+  float r = 0.0f;
+  auto fetch = [&](int64_t row, R (&a)[kNC], R (&b)[kNC], R (&d)[kNC], float& rs) {
+    rs = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+      a[i].zero();
+      b[i].zero();
+      d[i].zero();
+      const int c = c0 + i * step;
+      if (c < cols) {
+        const int64_t at = row * p.cols + c;
+        a[i].load(p.dy, at);
+        b[i].load(p.h, at);
+        if (p.dh) d[i].load(p.dh, at);
+      }
+    }
+  };
+  if (kAhead) fetch(blockIdx.x, dy, h, dh, r);
+  int k = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++k) {
+    R dy2[kNC], h2[kNC], dh2[kNC];
+    float r2 = 0.0f;
+    if (!kAhead) fetch(row, dy, h, dh, r);
+    else if (row + gridDim.x < p.rows) fetch(row + gridDim.x, dy2, h2, dh2, r2);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kNC; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const float g = dy[i].at(j), xh = h[i].at(j) * r;
+        dot += g * w[i][j] * xh;
+        acc[i][j] += g * xh;
+      }
+    // alternating buffers: the previous row's sums have been read by then
+    const float mean = block_sum(dot, part[k & 1]) / static_cast<float>(cols);
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+      float d[kVec];
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        d[j] = dh[i].at(j) + r * (dy[i].at(j) * w[i][j] - h[i].at(j) * r * mean);
+      if (c0 + i * step < cols) store_any<kVec>(p.dx, kElem, row * p.cols + c0 + i * step, d);
+    }
+    if (kAhead) {
+#pragma unroll
+      for (int i = 0; i < kNC; ++i) {
+        dy[i] = dy2[i];
+        h[i] = h2[i];
+        dh[i] = dh2[i];
+      }
+      r = r2;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kNC; ++i) {
+    const int c = c0 + i * step;
+    if (c >= cols) continue;
+    if (gridDim.x == 1) store_any<kVec>(p.dweight, p.w_elem, c, acc[i]);
+    else store_any<kVec>(p.partial, kElemF32, blockIdx.x * p.cols + c, acc[i]);
+  }
 }
 
-int threads_for(int64_t cols, int vec) {
-  const int64_t chunks = (cols + vec - 1) / vec;
-  return static_cast<int>(std::min<int64_t>(512, (chunks + 31) / 32 * 32));
+// dw = the sum of the partial rows: 32 columns a CTA, eight warps that each
+// add every eighth row, and their eight sums in order.
+__global__ void __launch_bounds__(256)
+rmsnorm_dweight_kernel(const float* __restrict__ partial, int parts, int64_t cols,
+                       void* __restrict__ dweight, int w_elem) {
+  __shared__ float sums[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial rows are written
+  float s = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int i = warp; i < parts; i += 8) s += partial[i * cols + c];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+    float v[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[0] += sums[i][lane];
+    store_any<1>(dweight, w_elem, c, v);
+  }
+}
+
+// Longest rows held in registers, and threads for n runs of them a thread.
+constexpr int64_t kFwdMaxCols = 32768, kFwdMaxOdd = 16384, kBwdMaxCols = 16384,
+                  kBwdMaxF32 = 8192, kBwdMaxOdd = 8192;
+
+int threads_for(int64_t cols, int vec, int nc, int most) {
+  const int64_t runs = (cols + vec * nc - 1) / (vec * nc);
+  return static_cast<int>(std::min<int64_t>(most, (runs + 31) / 32 * 32));
+}
+
+template <int kX, int kRes>
+cudaError_t launch_fwd(const NormFwdCall& c, const FwdArgs& a) {
+  const unsigned grid = static_cast<unsigned>(c.rows);
+  if (c.cols % 8 == 0 && c.cols <= kFwdMaxCols) {
+    // four runs a thread, whose loads are in flight together, in CTAs small
+    // enough that several rows share an SM. By the row's length alone: a row's
+    // sum, and with it the row's result, does not depend on how many rows the
+    // call has.
+    const int64_t runs = c.cols / 8;
+    if (runs <= 256)
+      rmsnorm_fwd_kernel<kX, kRes, 8, 2><<<grid, threads_for(c.cols, 8, 2, 1024), 0, c.st>>>(a);
+    else
+      rmsnorm_fwd_kernel<kX, kRes, 8, 4><<<grid, threads_for(c.cols, 8, 4, 1024), 0, c.st>>>(a);
+  } else if (c.cols % 8 != 0 && c.cols <= kFwdMaxOdd) {
+    if (c.cols <= 2048)
+      rmsnorm_fwd_kernel<kX, kRes, 1, 8><<<grid, threads_for(c.cols, 1, 8, 1024), 0, c.st>>>(a);
+    else
+      rmsnorm_fwd_kernel<kX, kRes, 1, 16><<<grid, threads_for(c.cols, 1, 16, 1024), 0, c.st>>>(a);
+  } else if (c.cols % 8 == 0) {
+    rmsnorm_fwd_long_kernel<8><<<grid, threads_for(c.cols, 8, 1, 512), 0, c.st>>>(a);
+  } else {
+    rmsnorm_fwd_long_kernel<1><<<grid, threads_for(c.cols, 1, 1, 512), 0, c.st>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+int64_t bwd_max_cols(int64_t cols, int elem) {
+  return cols % 8 != 0 ? kBwdMaxOdd : elem == kElemF32 ? kBwdMaxF32 : kBwdMaxCols;
+}
+
+template <int kElem>
+cudaError_t launch_bwd(const NormBwdCall& c, const BwdArgs& a, unsigned parts) {
+  const int64_t most = bwd_max_cols(c.cols, kElem);
+  if (c.cols % 8 == 0 && c.cols <= most) {
+    if (c.cols <= 4096)
+      rmsnorm_bwd_kernel<kElem, 8, 1, true><<<parts, threads_for(c.cols, 8, 1, 512), 0, c.st>>>(a);
+    else if (c.cols <= 8192)
+      rmsnorm_bwd_kernel<kElem, 8, 2, kElem != kElemF32><<<parts, threads_for(c.cols, 8, 2, 512), 0, c.st>>>(a);
+    else if constexpr (kElem != kElemF32)
+      rmsnorm_bwd_kernel<kElem, 8, 4, false><<<parts, threads_for(c.cols, 8, 4, 512), 0, c.st>>>(a);
+  } else if (c.cols % 8 != 0 && c.cols <= most) {
+    if (c.cols <= 2048)
+      rmsnorm_bwd_kernel<kElem, 1, 8, true><<<parts, threads_for(c.cols, 1, 8, 512), 0, c.st>>>(a);
+    else
+      rmsnorm_bwd_kernel<kElem, 1, 16, false><<<parts, threads_for(c.cols, 1, 16, 512), 0, c.st>>>(a);
+  } else if (c.cols % 8 == 0) {
+    rmsnorm_bwd_long_kernel<8><<<parts, threads_for(c.cols, 8, 1, 512), 0, c.st>>>(a);
+  } else {
+    rmsnorm_bwd_long_kernel<1><<<parts, threads_for(c.cols, 1, 1, 512), 0, c.st>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -225,29 +471,42 @@ int threads_for(int64_t cols, int vec) {
 cudaError_t launch_rmsnorm_fwd(const NormFwdCall& c) {
   const FwdArgs a = {c.x, c.residual, c.weight, c.h, c.y, c.scale, c.rstd, c.cols,
                      c.x_elem, c.h_elem, c.w_elem, c.y_elem, c.y_fp8 ? 1 : 0, c.eps};
-  const unsigned grid = static_cast<unsigned>(c.rows);
-  if (c.cols % 8 == 0)
-    rmsnorm_fwd_long_kernel<8><<<grid, threads_for(c.cols, 8), 0, c.st>>>(a);
-  else
-    rmsnorm_fwd_long_kernel<1><<<grid, threads_for(c.cols, 1), 0, c.st>>>(a);
-  return cudaGetLastError();
+  const int res = !c.residual ? 0 : c.h_elem == c.x_elem ? 1 : 2;
+  auto go = [&](auto x) {
+    constexpr int kX = decltype(x)::value;
+    if (res == 0) return launch_fwd<kX, 0>(c, a);
+    if (res == 1) return launch_fwd<kX, 1>(c, a);
+    return launch_fwd<kX, 2>(c, a);
+  };
+  if (c.x_elem == kElemF32) return go(std::integral_constant<int, kElemF32>{});
+  if (c.x_elem == kElemBf16) return go(std::integral_constant<int, kElemBf16>{});
+  return go(std::integral_constant<int, kElemF16>{});
 }
 
-// Rows of the workspace: one per CTA of the backward.
+// Rows of the workspace, one per CTA of the backward: two CTAs an SM.
 int64_t rmsnorm_bwd_parts(int64_t rows, int64_t) { return std::min<int64_t>(rows, 304); }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c) {
-  const BwdArgs a = {c.dy, c.h, c.dh, c.weight, c.rstd, c.dx, c.partial, c.rows, c.cols,
+  const BwdArgs a = {c.dy, c.h, c.dh, c.weight, c.rstd, c.dx, c.dweight, c.partial, c.rows, c.cols,
                      c.elem, c.w_elem};
-  const int64_t parts = rmsnorm_bwd_parts(c.rows, c.cols);
-  if (c.cols % 8 == 0)
-    rmsnorm_bwd_long_kernel<8><<<static_cast<unsigned>(parts), threads_for(c.cols, 8), 0, c.st>>>(a);
-  else
-    rmsnorm_bwd_long_kernel<1><<<static_cast<unsigned>(parts), threads_for(c.cols, 1), 0, c.st>>>(a);
-  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-  rmsnorm_dweight_kernel<<<static_cast<unsigned>((c.cols + 127) / 128), 128, 0, c.st>>>(
-      c.partial, parts, c.cols, c.dweight, c.w_elem);
-  return cudaGetLastError();
+  const unsigned parts = static_cast<unsigned>(rmsnorm_bwd_parts(c.rows, c.cols));
+  const bool regs = c.cols <= bwd_max_cols(c.cols, c.elem);
+  const cudaError_t e = c.elem == kElemF32 ? launch_bwd<kElemF32>(c, a, parts)
+                        : c.elem == kElemBf16 ? launch_bwd<kElemBf16>(c, a, parts)
+                                              : launch_bwd<kElemF16>(c, a, parts);
+  if (e != cudaSuccess || (regs && parts == 1)) return e;
+  // launched while the backward drains; it waits for the partial rows itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((c.cols + 31) / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = c.st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel, static_cast<const float*>(c.partial),
+                            static_cast<int>(parts), c.cols, c.dweight, c.w_elem);
 }
 
 }  // namespace nf4

@@ -22,7 +22,7 @@ FP8_BLOCK = 128
 FP8_DTYPE = torch.float8_e4m3fn
 
 
-@dataclass
+@dataclass(slots=True)
 class FP8Tensor:
     """codes float8_e4m3fn [rows, cols], scale float32
     [ceil(rows / block_rows), ceil(cols / 128)]; block_rows is 1 (activations,
@@ -65,16 +65,25 @@ def _check_fp8(t: FP8Tensor, name: str, device: torch.device):
     """Types, exact sizes, contiguity and device of one block-scaled tensor."""
     if not isinstance(t, FP8Tensor):
         raise ValueError(f"{name} must be an FP8Tensor, got {type(t)}")
-    _check_block_rows(t.block_rows)
-    _require(t.codes, f"{name}.codes", FP8_DTYPE)
-    if t.codes.dim() != 2:
+    codes, scale, block_rows = t.codes, t.scale, t.block_rows
+    try:                         # the whole check in one pass; what fails is named below
+        rows, cols = codes.shape
+        if (codes.dtype is FP8_DTYPE and scale.dtype is torch.float32 and codes.is_contiguous()
+                and scale.is_contiguous() and cols % 16 == 0 and block_rows in (1, FP8_BLOCK)
+                and scale.shape == (-(-rows // block_rows), -(-cols // FP8_BLOCK))
+                and codes.device == device and scale.device == device):
+            return
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _check_block_rows(block_rows)
+    _require(codes, f"{name}.codes", FP8_DTYPE)
+    if codes.dim() != 2:
         raise ValueError(f"{name}.codes must be 2-D [rows, cols]")
-    rows, cols = t.codes.shape
+    rows, cols = codes.shape
     if cols % 16:
         raise ValueError(f"{name}: cols = {cols} is not a multiple of 16")
-    _require(t.scale, f"{name}.scale", torch.float32, shape=_scale_shape(rows, cols, t.block_rows))
-    if t.codes.device != device or t.scale.device != device:
-        _same_device(device, **{f"{name}.codes": t.codes, f"{name}.scale": t.scale})
+    _require(scale, f"{name}.scale", torch.float32, shape=_scale_shape(rows, cols, block_rows))
+    _same_device(device, **{f"{name}.codes": codes, f"{name}.scale": scale})
 
 
 def alloc_fp8(rows: int, cols: int, device, block_rows: int = 1) -> FP8Tensor:
@@ -115,7 +124,7 @@ def nf4_fp8_dequantize(q: FP8Tensor, out: torch.Tensor | None = None,
                        out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """[rows, cols] values of q in fp32, or rounded to bf16 or fp16 (for checks
     and export)."""
-    _check_fp8(q, "q", getattr(q, "device", None))
+    _check_fp8(q, "q", q.device if isinstance(q, FP8Tensor) else None)
     if out is not None:
         if not isinstance(out, torch.Tensor):
             raise ValueError("out must be a tensor")
@@ -135,7 +144,7 @@ def nf4_fp8_dequantize(q: FP8Tensor, out: torch.Tensor | None = None,
 
 def _matmul(name: str, fn: str, a: FP8Tensor, w: FP8Tensor, dx: bool, out, out_dtype,
             accumulate: bool) -> torch.Tensor:
-    device = getattr(a, "device", None)
+    device = a.codes.device if isinstance(a, FP8Tensor) and isinstance(a.codes, torch.Tensor) else None
     _check_fp8(a, name, device)
     _check_fp8(w, "weight", device)
     if a.block_rows != 1 or w.block_rows != FP8_BLOCK:
@@ -161,9 +170,10 @@ def _matmul(name: str, fn: str, a: FP8Tensor, w: FP8Tensor, dx: bool, out, out_d
         raise ValueError("accumulate=True needs the output tensor to add to (out=)")
     _require_cuda_device(device)
     y = out if out is not None else torch.empty((M, out_cols), dtype=out_dtype, device=device)
-    _check(fn, _call_on(device, getattr(lib(), fn), ctypes.byref(a.c_struct()),
-                        ctypes.byref(w.c_struct()), y.data_ptr(), ELEM[out_dtype],
-                        ACCUMULATE if accumulate else 0))
+    sa = nf4_fp8_tensor(a.codes.data_ptr(), a.scale.data_ptr(), M, red, 1)
+    sw = nf4_fp8_tensor(w.codes.data_ptr(), w.scale.data_ptr(), rows, cols, FP8_BLOCK)
+    _check(fn, _call_on(device, getattr(lib(), fn), ctypes.byref(sa), ctypes.byref(sw), y.data_ptr(),
+                        ELEM[out_dtype], ACCUMULATE if accumulate else 0))
     return y
 
 

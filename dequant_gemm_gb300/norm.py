@@ -5,7 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import (ELEM, _call_on, _check, _require, _require_cuda_device, _same_device, lib)
-from .fp8 import FP8_DTYPE, FP8Tensor, alloc_fp8
+from .fp8 import FP8_BLOCK, FP8_DTYPE, FP8Tensor
 
 
 def _require_matrix(t, name: str, shape=None):
@@ -63,7 +63,8 @@ def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
         h = out_h if out_h is not None else torch.empty_like(residual)
     rstd = torch.empty(rows, dtype=torch.float32, device=device) if save_rstd else None
     if fp8:
-        y = alloc_fp8(rows, cols, device)
+        y = FP8Tensor(torch.empty((rows, cols), dtype=FP8_DTYPE, device=device),
+                      torch.empty((rows, -(-cols // FP8_BLOCK)), dtype=torch.float32, device=device))
         y_ptr, y_elem, scale = y.codes.data_ptr(), 0, y.scale.data_ptr()
     else:
         y = torch.empty((rows, cols), dtype=out_dtype, device=device)

@@ -53,3 +53,16 @@ def test_norm_gradients_against_differences():
         assert abs(num - (dx * vx).sum()) <= 1e-7 * (1 + abs(num))
         num = (loss(x, w + step * vw) - loss(x, w - step * vw)) / (2 * step)
         assert abs(num - (dw * vw).sum()) <= 1e-7 * (1 + abs(num))
+
+
+def test_division_by_448_in_three_roundings_is_exact():
+    """q = fl(x r), r = fl(1 / 448); fl(q + fl(x - 448 q) r) is the IEEE quotient
+    for every fp32 significand: fp64 holds each exact product and remainder."""
+    f32, f64 = np.float32, np.float64
+    x = (np.arange(1 << 23, dtype=np.uint32) | 0x3F800000).view(f32)
+    r = f32(1) / f32(448)
+    q = x * r
+    rem = (x.astype(f64) - q.astype(f64) * 448).astype(f32)       # one FMA: exact before its rounding
+    # fl(rem r + q): the exact sum needs more than fp64 only in bits far below a half ulp of q
+    got = (rem.astype(f64) * f64(r) + q.astype(f64)).astype(f32)
+    assert np.array_equal(got, x / f32(448))
