@@ -142,15 +142,17 @@ def _stream(device: torch.device):
 
 
 # The current stream's handle by device index, without building a Stream object
-# (0.1 us instead of 1.9); torch keeps this accessor private.
+# (0.1 us instead of 1.9), and the current device without the lazy set-up
+# (which the tensors at hand have behind them); torch keeps both private.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call_on(device: torch.device, fn, *args) -> int:
     """fn(*args, stream) with `device` current; no switch where it already is."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _raw_device():
         return fn(*args, _raw_stream(index))
     with torch.cuda.device(device):
         return fn(*args, _raw_stream(torch.cuda.current_device()))

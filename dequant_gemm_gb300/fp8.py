@@ -61,29 +61,34 @@ def _check_block_rows(block_rows: int):
         raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
 
 
+def _fp8_ok(t: FP8Tensor, block_rows: int, device: torch.device) -> bool:
+    """The whole check of one block-scaled tensor in one pass, without naming
+    what is wrong with it (a call's host time is mostly such lookups)."""
+    try:
+        codes, scale = t.codes, t.scale
+        rows, cols = codes.shape
+        return (type(t) is FP8Tensor and t.block_rows == block_rows
+                and codes.dtype is FP8_DTYPE and scale.dtype is torch.float32
+                and codes.is_contiguous() and scale.is_contiguous() and cols % 16 == 0
+                and scale.shape == (-(-rows // block_rows), -(-cols // FP8_BLOCK))
+                and codes.device == device and scale.device == device)
+    except (AttributeError, TypeError, ValueError):
+        return False
+
+
 def _check_fp8(t: FP8Tensor, name: str, device: torch.device):
     """Types, exact sizes, contiguity and device of one block-scaled tensor."""
     if not isinstance(t, FP8Tensor):
         raise ValueError(f"{name} must be an FP8Tensor, got {type(t)}")
-    codes, scale, block_rows = t.codes, t.scale, t.block_rows
-    try:                         # the whole check in one pass; what fails is named below
-        rows, cols = codes.shape
-        if (codes.dtype is FP8_DTYPE and scale.dtype is torch.float32 and codes.is_contiguous()
-                and scale.is_contiguous() and cols % 16 == 0 and block_rows in (1, FP8_BLOCK)
-                and scale.shape == (-(-rows // block_rows), -(-cols // FP8_BLOCK))
-                and codes.device == device and scale.device == device):
-            return
-    except (AttributeError, TypeError, ValueError):
-        pass
-    _check_block_rows(block_rows)
-    _require(codes, f"{name}.codes", FP8_DTYPE)
-    if codes.dim() != 2:
+    _check_block_rows(t.block_rows)
+    _require(t.codes, f"{name}.codes", FP8_DTYPE)
+    if t.codes.dim() != 2:
         raise ValueError(f"{name}.codes must be 2-D [rows, cols]")
-    rows, cols = codes.shape
+    rows, cols = t.codes.shape
     if cols % 16:
         raise ValueError(f"{name}: cols = {cols} is not a multiple of 16")
-    _require(scale, f"{name}.scale", torch.float32, shape=_scale_shape(rows, cols, block_rows))
-    _same_device(device, **{f"{name}.codes": codes, f"{name}.scale": scale})
+    _require(t.scale, f"{name}.scale", torch.float32, shape=_scale_shape(rows, cols, t.block_rows))
+    _same_device(device, **{f"{name}.codes": t.codes, f"{name}.scale": t.scale})
 
 
 def alloc_fp8(rows: int, cols: int, device, block_rows: int = 1) -> FP8Tensor:
@@ -142,21 +147,31 @@ def nf4_fp8_dequantize(q: FP8Tensor, out: torch.Tensor | None = None,
     return y
 
 
-def _matmul(name: str, fn: str, a: FP8Tensor, w: FP8Tensor, dx: bool, out, out_dtype,
-            accumulate: bool) -> torch.Tensor:
-    device = a.codes.device if isinstance(a, FP8Tensor) and isinstance(a.codes, torch.Tensor) else None
+def _check_matmul(name: str, a: FP8Tensor, w: FP8Tensor, dx: bool, device):
+    """Raises for what is wrong with a product's operands, if anything is."""
     _check_fp8(a, name, device)
     _check_fp8(w, "weight", device)
     if a.block_rows != 1 or w.block_rows != FP8_BLOCK:
         raise ValueError(f"{name} must have block_rows 1 and the weight {FP8_BLOCK}, got "
                          f"{a.block_rows} and {w.block_rows}")
-    M, red = a.codes.shape
+    if w.rows % 16:
+        raise ValueError(f"weight: rows = {w.rows} is not a multiple of 16")
+    want = w.rows if dx else w.cols
+    if a.cols != want:
+        raise ValueError(f"{name} must be [M, {want}], got [{a.rows}, {a.cols}]")
+
+
+def _matmul(name: str, fn: str, a: FP8Tensor, w: FP8Tensor, dx: bool, out, out_dtype,
+            accumulate: bool) -> torch.Tensor:
+    codes = getattr(a, "codes", None)
+    device = codes.device if isinstance(codes, torch.Tensor) else None
+    if not (_fp8_ok(a, 1, device) and _fp8_ok(w, FP8_BLOCK, device)):
+        _check_matmul(name, a, w, dx, device)
+    M, red = codes.shape
     rows, cols = w.codes.shape
-    if rows % 16:
-        raise ValueError(f"weight: rows = {rows} is not a multiple of 16")
-    if red != (rows if dx else cols):
-        raise ValueError(f"{name} must be [M, {rows if dx else cols}], got [{M}, {red}]")
-    out_cols = cols if dx else rows
+    if rows % 16 or red != (rows if dx else cols):
+        _check_matmul(name, a, w, dx, device)
+    shape = (M, cols if dx else rows)
     if out is not None:
         if not isinstance(out, torch.Tensor):
             raise ValueError("out must be a tensor")
@@ -164,16 +179,17 @@ def _matmul(name: str, fn: str, a: FP8Tensor, w: FP8Tensor, dx: bool, out, out_d
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"the output must be float32 or bfloat16, got {out_dtype}")
     if out is not None:
-        _require(out, "out", out_dtype, shape=(M, out_cols))
+        _require(out, "out", out_dtype, shape=shape)
         _same_device(device, out=out)
     elif accumulate:
         raise ValueError("accumulate=True needs the output tensor to add to (out=)")
     _require_cuda_device(device)
-    y = out if out is not None else torch.empty((M, out_cols), dtype=out_dtype, device=device)
-    sa = nf4_fp8_tensor(a.codes.data_ptr(), a.scale.data_ptr(), M, red, 1)
-    sw = nf4_fp8_tensor(w.codes.data_ptr(), w.scale.data_ptr(), rows, cols, FP8_BLOCK)
-    _check(fn, _call_on(device, getattr(lib(), fn), ctypes.byref(sa), ctypes.byref(sw), y.data_ptr(),
-                        ELEM[out_dtype], ACCUMULATE if accumulate else 0))
+    y = out if out is not None else torch.empty(shape, dtype=out_dtype, device=device)
+    _check(fn, _call_on(
+        device, getattr(lib(), fn),
+        ctypes.byref(nf4_fp8_tensor(codes.data_ptr(), a.scale.data_ptr(), M, red, 1)),
+        ctypes.byref(nf4_fp8_tensor(w.codes.data_ptr(), w.scale.data_ptr(), rows, cols, FP8_BLOCK)),
+        y.data_ptr(), ELEM[out_dtype], ACCUMULATE if accumulate else 0))
     return y
 
 

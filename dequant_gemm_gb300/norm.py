@@ -23,6 +23,33 @@ def _check_norm(x, name: str, weight):
         _same_device(x.device, weight=weight)
 
 
+def _plain_matrix(x, weight) -> bool:
+    """Whether x [rows, cols] and weight [cols] pass _check_norm, in one pass
+    that does not say why not."""
+    try:
+        rows, cols = x.shape
+        return (x.dtype in ELEM and weight.dtype in ELEM and weight.shape == (cols,) and cols > 0
+                and x.is_contiguous() and weight.is_contiguous() and weight.device == x.device)
+    except (AttributeError, TypeError, ValueError):
+        return False
+
+
+def _check_fwd(x, weight, residual):
+    """Raises for what is wrong with the forward's inputs, if anything is."""
+    _check_norm(x, "x", weight)
+    if residual is not None:
+        _require_matrix(residual, "residual", x.shape)
+        if residual.dtype not in (x.dtype, torch.float32):
+            raise ValueError(f"residual must be {x.dtype} or float32, got {residual.dtype}")
+        _same_device(x.device, residual=residual)
+
+
+def _like(t, h) -> bool:
+    """Whether t has h's type, shape and device and is contiguous."""
+    return (isinstance(t, torch.Tensor) and t.dtype is h.dtype and t.shape == h.shape
+            and t.is_contiguous() and t.device == h.device)
+
+
 def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
                     eps: float = 1e-6, out_dtype: torch.dtype | None = None,
                     save_rstd: bool = False, out_h: torch.Tensor | None = None):
@@ -35,14 +62,12 @@ def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
     multiple of 16). rstd (fp32 [rows]) is what the backward needs, None
     unless save_rstd. out_h: where to write h; the residual itself may be
     given, to update the stream in place."""
-    _check_norm(x, "x", weight)
+    if not _plain_matrix(x, weight) or residual is not None and not (
+            isinstance(residual, torch.Tensor) and residual.shape == x.shape
+            and (residual.dtype is x.dtype or residual.dtype is torch.float32)
+            and residual.is_contiguous() and residual.device == x.device):
+        _check_fwd(x, weight, residual)
     rows, cols = x.shape
-    if residual is not None:
-        _require_matrix(residual, "residual", x.shape)
-        if residual.dtype not in (x.dtype, torch.float32):
-            raise ValueError(f"residual must be {x.dtype} or float32, got {residual.dtype}")
-        if residual.device != x.device:
-            _same_device(x.device, residual=residual)
     if out_h is not None:
         if residual is None:
             raise ValueError("out_h without a residual: h is x itself")
@@ -84,15 +109,18 @@ def nf4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rst
     is the gradient of y and dh (optional) the one that reaches h from the
     residual stream, both of h's type; h and rstd as the forward returned
     them. An 8-bit y passes its gradient through."""
-    _check_norm(h, "h", weight)
+    if not _plain_matrix(h, weight):
+        _check_norm(h, "h", weight)
     rows, cols = h.shape
-    _require(dy, "dy", h.dtype, shape=h.shape)
-    _require(rstd, "rstd", torch.float32, shape=(rows,))
-    if dh is not None:
+    if not _like(dy, h):
+        _require(dy, "dy", h.dtype, shape=h.shape)
+        _same_device(h.device, dy=dy)
+    if dh is not None and not _like(dh, h):
         _require(dh, "dh", h.dtype, shape=h.shape)
         _same_device(h.device, dh=dh)
-    if dy.device != h.device or rstd.device != h.device:
-        _same_device(h.device, dy=dy, rstd=rstd)
+    _require(rstd, "rstd", torch.float32, shape=(rows,))
+    if rstd.device != h.device:
+        _same_device(h.device, rstd=rstd)
     device = h.device
     _require_cuda_device(device)
     L = lib()
