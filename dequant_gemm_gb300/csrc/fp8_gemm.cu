@@ -71,12 +71,20 @@ __device__ __forceinline__ float4 lds128(uint32_t a) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void sts(uint32_t a, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
+}
+
+// Four bytes from global to shared memory, or zeros (ok false: src is not
+// read), without a register or a wait; and this thread's arrival on an mbarrier
+// once all its copies so far have landed.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_on_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Arrive on an mbarrier of the cluster without ordering this thread's memory
@@ -146,7 +154,7 @@ struct MatmulArgs {
 // of 168: the first four warps give theirs up.
 // Persistent: a pair takes the tiles c, c + G, ... in turn, tokens fastest,
 // and the copies and MMAs of the next tile start while one is written out.
-constexpr int kPairStages = 5;
+constexpr int kPairStages = 4;
 constexpr int kPairBN = 256;
 constexpr int kTileBytes = 128 * 128;                  // 128 rows of one block
 constexpr int kPairStageBytes = 2 * kTileBytes;
@@ -165,7 +173,7 @@ constexpr int kPairOffBox = kPairStages * kPairStageBytes;
 constexpr int kScaleChunk = 16;
 constexpr int kScalePitch = 130;
 constexpr int kScaleBytes = kScaleChunk * kScalePitch * 4;
-constexpr int kPairOffScale = kPairOffBox + kPairTotalWarps * kBoxBytes;
+constexpr int kPairOffScale = kPairOffBox + 2 * kPairTotalWarps * kBoxBytes;
 constexpr int kPairOffBars = kPairOffScale + 2 * kScaleBytes;
 constexpr int kPairSmem = kPairOffBars + 256 + 1024;   // + alignment slack
 static_assert(kPairSmem <= 227 * 1024, "shared memory");
@@ -201,7 +209,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(sum_bar(b), 1);
       tc::mbar_init(read_bar(b), 2 * kPairTotalWarps);
-      tc::mbar_init(sfull_bar(b), 2);
+      tc::mbar_init(sfull_bar(b), 64);   // the scale warps' lanes
       tc::mbar_init(sempty_bar(b), kPairTotalWarps);
     }
     tc::mbar_init(drain_bar, 1);
@@ -340,7 +348,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       const int64_t m0 = tile_m(u), cb = tile_c(u) / 128 + (lane >> 4);
       const int tokens = static_cast<int>(min(p.M - m0, static_cast<int64_t>(128)));
       const float* src = p.a_scale + (m0 + t0) * p.rb + j;
-      const float* wsrc = warp == 2 && cb < col_blocks ? p.w_scale + cb * p.ws_col + j * p.ws_red : nullptr;
+      const float* wsrc = p.w_scale + cb * p.ws_col + j * p.ws_red;
+      const bool w_in = cb < col_blocks;
       for (int i = 0; i < p.rb; i += kScaleChunk, ++ch) {
         int r = tc::mbar_wait_abortable(sempty_bar(ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag);
         r = __shfl_sync(0xffffffffu, r, 0);
@@ -351,19 +360,11 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
         const uint32_t dst = base + kPairOffScale + (ch & 1) * kScaleBytes + j * kScalePitch * 4;
         const int n = i + j < p.rb ? tokens : 0;       // tokens to read in this lane's block
-        const float* at = src + i;
-#pragma unroll 1
-        for (int h = 0; h < 128; h += 32, at += 32ll * p.rb) {
-          float v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            v[k] = t0 + h + 4 * k < n ? __ldg(at + 4ll * k * p.rb) : 0.0f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sts(dst + 4 * (t0 + h + 4 * k), v[k]);
-        }
-        if (warp == 2) sts(dst + 4 * (128 + (lane >> 4)), n > 0 && wsrc ? __ldg(wsrc + i * p.ws_red) : 0.0f);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sfull_bar(ch & 1));
+#pragma unroll 2
+        for (int t = t0; t < 128; t += 4)
+          copy4(dst + 4 * t, src + i + static_cast<int64_t>(t < n ? t - t0 : 0) * p.rb, t < n);
+        if (warp == 2) copy4(dst + 4 * (128 + (lane >> 4)), wsrc + i * p.ws_red, n > 0 && w_in);
+        arrive_on_copies(sfull_bar(ch & 1));
       }
     }
    }
@@ -371,7 +372,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairManyRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128u * half;
-    const uint32_t box_addr = base + kPairOffBox + (warp - 4) * kBoxBytes;
+    const uint32_t box_addr = base + kPairOffBox + (warp - 4) * 2 * kBoxBytes;
     const int row = 32 * q + lane;       // token of this thread within the CTA's 128
     const uint32_t scales = base + kPairOffScale;
 
@@ -445,11 +446,11 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           for (int t = 0; t < 8; ++t) acc[j + t] += o[t];
         }
       }
-      auto send = [&](int64_t c) {
+      auto send = [&](int64_t c, int k) {
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0 && c < p.cols) {
-          tc::tma_store_2d(&tm_out, box_addr, static_cast<int32_t>(c), static_cast<int32_t>(m0));
+          tc::tma_store_2d(&tm_out, box_addr + (k & 1) * kBoxBytes, static_cast<int32_t>(c), static_cast<int32_t>(m0));
           tc::bulk_commit();
         }
       };
@@ -461,26 +462,26 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (p.out_bf16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          reuse();
+          if (h == 0) reuse();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float* a = acc + 64 * h + 8 * j;
-            sts128(rowp + 16 * (j ^ (lane & 7)), pack2<kElemBf16>(a[0], a[1]), pack2<kElemBf16>(a[2], a[3]),
+            sts128(rowp + h * kBoxBytes + 16 * (j ^ (lane & 7)), pack2<kElemBf16>(a[0], a[1]), pack2<kElemBf16>(a[2], a[3]),
                    pack2<kElemBf16>(a[4], a[5]), pack2<kElemBf16>(a[6], a[7]));
           }
-          send(c0 + 64 * h);
+          send(c0 + 64 * h, h);
         }
       } else {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          reuse();
+          if (h % 2 == 0) reuse();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float* a = acc + 32 * h + 4 * j;
-            sts128(rowp + 16 * (j ^ (lane & 7)), __float_as_uint(a[0]), __float_as_uint(a[1]),
+            sts128(rowp + (h & 1) * kBoxBytes + 16 * (j ^ (lane & 7)), __float_as_uint(a[0]), __float_as_uint(a[1]),
                    __float_as_uint(a[2]), __float_as_uint(a[3]));
           }
-          send(c0 + 32 * h);
+          send(c0 + 32 * h, h);
         }
       }
     }
@@ -506,7 +507,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 // receives the others' totals of them and adds the S contributions in rank
 // order (repeatable, no workspace, no zeroing pass).
 //   warp 0 copies, warp 1 MMAs into kBufs buffers of kBT columns, warps 2-3
-//   scales (token scale times the tile's weight scale, [block][token]),
+//   scales (the tokens', [block][token], and the tile's weight scale),
 //   warps 4.. totals: a thread holds one output column for kBT / kGroups
 //   tokens, whose factors it reads as broadcasts.
 template <int kBT>
@@ -568,7 +569,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       tc::mbar_init(read_bar(i), C::kTotalWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(sfull_bar(i), 2);
+      tc::mbar_init(sfull_bar(i), 64);
       tc::mbar_init(sempty_bar(i), C::kTotalWarps);
     }
     tc::mbar_init(drain_bar, 1);
@@ -666,24 +667,16 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (!waited(sempty_bar(ch & 1), ((ch >> 1) & 1) ^ 1, kRoleProducer)) break;
       const uint32_t dst = base + C::kOffScale + (ch & 1) * C::kChunkBytes + j * (C::kPitch * 4);
       const int n = i + j < nb ? tokens : 0;
-      const float w = n > 0 ? __ldg(ws + i * p.ws_red) : 0.0f;
-      constexpr int kStep = kBT < 32 ? kBT / 4 : 8;
-#pragma unroll 1
-      for (int h = 0; h < kBT; h += 4 * kStep) {
-        float v[kStep];
-#pragma unroll
-        for (int k = 0; k < kStep; ++k)
-          v[k] = t0 + h + 4 * k < n ? __ldg(as + i + (h + 4ll * k) * p.rb) : 0.0f;
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) sts(dst + 4 * (t0 + h + 4 * k), v[k] * w);
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(sfull_bar(ch & 1));
+#pragma unroll 8
+      for (int t = t0; t < kBT; t += 4)
+        copy4(dst + 4 * t, as + i + static_cast<int64_t>(t < n ? t - t0 : 0) * p.rb, t < n);
+      if (warp == 2 && lane < 16) copy4(dst + 4 * kBT, ws + i * p.ws_red, n > 0);
+      arrive_on_copies(sfull_bar(ch & 1));
     }
   } else {
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kCols * part;
-    const uint32_t scales = base + C::kOffScale + 4 * C::kCols * part;
+    const uint32_t scales = base + C::kOffScale;
     // read back into this CTA's own barrier, by its cluster address (the
     // relaxed arrival costs half of the local releasing one)
     const uint32_t read_remote = tc::mapa(read_bar(0), tc::cluster_ctarank());
@@ -696,20 +689,21 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (!waited(sum_bar(buf), ph, kRoleCompute)) break;
       tc::fence_after_sync();
       const uint32_t sp = scales + (ch & 1) * C::kChunkBytes + in * (C::kPitch * 4);
+      const float w = lds(sp + 4 * kBT);
 #pragma unroll
       for (int c = 0; c < C::kCols; c += 16) {
         float v[16];
         tmem_ld16f(src + kBT * buf + c, v);
         float4 f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = lds128(sp + 4 * c + 16 * k);
+        for (int k = 0; k < 4; ++k) f[k] = lds128(sp + 4 * (C::kCols * part + c) + 16 * k);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          acc[c + 4 * k] = fmaf(v[4 * k], f[k].x, acc[c + 4 * k]);
-          acc[c + 4 * k + 1] = fmaf(v[4 * k + 1], f[k].y, acc[c + 4 * k + 1]);
-          acc[c + 4 * k + 2] = fmaf(v[4 * k + 2], f[k].z, acc[c + 4 * k + 2]);
-          acc[c + 4 * k + 3] = fmaf(v[4 * k + 3], f[k].w, acc[c + 4 * k + 3]);
+          acc[c + 4 * k] = fmaf(v[4 * k] * w, f[k].x, acc[c + 4 * k]);
+          acc[c + 4 * k + 1] = fmaf(v[4 * k + 1] * w, f[k].y, acc[c + 4 * k + 1]);
+          acc[c + 4 * k + 2] = fmaf(v[4 * k + 2] * w, f[k].z, acc[c + 4 * k + 2]);
+          acc[c + 4 * k + 3] = fmaf(v[4 * k + 3] * w, f[k].w, acc[c + 4 * k + 3]);
         }
       }
       tc::fence_before_sync();
