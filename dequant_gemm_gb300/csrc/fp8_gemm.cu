@@ -778,22 +778,88 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   }
 }
 
+// Launch shape of a rows call: splits of the reduction, and its time in 0.01
+// us, start-up left out. Measured at 128 tokens a tile on the decoder shapes:
+// 0.46 us a block, 1.5 us a round for the last block and the reduction.
+struct RowsPlan {
+  int splits;
+  int64_t cost;
+};
+
+template <bool kDx, int kBT>
+cudaLaunchConfig_t rows_config(int splits, int64_t row_tiles, int64_t m_tiles, cudaStream_t st,
+                               cudaLaunchAttribute* attr) {
+  using C = RowsCfg<kBT>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(row_tiles),
+                     static_cast<unsigned>(m_tiles));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = static_cast<unsigned>(splits);
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// CTAs that run at once in clusters of 1, 2, 4 and 8 (one an SM; a cluster
+// stays within a group of SMs, so that fewer CTAs fit in large ones).
+struct RowsCapacity {
+  int ctas[4];
+};
+
+template <bool kDx, int kBT>
+RowsCapacity rows_capacity(const Fp8Call& c) {
+  static std::once_flag once[kOnceDevices];
+  static RowsCapacity known[kOnceDevices];
+  RowsCapacity here = {};
+  auto find = [&] {
+    cudaFuncSetAttribute(fp8_rows_kernel<kDx, kBT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         RowsCfg<kBT>::kSmem);
+    for (int i = 0; i < 4; ++i) {
+      cudaLaunchAttribute attr;
+      const cudaLaunchConfig_t cfg = rows_config<kDx, kBT>(1 << i, c.num_sms, 1, c.st, &attr);
+      int clusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters, fp8_rows_kernel<kDx, kBT>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        clusters = i == 0 ? c.num_sms : 0;
+      }
+      here.ctas[i] = clusters << i;
+    }
+  };
+  if (c.device < 0 || c.device >= kOnceDevices) {
+    find();
+    return here;
+  }
+  once_per_device(once, c.device, [&] {
+    find();
+    known[c.device] = here;
+  });
+  return known[c.device];
+}
+
+template <bool kDx, int kBT>
+RowsPlan plan_rows(const Fp8Call& c, const MatmulArgs& a) {
+  const RowsCapacity cap = rows_capacity<kDx, kBT>(c);
+  const int64_t tiles = (a.cols + 127) / 128 * ((c.M + kBT - 1) / kBT);
+  RowsPlan best = {1, INT64_MAX};
+  for (int i = 0; i < 4 && (1 << i) <= a.rb; ++i) {
+    const int s = 1 << i;
+    if (cap.ctas[i] < s) break;
+    const int64_t rounds = (tiles * s + cap.ctas[i] - 1) / cap.ctas[i];
+    const int64_t cost = rounds * ((a.rb + s - 1) / s * 46 + 150);
+    if (cost < best.cost) best = {s, cost};
+  }
+  return best;
+}
+
 template <bool kDx, int kBT>
 cudaError_t launch_rows(const Fp8Call& c, const MatmulArgs& a, int64_t red) {
-  using C = RowsCfg<kBT>;
   const int64_t row_tiles = (a.cols + 127) / 128, m_tiles = (c.M + kBT - 1) / kBT;
-  // splits: the shortest makespan in blocks, a CTA's fixed cost (start, last
-  // block, reduction) counted as 8
-  int splits = 1;
-  int64_t best = INT64_MAX;
-  for (int s = 1; s <= 8 && s <= a.rb; s *= 2) {
-    const int64_t rounds = (row_tiles * m_tiles * s + c.num_sms - 1) / c.num_sms;
-    const int64_t cost = rounds * ((a.rb + s - 1) / s + 8);
-    if (cost < best) {
-      best = cost;
-      splits = s;
-    }
-  }
+  const int splits = plan_rows<kDx, kBT>(c, a).splits;
   CUtensorMap tm_a, tm_w;
   const uint64_t ur = static_cast<uint64_t>(red), um = static_cast<uint64_t>(c.M);
   if (!encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.a, ur, um, ur, 128, kBT,
@@ -802,23 +868,8 @@ cudaError_t launch_rows(const Fp8Call& c, const MatmulArgs& a, int64_t red) {
                  static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.K), 128, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  static std::once_flag once[kOnceDevices];
-  once_per_device(once, c.device, [] {
-    cudaFuncSetAttribute(fp8_rows_kernel<kDx, kBT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  });
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(row_tiles),
-                     static_cast<unsigned>(m_tiles));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = c.st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = rows_config<kDx, kBT>(splits, row_tiles, m_tiles, c.st, &attr);
   return cudaLaunchKernelEx(&cfg, fp8_rows_kernel<kDx, kBT>, tm_a, tm_w, a);
 }
 
@@ -880,6 +931,12 @@ cudaError_t launch_any(const Fp8Call& c) {
   if (c.M <= 32) return launch_rows<kDx, 32>(c, a, red);
   if (c.M <= 64) return launch_rows<kDx, 64>(c, a, red);
   if (c.M <= 128) return launch_rows<kDx, 128>(c, a, red);
+  // more tokens: pairs, unless their tiles leave most SMs idle for a long
+  // reduction, which the rows kernel splits (512 x 3584 forward at 250 tokens
+  // 16.2 us on pairs, 7.8 in rows; 4096 x 4096 at 512 tokens 18.8 and 20.4)
+  const int64_t units = (c.M + 255) / 256 * ((a.cols + kPairBN - 1) / kPairBN);
+  const int64_t rounds = (units + c.num_sms / 2 - 1) / std::max(1, c.num_sms / 2);
+  if (plan_rows<kDx, 128>(c, a).cost < rounds * (a.rb * 39 + 100)) return launch_rows<kDx, 128>(c, a, red);
   return launch_pair<kDx>(c, a, red);
 }
 
