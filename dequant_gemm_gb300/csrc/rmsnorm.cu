@@ -47,6 +47,104 @@ __device__ __forceinline__ void store_any(void* p, int elem, int64_t i, const fl
   }
 }
 
+// Runs of 8 elements. Where a row's length is a multiple of 8 its runs start at
+// its first element; otherwise (kShift) rows start anywhere, and the runs are
+// those of the whole tensor, on 16-byte boundaries: a row's first run starts
+// up to 7 elements before it and its last may end behind it. `col` is the
+// column of the run's first element, `at` its index in the tensor of `total`
+// elements. What a run holds of the neighbouring rows is loaded with it and
+// dropped (eight guarded loads of single elements took as many round trips
+// to memory), and never written.
+template <bool kShift>
+__device__ __forceinline__ bool whole_run(int col, int cols) {
+  return kShift ? col >= 0 && col + 8 <= cols : col < cols;
+}
+template <bool kShift>
+__device__ __forceinline__ bool any_of_run(int col, int cols) {
+  return kShift ? col + 8 > 0 && col < cols : col < cols;
+}
+
+template <bool kShift>
+__device__ __forceinline__ void load_run(const void* p, int elem, int64_t at, int col, int cols,
+                                         int64_t total, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  if (!any_of_run<kShift>(col, cols)) return;
+  if (!kShift || at + 8 <= total) {
+    load_any<8>(p, elem, at, v);
+  } else {                           // the tensor's last run
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j >= 0 && col + j < cols) {
+        float u[1];
+        load_any<1>(p, elem, at + j, u);
+        v[j] = u[0];
+      }
+  }
+}
+
+// Drops what lies outside the row; after all loads have gone out, so that none
+// is waited for before the next.
+template <bool kShift>
+__device__ __forceinline__ void trim_run(int col, int cols, float (&v)[8]) {
+  if (!kShift || whole_run<kShift>(col, cols)) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (col + j < 0 || col + j >= cols) v[j] = 0.0f;
+}
+
+// Eight consecutive elements of a vector over the columns, zeros outside it.
+// Unaligned with kShift: single elements at indexes held within the vector, so
+// that the loads need no guards and go out together, or for fp32 the three
+// aligned quadruples around them (single elements lie 32 bytes apart between
+// lanes, and cost eight times the wavefronts).
+template <int kElem>
+__device__ __forceinline__ void load8_clamped(const void* p, int col, int cols, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = to_float<kElem>(static_cast<const typename Elem<kElem>::T*>(p)[min(max(col + j, 0), cols - 1)]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (col + j < 0 || col + j >= cols) v[j] = 0.0f;
+}
+
+template <bool kShift>
+__device__ __forceinline__ void load_weight(const void* p, int elem, int col, int cols, float (&v)[8]) {
+  if constexpr (!kShift) {
+    load_run<false>(p, elem, col, col, cols, cols, v);
+  } else if (elem == kElemF32) {
+    const int q = col & ~3, m = col & 3;           // m: the same in the whole row
+    if (q >= 0 && q + 12 <= cols) {
+      const float4* w = reinterpret_cast<const float4*>(static_cast<const float*>(p) + q);
+      const float4 a = w[0], b = w[1], c = w[2];
+      const float f[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = m == 0 ? f[j] : m == 1 ? f[j + 1] : m == 2 ? f[j + 2] : f[j + 3];
+    } else {
+      load8_clamped<kElemF32>(p, col, cols, v);
+    }
+  } else if (elem == kElemBf16) {
+    load8_clamped<kElemBf16>(p, col, cols, v);
+  } else {
+    load8_clamped<kElemF16>(p, col, cols, v);
+  }
+}
+
+template <bool kShift>
+__device__ __forceinline__ void store_run(void* p, int elem, int64_t at, int col, int cols,
+                                          const float (&v)[8]) {
+  if (whole_run<kShift>(col, cols)) {
+    store_any<8>(p, elem, at, v);
+  } else if (kShift) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j >= 0 && col + j < cols) {
+        const float u[1] = {v[j]};
+        store_any<1>(p, elem, at + j, u);
+      }
+  }
+}
+
 // v rounded to the type `elem` and widened again.
 __device__ __forceinline__ float round_to(float v, int elem) {
   if (elem == kElemBf16) return __bfloat162float(__float2bfloat16_rn(v));
@@ -118,64 +216,58 @@ __device__ __forceinline__ void write_y(const FwdArgs& p, int64_t row, int64_t c
 }
 
 // One CTA a row, held in registers between the sum and the output: x and the
-// residual are read once, h and y written once. A thread holds kNC runs of
-// kVec elements, blockDim.x runs apart (8 elements, so that 16 lanes hold a
-// block of the 8-bit output; single elements where the row's length leaves
-// rows unaligned).
-template <int kX, int kRes, int kVec, int kNC>
+// residual are read once, h and y written once. A thread holds kNC runs of 8
+// elements, blockDim.x runs apart (so that 16 lanes hold a block of the 8-bit
+// output). Odd lengths keep the 16-byte accesses (kShift): with single elements
+// a lane the norm of 4096 x 5119 took 62 us.
+template <int kX, int kRes, bool kShift, int kNC>
 __global__ void __launch_bounds__(1024)
 rmsnorm_fwd_kernel(const FwdArgs p) {
   __shared__ float part[32];
   constexpr int kH = kRes == 2 ? kElemF32 : kX;    // the stream's type
-  const int64_t row = blockIdx.x, row0 = row * p.cols;
-  const int cols = static_cast<int>(p.cols), step = blockDim.x * kVec;
-  float v[kNC][kVec];
+  const int64_t row = blockIdx.x, row0 = row * p.cols, total = gridDim.x * p.cols;
+  const int cols = static_cast<int>(p.cols), step = blockDim.x * 8;
+  const int c0 = static_cast<int>(threadIdx.x) * 8 - (kShift ? static_cast<int>(row0 & 7) : 0);
+  float v[kNC][8];
 #pragma unroll
-  for (int i = 0; i < kNC; ++i) {
-    const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) v[i][j] = 0.0f;
-    if (c < cols) load_any<kVec>(p.x, kX, row0 + c, v[i]);
-  }
+  for (int i = 0; i < kNC; ++i)
+    load_run<kShift>(p.x, kX, row0 + c0 + i * step, c0 + i * step, cols, total, v[i]);
   if constexpr (kRes != 0) {
-    float r[kNC][kVec];
+    float r[kNC][8];
 #pragma unroll
-    for (int i = 0; i < kNC; ++i) {
-      const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) r[i][j] = 0.0f;
-      if (c < cols) load_any<kVec>(p.residual, kH, row0 + c, r[i]);
-    }
+    for (int i = 0; i < kNC; ++i)
+      load_run<kShift>(p.residual, kH, row0 + c0 + i * step, c0 + i * step, cols, total, r[i]);
 #pragma unroll
     for (int i = 0; i < kNC; ++i)
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] = round_to(v[i][j] + r[i][j], kH);
+      for (int j = 0; j < 8; ++j) v[i][j] = round_to(v[i][j] + r[i][j], kH);
   }
   float ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kNC; ++i)
+  for (int i = 0; i < kNC; ++i) {
+    trim_run<kShift>(c0 + i * step, cols, v[i]);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) ss += v[i][j] * v[i][j];
+    for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+  }
   if constexpr (kRes != 0) {
 #pragma unroll
-    for (int i = 0; i < kNC; ++i) {
-      const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
-      if (c < cols) store_any<kVec>(p.h, kH, row0 + c, v[i]);
-    }
+    for (int i = 0; i < kNC; ++i)
+      store_run<kShift>(p.h, kH, row0 + c0 + i * step, c0 + i * step, cols, v[i]);
   }
   const float rstd = rsqrtf(block_sum(ss, part) / static_cast<float>(cols) + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < kNC; ++i) {
-    const int c = static_cast<int>(threadIdx.x) * kVec + i * step;
-    const bool in = c < cols;
+    const int c = c0 + i * step;
+    const bool in = any_of_run<kShift>(c, cols);
     if (in) {
-      float w[kVec];
-      load_any<kVec>(p.weight, p.w_elem, c, w);
+      float w[8];
+      load_weight<kShift>(p.weight, p.w_elem, c, cols, w);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[i][j] = v[i][j] * rstd * w[j];
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
     }
-    write_y<kVec>(p, row, c, in, v[i]);
+    if (p.y_fp8) write_y<8>(p, row, c, in, v[i]);
+    else store_run<kShift>(p.y, p.y_elem, row0 + c, c, cols, v[i]);
   }
 }
 
@@ -265,20 +357,20 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_long_kernel(const BwdArgs p) 
   }
 }
 
-// kVec elements as they lie in memory (16 or 32 bytes, or one element), so
-// that a row on its way costs no more registers than it has bytes.
-template <int kElem, int kVec>
+// A run as it lies in memory (16 or 32 bytes), so that a row on its way costs
+// no more registers than it has bytes.
+template <int kElem>
 struct Raw {
-  static constexpr int kWords = kVec == 8 ? 2 * Elem<kElem>::kBytes : 1;
+  static constexpr int kWords = 2 * Elem<kElem>::kBytes;
   uint32_t w[kWords];
 
-  __device__ __forceinline__ void zero() {
+  template <bool kShift>
+  __device__ __forceinline__ void load(const void* p, int64_t at, int col, int cols, int64_t total) {
 #pragma unroll
     for (int j = 0; j < kWords; ++j) w[j] = 0u;
-  }
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    if constexpr (kVec == 8) {
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * Elem<kElem>::kBytes);
+    if (!any_of_run<kShift>(col, cols)) return;
+    if (!kShift || at + 8 <= total) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * Elem<kElem>::kBytes);
 #pragma unroll
       for (int j = 0; j < kWords / 4; ++j) {
         const uint4 u = q[j];
@@ -287,11 +379,25 @@ struct Raw {
         w[4 * j + 2] = u.z;
         w[4 * j + 3] = u.w;
       }
-    } else if constexpr (kElem == kElemF32) {
-      w[0] = static_cast<const uint32_t*>(p)[i];
-    } else {
-      w[0] = static_cast<const uint16_t*>(p)[i];
+    } else {                         // the tensor's last run
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j >= 0 && col + j < cols) {
+          if constexpr (kElem == kElemF32) w[j] = static_cast<const uint32_t*>(p)[at + j];
+          else w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at + j]) << (16 * (j & 1));
+        }
     }
+  }
+  // As trim_run.
+  template <bool kShift>
+  __device__ __forceinline__ void trim(int col, int cols) {
+    if (!kShift || whole_run<kShift>(col, cols)) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < 0 || col + j >= cols) {
+        if constexpr (kElem == kElemF32) w[j] = 0u;
+        else w[j >> 1] &= (j & 1) ? 0xffffu : 0xffff0000u;
+      }
   }
   __device__ __forceinline__ float at(int j) const {
     if constexpr (kElem == kElemF32) return __uint_as_float(w[j]);
@@ -302,40 +408,39 @@ struct Raw {
 
 // Rows of up to kNC runs a thread, in registers: gridDim.x CTAs take the rows
 // in turn, the next row's loads under way while this one is reduced (kAhead),
-// each thread's share of dw in registers until the CTA is done. One CTA alone
-// writes dw itself.
-template <int kElem, int kVec, int kNC, bool kAhead>
-__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const BwdArgs p) {
-  using R = Raw<kElem, kVec>;
+// each thread's share of dw in registers until the CTA is done. That wants a
+// thread's columns to be the same in all rows of its CTA: with kShift the
+// rows' offsets repeat every 8 rows, and gridDim.x is a multiple of 8 (or
+// every CTA has one row). One CTA alone writes dw itself.
+template <int kElem, bool kShift, int kNC, bool kAhead, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_bwd_kernel(const BwdArgs p) {
+  using R = Raw<kElem>;
   __shared__ float part[2][32];
-  const int cols = static_cast<int>(p.cols), step = blockDim.x * kVec;
-  const int c0 = static_cast<int>(threadIdx.x) * kVec;
-  float w[kNC][kVec], acc[kNC][kVec];
-#pragma unroll
-  for (int i = 0; i < kNC; ++i) {
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) w[i][j] = acc[i][j] = 0.0f;
-    if (c0 + i * step < cols) load_any<kVec>(p.weight, p.w_elem, c0 + i * step, w[i]);
-  }
+  const int cols = static_cast<int>(p.cols), step = blockDim.x * 8;
+  const int c0 = static_cast<int>(threadIdx.x) * 8 -
+                 (kShift ? static_cast<int>((blockIdx.x * p.cols) & 7) : 0);
+  const int64_t total = p.rows * p.cols;
   R dy[kNC], h[kNC], dh[kNC];
   float r = 0.0f;
   auto fetch = [&](int64_t row, R (&a)[kNC], R (&b)[kNC], R (&d)[kNC], float& rs) {
     rs = p.rstd[row];
 #pragma unroll
     for (int i = 0; i < kNC; ++i) {
-      a[i].zero();
-      b[i].zero();
-      d[i].zero();
       const int c = c0 + i * step;
-      if (c < cols) {
-        const int64_t at = row * p.cols + c;
-        a[i].load(p.dy, at);
-        b[i].load(p.h, at);
-        if (p.dh) d[i].load(p.dh, at);
-      }
+      const int64_t at = row * p.cols + c;
+      a[i].template load<kShift>(p.dy, at, c, cols, total);
+      b[i].template load<kShift>(p.h, at, c, cols, total);
+      d[i].template load<kShift>(p.dh, at, c, p.dh ? cols : -8, total);
     }
   };
   if (kAhead) fetch(blockIdx.x, dy, h, dh, r);
+  float w[kNC][8], acc[kNC][8];
+#pragma unroll
+  for (int i = 0; i < kNC; ++i) {
+    load_weight<kShift>(p.weight, p.w_elem, c0 + i * step, cols, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+  }
   int k = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++k) {
     R dy2[kNC], h2[kNC], dh2[kNC];
@@ -344,22 +449,25 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const BwdArgs p) {
     else if (row + gridDim.x < p.rows) fetch(row + gridDim.x, dy2, h2, dh2, r2);
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kNC; ++i)
+    for (int i = 0; i < kNC; ++i) {
+      dy[i].template trim<kShift>(c0 + i * step, cols);
+      h[i].template trim<kShift>(c0 + i * step, cols);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float g = dy[i].at(j), xh = h[i].at(j) * r;
-        dot += g * w[i][j] * xh;
-        acc[i][j] += g * xh;
+      for (int j = 0; j < 8; ++j) {
+        const float gx = dy[i].at(j) * (h[i].at(j) * r);
+        dot += gx * w[i][j];
+        acc[i][j] += gx;
       }
+    }
     // alternating buffers: the previous row's sums have been read by then
     const float mean = block_sum(dot, part[k & 1]) / static_cast<float>(cols);
 #pragma unroll
     for (int i = 0; i < kNC; ++i) {
-      float d[kVec];
+      float d[8];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
+      for (int j = 0; j < 8; ++j)
         d[j] = dh[i].at(j) + r * (dy[i].at(j) * w[i][j] - h[i].at(j) * r * mean);
-      if (c0 + i * step < cols) store_any<kVec>(p.dx, kElem, row * p.cols + c0 + i * step, d);
+      store_run<kShift>(p.dx, kElem, row * p.cols + c0 + i * step, c0 + i * step, cols, d);
     }
     if (kAhead) {
 #pragma unroll
@@ -374,94 +482,91 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const BwdArgs p) {
 #pragma unroll
   for (int i = 0; i < kNC; ++i) {
     const int c = c0 + i * step;
-    if (c >= cols) continue;
-    if (gridDim.x == 1) store_any<kVec>(p.dweight, p.w_elem, c, acc[i]);
-    else store_any<kVec>(p.partial, kElemF32, blockIdx.x * p.cols + c, acc[i]);
+    void* out = gridDim.x == 1 ? p.dweight : p.partial + blockIdx.x * p.cols;
+    const int elem = gridDim.x == 1 ? p.w_elem : kElemF32;
+    if constexpr (!kShift) {
+      if (c < cols) store_any<8>(out, elem, c, acc[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j >= 0 && c + j < cols) {
+          const float u[1] = {acc[i][j]};
+          store_any<1>(out, elem, c + j, u);
+        }
+    }
   }
 }
 
-// dw = the sum of the partial rows: 32 columns a CTA, eight warps that each
-// add every eighth row, and their eight sums in order.
-__global__ void __launch_bounds__(256)
+// dw = the sum of the partial rows: 32 columns a CTA, 32 warps that each add
+// every 32nd row (so that a thread has its ten loads or so in flight at once;
+// eight warps took 2 us longer), and their sums in a fixed order.
+__global__ void __launch_bounds__(1024)
 rmsnorm_dweight_kernel(const float* __restrict__ partial, int parts, int64_t cols,
                        void* __restrict__ dweight, int w_elem) {
-  __shared__ float sums[8][33];
+  __shared__ float sums[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial rows are written
   float s = 0.0f;
   if (c < cols) {
-#pragma unroll 8
-    for (int i = warp; i < parts; i += 8) s += partial[i * cols + c];
+#pragma unroll 10
+    for (int i = warp; i < parts; i += 32) s += partial[i * cols + c];
   }
   sums[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-    float v[1] = {0.0f};
+  // warp w adds up column w's 32 sums
+  float v[1] = {sums[lane][warp]};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[0] += sums[i][lane];
-    store_any<1>(dweight, w_elem, c, v);
-  }
+  for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  const int64_t cw = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && cw < cols) store_any<1>(dweight, w_elem, cw, v);
 }
 
-// Longest rows held in registers, and threads for n runs of them a thread.
-constexpr int64_t kFwdMaxCols = 32768, kFwdMaxOdd = 16384, kBwdMaxCols = 16384,
-                  kBwdMaxF32 = 8192, kBwdMaxOdd = 8192;
+// Runs of a row (of any length: wherever it starts), and threads for n each.
+int64_t runs_of(int64_t cols) { return cols % 8 == 0 ? cols / 8 : (cols + 14) / 8; }
+int threads_for(int64_t runs, int n) {
+  return static_cast<int>(((runs + n - 1) / n + 31) / 32 * 32);
+}
 
-int threads_for(int64_t cols, int vec, int nc, int most) {
-  const int64_t runs = (cols + vec * nc - 1) / (vec * nc);
-  return static_cast<int>(std::min<int64_t>(most, (runs + 31) / 32 * 32));
+// Whether rows are held in registers: up to 1024 threads of 4 runs (forward,
+// 2 with odd lengths, whose addresses cost registers) or 1 run (gradients; 4
+// in 512 threads for 16-bit types of even length).
+bool fwd_in_registers(int64_t cols) { return runs_of(cols) <= (cols % 8 == 0 ? 4096 : 2048); }
+bool bwd_in_registers(int64_t cols, int elem) {
+  return runs_of(cols) <= (cols % 8 == 0 && elem != kElemF32 ? 2048 : 1024);
 }
 
 template <int kX, int kRes>
 cudaError_t launch_fwd(const NormFwdCall& c, const FwdArgs& a) {
   const unsigned grid = static_cast<unsigned>(c.rows);
-  if (c.cols % 8 == 0 && c.cols <= kFwdMaxCols) {
-    // four runs a thread, whose loads are in flight together, in CTAs small
-    // enough that several rows share an SM. By the row's length alone: a row's
-    // sum, and with it the row's result, does not depend on how many rows the
-    // call has.
-    const int64_t runs = c.cols / 8;
-    if (runs <= 256)
-      rmsnorm_fwd_kernel<kX, kRes, 8, 2><<<grid, threads_for(c.cols, 8, 2, 1024), 0, c.st>>>(a);
-    else
-      rmsnorm_fwd_kernel<kX, kRes, 8, 4><<<grid, threads_for(c.cols, 8, 4, 1024), 0, c.st>>>(a);
-  } else if (c.cols % 8 != 0 && c.cols <= kFwdMaxOdd) {
-    if (c.cols <= 2048)
-      rmsnorm_fwd_kernel<kX, kRes, 1, 8><<<grid, threads_for(c.cols, 1, 8, 1024), 0, c.st>>>(a);
-    else
-      rmsnorm_fwd_kernel<kX, kRes, 1, 16><<<grid, threads_for(c.cols, 1, 16, 1024), 0, c.st>>>(a);
-  } else if (c.cols % 8 == 0) {
-    rmsnorm_fwd_long_kernel<8><<<grid, threads_for(c.cols, 8, 1, 512), 0, c.st>>>(a);
-  } else {
-    rmsnorm_fwd_long_kernel<1><<<grid, threads_for(c.cols, 1, 1, 512), 0, c.st>>>(a);
-  }
+  // four runs a thread, whose loads are in flight together, in CTAs small
+  // enough that several rows share an SM. By the row's length alone: a row's
+  // sum, and with it the row's result, does not depend on how many rows the
+  // call has.
+  const int64_t runs = runs_of(c.cols);
+  if (c.cols % 8 != 0)
+    rmsnorm_fwd_kernel<kX, kRes, true, 2><<<grid, threads_for(runs, 2), 0, c.st>>>(a);
+  else if (runs <= 256)
+    rmsnorm_fwd_kernel<kX, kRes, false, 2><<<grid, threads_for(runs, 2), 0, c.st>>>(a);
+  else
+    rmsnorm_fwd_kernel<kX, kRes, false, 4><<<grid, threads_for(runs, 4), 0, c.st>>>(a);
   return cudaGetLastError();
 }
 
-int64_t bwd_max_cols(int64_t cols, int elem) {
-  return cols % 8 != 0 ? kBwdMaxOdd : elem == kElemF32 ? kBwdMaxF32 : kBwdMaxCols;
-}
-
-template <int kElem>
+template <int kElem, bool kShift>
 cudaError_t launch_bwd(const NormBwdCall& c, const BwdArgs& a, unsigned parts) {
-  const int64_t most = bwd_max_cols(c.cols, kElem);
-  if (c.cols % 8 == 0 && c.cols <= most) {
-    if (c.cols <= 4096)
-      rmsnorm_bwd_kernel<kElem, 8, 1, true><<<parts, threads_for(c.cols, 8, 1, 512), 0, c.st>>>(a);
-    else if (c.cols <= 8192)
-      rmsnorm_bwd_kernel<kElem, 8, 2, kElem != kElemF32><<<parts, threads_for(c.cols, 8, 2, 512), 0, c.st>>>(a);
-    else if constexpr (kElem != kElemF32)
-      rmsnorm_bwd_kernel<kElem, 8, 4, false><<<parts, threads_for(c.cols, 8, 4, 512), 0, c.st>>>(a);
-  } else if (c.cols % 8 != 0 && c.cols <= most) {
-    if (c.cols <= 2048)
-      rmsnorm_bwd_kernel<kElem, 1, 8, true><<<parts, threads_for(c.cols, 1, 8, 512), 0, c.st>>>(a);
-    else
-      rmsnorm_bwd_kernel<kElem, 1, 16, false><<<parts, threads_for(c.cols, 1, 16, 512), 0, c.st>>>(a);
-  } else if (c.cols % 8 == 0) {
-    rmsnorm_bwd_long_kernel<8><<<parts, threads_for(c.cols, 8, 1, 512), 0, c.st>>>(a);
-  } else {
-    rmsnorm_bwd_long_kernel<1><<<parts, threads_for(c.cols, 1, 1, 512), 0, c.st>>>(a);
+  const int64_t runs = runs_of(c.cols);
+  if (!bwd_in_registers(c.cols, kElem)) {
+    rmsnorm_bwd_long_kernel<kShift ? 1 : 8><<<parts, 512, 0, c.st>>>(a);
+  } else if constexpr (kElem == kElemF32) {
+    // the next row on its way needs 32 more registers a thread than 1024
+    // threads can have
+    if (runs <= 640) rmsnorm_bwd_kernel<kElem, kShift, 1, true, 640><<<parts, threads_for(runs, 1), 0, c.st>>>(a);
+    else rmsnorm_bwd_kernel<kElem, kShift, 1, false, 1024><<<parts, threads_for(runs, 1), 0, c.st>>>(a);
+  } else if (runs <= 1024) {
+    rmsnorm_bwd_kernel<kElem, kShift, 1, true, 1024><<<parts, threads_for(runs, 1), 0, c.st>>>(a);
+  } else if constexpr (!kShift) {
+    rmsnorm_bwd_kernel<kElem, false, 4, false, 512><<<parts, threads_for(runs, 4), 0, c.st>>>(a);
   }
   return cudaGetLastError();
 }
@@ -471,6 +576,12 @@ cudaError_t launch_bwd(const NormBwdCall& c, const BwdArgs& a, unsigned parts) {
 cudaError_t launch_rmsnorm_fwd(const NormFwdCall& c) {
   const FwdArgs a = {c.x, c.residual, c.weight, c.h, c.y, c.scale, c.rstd, c.cols,
                      c.x_elem, c.h_elem, c.w_elem, c.y_elem, c.y_fp8 ? 1 : 0, c.eps};
+  if (!fwd_in_registers(c.cols)) {
+    const unsigned grid = static_cast<unsigned>(c.rows);
+    if (c.cols % 8 == 0) rmsnorm_fwd_long_kernel<8><<<grid, 512, 0, c.st>>>(a);
+    else rmsnorm_fwd_long_kernel<1><<<grid, 512, 0, c.st>>>(a);
+    return cudaGetLastError();
+  }
   const int res = !c.residual ? 0 : c.h_elem == c.x_elem ? 1 : 2;
   auto go = [&](auto x) {
     constexpr int kX = decltype(x)::value;
@@ -483,22 +594,28 @@ cudaError_t launch_rmsnorm_fwd(const NormFwdCall& c) {
   return go(std::integral_constant<int, kElemF16>{});
 }
 
-// Rows of the workspace, one per CTA of the backward: two CTAs an SM.
-int64_t rmsnorm_bwd_parts(int64_t rows, int64_t) { return std::min<int64_t>(rows, 304); }
+// Rows of the workspace, one per CTA of the backward: as many CTAs as run at
+// once (about 1024 threads an SM), a multiple of 8 (rmsnorm_bwd_kernel).
+int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols) {
+  return std::min<int64_t>(rows, cols <= 1024 ? 1216 : cols <= 2048 ? 608 : cols <= 4096 ? 304 : 152);
+}
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c) {
   const BwdArgs a = {c.dy, c.h, c.dh, c.weight, c.rstd, c.dx, c.dweight, c.partial, c.rows, c.cols,
                      c.elem, c.w_elem};
   const unsigned parts = static_cast<unsigned>(rmsnorm_bwd_parts(c.rows, c.cols));
-  const bool regs = c.cols <= bwd_max_cols(c.cols, c.elem);
-  const cudaError_t e = c.elem == kElemF32 ? launch_bwd<kElemF32>(c, a, parts)
-                        : c.elem == kElemBf16 ? launch_bwd<kElemBf16>(c, a, parts)
-                                              : launch_bwd<kElemF16>(c, a, parts);
-  if (e != cudaSuccess || (regs && parts == 1)) return e;
+  auto go = [&](auto elem) {
+    constexpr int kElem = decltype(elem)::value;
+    return c.cols % 8 == 0 ? launch_bwd<kElem, false>(c, a, parts) : launch_bwd<kElem, true>(c, a, parts);
+  };
+  const cudaError_t e = c.elem == kElemF32 ? go(std::integral_constant<int, kElemF32>{})
+                        : c.elem == kElemBf16 ? go(std::integral_constant<int, kElemBf16>{})
+                                              : go(std::integral_constant<int, kElemF16>{});
+  if (e != cudaSuccess || (parts == 1 && bwd_in_registers(c.cols, c.elem))) return e;
   // launched while the backward drains; it waits for the partial rows itself
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((c.cols + 31) / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.stream = c.st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
