@@ -426,7 +426,8 @@ def describe_site(site: int) -> str:
     """Readable form of a timeout site."""
     if site == 0:
         return "none"
-    kernel = {1: "small-M forward", 2: "tensor-core forward", 3: "tensor-core input gradient"}
+    kernel = {1: "small-M forward", 2: "tensor-core forward", 3: "tensor-core input gradient",
+              4: "8-bit forward", 5: "8-bit input gradient"}
     role = {1: "copy producer", 2: "MMA issuer", 3: "dequantizing warp", 4: "epilogue"}
     u = site & 0xffffffff
     return (f"{kernel.get(u >> 28, u >> 28)}, {role.get((u >> 24) & 15, (u >> 24) & 15)}, "

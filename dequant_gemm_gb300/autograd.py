@@ -12,12 +12,19 @@ types) and the returned gradient to the input's dtype. Every product runs in
 the library's kernels. Weights may be NF4, FP4 or int8 ("bitsandbytes", the
 4-bit paragraph: Linear4bit / LinearNF4 / LinearFP4 layers; "Zenbit",
 zenbit.int8 bullet).
+
+The second half of the module does the same for the 8-bit floating point
+products and the RMS norm in front of them. Rounding to 8 bits passes its
+gradient through; gradients of a product's output are rounded to 8 bits
+themselves (1 x 128 blocks) before they meet the weight.
 """
 from __future__ import annotations
 
 import torch
 
-from . import NF4Weight, nf4_matmul_bwd_dx, nf4_matmul_fwd, nf4_quantize
+from . import (FP8Tensor, NF4Weight, nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd,
+               nf4_fp8_quantize, nf4_matmul_bwd_dx, nf4_matmul_fwd, nf4_quantize,
+               nf4_rmsnorm_bwd, nf4_rmsnorm_fwd)
 
 
 class NF4LinearFunction(torch.autograd.Function):
@@ -92,3 +99,128 @@ class NF4Linear(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, out_features={self.out_features}, "
                 f"{self.qdtype}")
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """(y, h) with h = x + residual and y = h / rms(h) * weight, y of x's type.
+    Without a residual h is not returned (None)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual=None, eps=1e-6):
+        shape = x.shape
+        rows = x.reshape(-1, shape[-1]).contiguous()
+        res = None if residual is None else residual.reshape(rows.shape).contiguous()
+        y, h, rstd = nf4_rmsnorm_fwd(rows, weight, res, eps=eps, save_rstd=True)
+        ctx.save_for_backward(h, weight, rstd)
+        ctx.x_dtype = x.dtype
+        ctx.with_residual = residual is not None
+        return y.reshape(shape), (h.reshape(shape) if residual is not None else None)
+
+    @staticmethod
+    def backward(ctx, gy, gh):
+        h, weight, rstd = ctx.saved_tensors
+        flat = lambda g: None if g is None else g.reshape(h.shape).to(h.dtype).contiguous()  # noqa: E731
+        dx, dweight = nf4_rmsnorm_bwd(flat(gy), h, weight, rstd, dh=flat(gh))
+        dx = dx.reshape(gy.shape)
+        return dx.to(ctx.x_dtype), dweight, (dx if ctx.with_residual else None), None
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+             eps: float = 1e-6):
+    """Differentiable RMS norm with the residual's addition: (y, h), h None
+    without a residual."""
+    return RMSNormFunction.apply(x, weight, residual, eps)
+
+
+class FP8LinearFunction(torch.autograd.Function):
+    """y = x · value(weight)ᵀ, x [..., cols] (fp32, bf16 or fp16) rounded to 8
+    bits, y of `out_dtype` (fp32 or bf16); differentiable in x."""
+
+    @staticmethod
+    def forward(ctx, x, weight: FP8Tensor, out_dtype=torch.bfloat16):
+        ctx.weight, ctx.x_dtype, ctx.shape = weight, x.dtype, x.shape
+        q = nf4_fp8_quantize(x.reshape(-1, x.shape[-1]).contiguous())
+        return nf4_fp8_matmul_fwd(q, weight, out_dtype=out_dtype).reshape(*x.shape[:-1], weight.rows)
+
+    @staticmethod
+    def backward(ctx, gy):
+        if not ctx.needs_input_grad[0]:
+            return None, None, None
+        w = ctx.weight
+        q = nf4_fp8_quantize(gy.reshape(-1, w.rows).contiguous())
+        out = torch.bfloat16 if ctx.x_dtype == torch.bfloat16 else torch.float32
+        return nf4_fp8_matmul_bwd_dx(q, w, out_dtype=out).reshape(ctx.shape).to(ctx.x_dtype), None, None
+
+
+def fp8_linear(x: torch.Tensor, weight: FP8Tensor,
+               out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    return FP8LinearFunction.apply(x, weight, out_dtype)
+
+
+class NormFP8LinearsFunction(torch.autograd.Function):
+    """The norm and the products that read its output, joined: the norm writes
+    the 8-bit operand once for all weights. Returns (h, y_0, y_1, ...)."""
+
+    @staticmethod
+    def forward(ctx, x, norm_weight, residual, eps, out_dtype, *weights):
+        shape = x.shape
+        rows = x.reshape(-1, shape[-1]).contiguous()
+        res = None if residual is None else residual.reshape(rows.shape).contiguous()
+        q, h, rstd = nf4_rmsnorm_fwd(rows, norm_weight, res, eps=eps, out_dtype=torch.float8_e4m3fn,
+                                     save_rstd=True)
+        ctx.save_for_backward(h, norm_weight, rstd)
+        ctx.weights, ctx.x_dtype, ctx.shape = weights, x.dtype, shape
+        ctx.with_residual = residual is not None
+        ctx.set_materialize_grads(False)     # an output that nothing used costs no product
+        ys = [nf4_fp8_matmul_fwd(q, w, out_dtype=out_dtype).reshape(*shape[:-1], w.rows)
+              for w in weights]
+        if residual is None:
+            h = h.clone()            # an output may not be the input itself
+        return (h.reshape(shape), *ys)
+
+    @staticmethod
+    def backward(ctx, gh, *gys):
+        h, norm_weight, rstd = ctx.saved_tensors
+        dy = None                    # the products' input gradients, summed in fp32
+        for w, g in zip(ctx.weights, gys):
+            if g is not None:
+                q = nf4_fp8_quantize(g.reshape(-1, w.rows).contiguous())
+                dy = nf4_fp8_matmul_bwd_dx(q, w, out=dy, accumulate=dy is not None)
+        dy = torch.zeros_like(h) if dy is None else dy.to(h.dtype)
+        dh = None if gh is None else gh.reshape(h.shape).to(h.dtype).contiguous()
+        dx, dweight = nf4_rmsnorm_bwd(dy, h, norm_weight, rstd, dh=dh)
+        dx = dx.reshape(ctx.shape)
+        return (dx.to(ctx.x_dtype), dweight, dx if ctx.with_residual else None, None, None,
+                *[None] * len(ctx.weights))
+
+
+def norm_fp8_linears(x: torch.Tensor, norm_weight: torch.Tensor, weights, residual=None,
+                     eps: float = 1e-6, out_dtype: torch.dtype = torch.bfloat16):
+    """h = x + residual and, for each 8-bit weight, rms_norm(h) · value(weight)ᵀ:
+    (h, [y, ...]). Differentiable in x, the residual and the norm's weight."""
+    h, *ys = NormFP8LinearsFunction.apply(x, norm_weight, residual, eps, out_dtype, *weights)
+    return h, ys
+
+
+class FP8Linear(torch.nn.Module):
+    """A frozen linear layer (no bias) holding its weight in 8 bits, with a
+    scale for each 128 x 128 block. Codes and scales are buffers."""
+
+    def __init__(self, weight: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16):
+        super().__init__()
+        if weight.dim() != 2:
+            raise ValueError("weight must be 2-D [out_features, in_features]")
+        q = nf4_fp8_quantize(weight.detach().contiguous(), block_rows=128)
+        self.register_buffer("codes", q.codes)
+        self.register_buffer("scale", q.scale)
+        self.out_features, self.in_features = q.rows, q.cols
+        self.out_dtype = out_dtype
+
+    def quantized_weight(self) -> FP8Tensor:
+        return FP8Tensor(self.codes, self.scale, 128)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return fp8_linear(x, self.quantized_weight(), self.out_dtype)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, fp8"

@@ -367,6 +367,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         arrive_on_copies(sfull_bar(ch & 1));
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // also after an abort
    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairManyRegs));
@@ -673,6 +674,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (warp == 2 && lane < 16) copy4(dst + 4 * kBT, ws + i * p.ws_red, n > 0);
       arrive_on_copies(sfull_bar(ch & 1));
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // also after an abort
   } else {
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::kCols * part;

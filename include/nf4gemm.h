@@ -345,7 +345,8 @@ nf4_status nf4_poll_device_status(void* stream);
 /* As nf4_poll_device_status, and if `site` is not NULL it receives where the
  * first timeout since the last poll happened (0 when there was none):
  *   bits 28-31  kernel: 1 small-M forward, 2 tensor-core forward,
- *               3 tensor-core input gradient
+ *               3 tensor-core input gradient, 4 8-bit forward, 5 8-bit
+ *               input gradient
  *   bits 24-27  role: 1 copy producer, 2 MMA issuer, 3 dequantizing /
  *               computing warp, 4 epilogue
  *   bits  0-23  linear index of the CTA within its grid (low 24 bits).
@@ -362,7 +363,7 @@ nf4_status nf4_codebook(float* out16);
 nf4_status nf4_codebook_of(int32_t dtype, float* out16);
 
 /* Diagnostic, for testing the timeout path: from the next launch on, the
- * tensor-core kernels' MMA issuer gives up waiting for a dequantized stage
+ * tensor-core kernels' MMA issuer gives up waiting for a stage's operands
  * after `cycles` clock cycles (<= 0 restores the default of about a second)
  * and the kernel takes its abort path: it records NF4_ERR_DEVICE_TIMEOUT
  * with its site, lets its copies and MMAs in flight finish, frees its
