@@ -237,6 +237,7 @@ nf4_status fp8_matmul(bool dx, const nf4_fp8_tensor* a, const nf4_fp8_tensor* w,
   if ((flags & ~NF4_ACCUMULATE) != 0) return NF4_ERR_SHAPE;
   const int64_t red = dx ? w->rows : w->cols, out_cols = dx ? w->cols : w->rows;
   if ((w->rows % 16) != 0 || a->cols != red) return NF4_ERR_SHAPE;
+  if (a->rows > INT32_MAX || w->rows > INT32_MAX || w->cols > INT32_MAX) return NF4_ERR_SHAPE;
   if (a->rows == 0 || out_cols == 0) return NF4_OK;
   if (!out) return NF4_ERR_NULL;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -929,16 +929,21 @@ cudaError_t launch_any(const Fp8Call& c) {
   a.accumulate = c.accumulate;
   a.mma_wait_limit = c.wait_limit;
   a.status = c.status;
-  if (c.M <= 16) return launch_rows<kDx, 16>(c, a, red);
-  if (c.M <= 32) return launch_rows<kDx, 32>(c, a, red);
-  if (c.M <= 64) return launch_rows<kDx, 64>(c, a, red);
-  if (c.M <= 128) return launch_rows<kDx, 128>(c, a, red);
-  // more tokens: pairs, unless their tiles leave most SMs idle for a long
-  // reduction, which the rows kernel splits (512 x 3584 forward at 250 tokens
-  // 16.2 us on pairs, 7.8 in rows; 4096 x 4096 at 512 tokens 18.8 and 20.4)
-  const int64_t units = (c.M + 255) / 256 * ((a.cols + kPairBN - 1) / kPairBN);
-  const int64_t rounds = (units + c.num_sms / 2 - 1) / std::max(1, c.num_sms / 2);
-  if (plan_rows<kDx, 128>(c, a).cost < rounds * (a.rb * 39 + 100)) return launch_rows<kDx, 128>(c, a, red);
+  // the rows kernel's tiles are grid dimensions of at most 65535
+  constexpr int64_t kMostTiles = 65535;
+  if ((a.cols + 127) / 128 <= kMostTiles && (c.M + 127) / 128 <= kMostTiles) {
+    if (c.M <= 16) return launch_rows<kDx, 16>(c, a, red);
+    if (c.M <= 32) return launch_rows<kDx, 32>(c, a, red);
+    if (c.M <= 64) return launch_rows<kDx, 64>(c, a, red);
+    if (c.M <= 128) return launch_rows<kDx, 128>(c, a, red);
+    // more tokens: pairs, unless their tiles leave most SMs idle for a long
+    // reduction, which the rows kernel splits (512 x 3584 forward at 250
+    // tokens 16.2 us on pairs, 7.8 in rows; 4096 x 4096 at 512 tokens 18.8 and
+    // 20.4). Pairs: 0.39 us a block, 1 us a tile.
+    const int64_t units = (c.M + 255) / 256 * ((a.cols + kPairBN - 1) / kPairBN);
+    const int64_t rounds = (units + c.num_sms / 2 - 1) / std::max(1, c.num_sms / 2);
+    if (plan_rows<kDx, 128>(c, a).cost < rounds * (a.rb * 39 + 100)) return launch_rows<kDx, 128>(c, a, red);
+  }
   return launch_pair<kDx>(c, a, red);
 }
 

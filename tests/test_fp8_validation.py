@@ -100,6 +100,7 @@ def test_c_abi_validates_products():
     assert f(ctypes.byref(_t(rows=4, cols=128, block_rows=1)), w, P, 0, 0, None) == 2
     assert f(ctypes.byref(_t(rows=-1, block_rows=1)), w, P, 0, 0, None) == 2
     assert d(a, w, P, 0, 0, None) == 2
+    assert f(ctypes.byref(_t(rows=1 << 31, block_rows=1)), w, P, 0, 0, None) == 2
     assert f(a, w, P + 4, 0, 0, None) == 3
     assert f(ctypes.byref(_t(codes=P + 8, rows=4, block_rows=1)), w, P, 0, 0, None) == 3
     assert f(ctypes.byref(_t(scale=P + 2, rows=4, block_rows=1)), w, P, 0, 0, None) == 3
