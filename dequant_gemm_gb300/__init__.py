@@ -149,13 +149,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call_on(device: torch.device, fn, *args) -> int:
-    """fn(*args, stream) with `device` current; no switch where it already is."""
-    index = device.index
+def _call_on(index: int, name: str, *args):
+    """The library's `name`(*args, stream) with device `index` current (no
+    switch where it already is); raises on a non-OK status."""
+    fn = getattr(_lib or lib(), name)
     if index == _raw_device():
-        return fn(*args, _raw_stream(index))
-    with torch.cuda.device(device):
-        return fn(*args, _raw_stream(torch.cuda.current_device()))
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != 0:
+        raise NF4Error(name, status)
 
 
 @dataclass

@@ -15,11 +15,14 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (ACCUMULATE, ELEM, _call_on, _check, _require, _require_cuda_device, _same_device,
-               lib, nf4_fp8_tensor)
+from . import (ACCUMULATE, ELEM, _call_on, _require, _require_cuda_device, _same_device,
+               nf4_fp8_tensor)
 
 FP8_BLOCK = 128
 FP8_DTYPE = torch.float8_e4m3fn
+_F32 = torch.float32
+_OUT = {torch.float32: ELEM[torch.float32], torch.bfloat16: ELEM[torch.bfloat16]}
+_empty, _byref = torch.empty, ctypes.byref
 
 
 @dataclass(slots=True)
@@ -61,21 +64,6 @@ def _check_block_rows(block_rows: int):
         raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
 
 
-def _fp8_ok(t: FP8Tensor, block_rows: int, device: torch.device) -> bool:
-    """The whole check of one block-scaled tensor in one pass, without naming
-    what is wrong with it (a call's host time is mostly such lookups)."""
-    try:
-        codes, scale = t.codes, t.scale
-        rows, cols = codes.shape
-        return (type(t) is FP8Tensor and t.block_rows == block_rows
-                and codes.dtype is FP8_DTYPE and scale.dtype is torch.float32
-                and codes.is_contiguous() and scale.is_contiguous() and cols % 16 == 0
-                and scale.shape == (-(-rows // block_rows), -(-cols // FP8_BLOCK))
-                and codes.device == device and scale.device == device)
-    except (AttributeError, TypeError, ValueError):
-        return False
-
-
 def _check_fp8(t: FP8Tensor, name: str, device: torch.device):
     """Types, exact sizes, contiguity and device of one block-scaled tensor."""
     if not isinstance(t, FP8Tensor):
@@ -105,23 +93,28 @@ def nf4_fp8_quantize(x: torch.Tensor, block_rows: int = 1,
     in 128 x 128 blocks (weights)."""
     if not isinstance(x, torch.Tensor) or x.dtype not in ELEM:
         raise ValueError(f"x must be float32, bfloat16 or float16, got {getattr(x, 'dtype', type(x))}")
-    _require(x, "x", x.dtype)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if x.dim() != 2:
         raise ValueError("x must be 2-D [rows, cols]")
     _check_block_rows(block_rows)
     rows, cols = x.shape
     if cols % 16:
         raise ValueError(f"cols = {cols} is not a multiple of 16")
+    device = x.device
     if out is not None:
-        _check_fp8(out, "out", x.device)
+        _check_fp8(out, "out", device)
         if out.codes.shape != x.shape or out.block_rows != block_rows:
             raise ValueError(f"out holds a {out.rows}x{out.cols} tensor in blocks of "
                              f"{out.block_rows} rows, asked for {rows}x{cols} and {block_rows}")
-    _require_cuda_device(x.device)
-    q = out if out is not None else alloc_fp8(rows, cols, x.device, block_rows)
-    _check("nf4_fp8_quantize",
-           _call_on(x.device, lib().nf4_fp8_quantize, x.data_ptr(), ELEM[x.dtype], rows, cols,
-                    block_rows, q.codes.data_ptr(), q.scale.data_ptr()))
+    _require_cuda_device(device)
+    q = out
+    if q is None:
+        q = FP8Tensor(_empty((rows, cols), dtype=FP8_DTYPE, device=device),
+                      _empty((-(-rows // block_rows), -(-cols // FP8_BLOCK)), dtype=_F32, device=device),
+                      block_rows)
+    _call_on(device.index, "nf4_fp8_quantize", x.data_ptr(), ELEM[x.dtype], rows, cols, block_rows,
+             q.codes.data_ptr(), q.scale.data_ptr())
     return q
 
 
@@ -141,9 +134,7 @@ def nf4_fp8_dequantize(q: FP8Tensor, out: torch.Tensor | None = None,
         _same_device(q.device, out=out)
     _require_cuda_device(q.device)
     y = out if out is not None else torch.empty(q.codes.shape, dtype=out_dtype, device=q.device)
-    _check("nf4_fp8_dequantize",
-           _call_on(q.device, lib().nf4_fp8_dequantize, ctypes.byref(q.c_struct()), y.data_ptr(),
-                    ELEM[out_dtype]))
+    _call_on(q.device.index, "nf4_fp8_dequantize", _byref(q.c_struct()), y.data_ptr(), ELEM[out_dtype])
     return y
 
 
@@ -163,33 +154,50 @@ def _check_matmul(name: str, a: FP8Tensor, w: FP8Tensor, dx: bool, device):
 
 def _matmul(name: str, fn: str, a: FP8Tensor, w: FP8Tensor, dx: bool, out, out_dtype,
             accumulate: bool) -> torch.Tensor:
-    codes = getattr(a, "codes", None)
-    device = codes.device if isinstance(codes, torch.Tensor) else None
-    if not (_fp8_ok(a, 1, device) and _fp8_ok(w, FP8_BLOCK, device)):
-        _check_matmul(name, a, w, dx, device)
-    M, red = codes.shape
-    rows, cols = w.codes.shape
-    if rows % 16 or red != (rows if dx else cols):
+    # Everything that _check_matmul and the checks of `out` would refuse, in one
+    # pass that does not say what it is: a small call's host time is mostly
+    # such lookups.
+    try:
+        ac, ascale, wc, wscale = a.codes, a.scale, w.codes, w.scale
+        (M, red), (rows, cols) = ac.shape, wc.shape
+        device = ac.device
+        row_blocks, col_blocks = (rows + 127) // FP8_BLOCK, (cols + 127) // FP8_BLOCK
+        ok = (type(a) is FP8Tensor and type(w) is FP8Tensor and a.block_rows == 1
+              and w.block_rows == FP8_BLOCK and red == (rows if dx else cols)
+              and rows % 16 == 0 and cols % 16 == 0 and device.type == "cuda"
+              and ac.dtype is FP8_DTYPE and wc.dtype is FP8_DTYPE
+              and ascale.dtype is _F32 and wscale.dtype is _F32
+              and ascale.shape == (M, row_blocks if dx else col_blocks)
+              and wscale.shape == (row_blocks, col_blocks)
+              and ac.is_contiguous() and wc.is_contiguous()
+              and ascale.is_contiguous() and wscale.is_contiguous()
+              and ascale.device == device and wc.device == device and wscale.device == device)
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        codes = getattr(a, "codes", None)
+        device = codes.device if isinstance(codes, torch.Tensor) else None
         _check_matmul(name, a, w, dx, device)
     shape = (M, cols if dx else rows)
     if out is not None:
         if not isinstance(out, torch.Tensor):
             raise ValueError("out must be a tensor")
         out_dtype = out.dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
+    elem = _OUT.get(out_dtype)
+    if elem is None:
         raise ValueError(f"the output must be float32 or bfloat16, got {out_dtype}")
     if out is not None:
         _require(out, "out", out_dtype, shape=shape)
         _same_device(device, out=out)
     elif accumulate:
         raise ValueError("accumulate=True needs the output tensor to add to (out=)")
-    _require_cuda_device(device)
-    y = out if out is not None else torch.empty(shape, dtype=out_dtype, device=device)
-    _check(fn, _call_on(
-        device, getattr(lib(), fn),
-        ctypes.byref(nf4_fp8_tensor(codes.data_ptr(), a.scale.data_ptr(), M, red, 1)),
-        ctypes.byref(nf4_fp8_tensor(w.codes.data_ptr(), w.scale.data_ptr(), rows, cols, FP8_BLOCK)),
-        y.data_ptr(), ELEM[out_dtype], ACCUMULATE if accumulate else 0))
+    if not ok:
+        _require_cuda_device(device)
+    y = _empty(shape, dtype=out_dtype, device=device) if out is None else out
+    _call_on(device.index, fn,
+             _byref(nf4_fp8_tensor(ac.data_ptr(), ascale.data_ptr(), M, red, 1)),
+             _byref(nf4_fp8_tensor(wc.data_ptr(), wscale.data_ptr(), rows, cols, FP8_BLOCK)),
+             y.data_ptr(), elem, ACCUMULATE if accumulate else 0)
     return y
 
 

@@ -4,8 +4,11 @@ from __future__ import annotations
 
 import torch
 
-from . import (ELEM, _call_on, _check, _require, _require_cuda_device, _same_device, lib)
+from . import (ELEM, _call_on, _require, _require_cuda_device, _same_device, lib)
 from .fp8 import FP8_BLOCK, FP8_DTYPE, FP8Tensor
+
+
+_F32, _empty = torch.float32, torch.empty
 
 
 def _require_matrix(t, name: str, shape=None):
@@ -84,21 +87,21 @@ def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
     device = x.device
     _require_cuda_device(device)
     h = x
+    res_ptr = h_ptr = None
     if residual is not None:
-        h = out_h if out_h is not None else torch.empty_like(residual)
-    rstd = torch.empty(rows, dtype=torch.float32, device=device) if save_rstd else None
+        h = torch.empty_like(residual) if out_h is None else out_h
+        res_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
+    rstd = _empty(rows, dtype=_F32, device=device) if save_rstd else None
     if fp8:
-        y = FP8Tensor(torch.empty((rows, cols), dtype=FP8_DTYPE, device=device),
-                      torch.empty((rows, -(-cols // FP8_BLOCK)), dtype=torch.float32, device=device))
-        y_ptr, y_elem, scale = y.codes.data_ptr(), 0, y.scale.data_ptr()
+        codes = _empty((rows, cols), dtype=FP8_DTYPE, device=device)
+        scale = _empty((rows, -(-cols // FP8_BLOCK)), dtype=_F32, device=device)
+        y, y_ptr, y_elem, scale_ptr = FP8Tensor(codes, scale), codes.data_ptr(), 0, scale.data_ptr()
     else:
-        y = torch.empty((rows, cols), dtype=out_dtype, device=device)
-        y_ptr, y_elem, scale = y.data_ptr(), ELEM[out_dtype], None
-    _check("nf4_rmsnorm_fwd", _call_on(
-        device, lib().nf4_rmsnorm_fwd, x.data_ptr(), ELEM[x.dtype],
-        None if residual is None else residual.data_ptr(), ELEM[h.dtype], weight.data_ptr(),
-        ELEM[weight.dtype], rows, cols, eps, None if residual is None else h.data_ptr(), y_ptr,
-        y_elem, scale, None if rstd is None else rstd.data_ptr()))
+        y = _empty((rows, cols), dtype=out_dtype, device=device)
+        y_ptr, y_elem, scale_ptr = y.data_ptr(), ELEM[out_dtype], None
+    _call_on(device.index, "nf4_rmsnorm_fwd", x.data_ptr(), ELEM[x.dtype], res_ptr, ELEM[h.dtype],
+             weight.data_ptr(), ELEM[weight.dtype], rows, cols, eps, h_ptr, y_ptr, y_elem, scale_ptr,
+             None if rstd is None else rstd.data_ptr())
     return y, h, rstd
 
 
@@ -123,13 +126,11 @@ def nf4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rst
         _same_device(h.device, rstd=rstd)
     device = h.device
     _require_cuda_device(device)
-    L = lib()
     dx, dweight = torch.empty_like(h), torch.empty_like(weight)
-    size = L.nf4_rmsnorm_bwd_workspace(rows, cols)
-    work = torch.empty(size, dtype=torch.uint8, device=device)
-    _check("nf4_rmsnorm_bwd", _call_on(
-        device, L.nf4_rmsnorm_bwd, dy.data_ptr(), h.data_ptr(),
-        None if dh is None else dh.data_ptr(), ELEM[h.dtype], weight.data_ptr(),
-        ELEM[weight.dtype], rstd.data_ptr(), rows, cols, dx.data_ptr(), dweight.data_ptr(),
-        work.data_ptr(), size))
+    size = lib().nf4_rmsnorm_bwd_workspace(rows, cols)
+    work = _empty(size, dtype=torch.uint8, device=device)
+    _call_on(device.index, "nf4_rmsnorm_bwd", dy.data_ptr(), h.data_ptr(),
+             None if dh is None else dh.data_ptr(), ELEM[h.dtype], weight.data_ptr(),
+             ELEM[weight.dtype], rstd.data_ptr(), rows, cols, dx.data_ptr(), dweight.data_ptr(),
+             work.data_ptr(), size)
     return dx, dweight
