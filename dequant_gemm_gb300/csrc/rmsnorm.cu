@@ -497,29 +497,35 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_bwd_kernel(const BwdArgs 
   }
 }
 
-// dw = the sum of the partial rows: 32 columns a CTA, 32 warps that each add
-// every 32nd row (so that a thread has its ten loads or so in flight at once;
-// eight warps took 2 us longer), and their sums in a fixed order.
-__global__ void __launch_bounds__(1024)
+// dw = the sum of the partial rows: 8 columns (a 32-byte sector of each row) a
+// CTA, 64 threads a column, so that a thread has its few loads in flight at
+// once and the loads of all columns fill the GPU; their sums in a fixed order.
+// (32 columns of 32 threads each: 300 x 1001 8.3 us in all against 7.2 now, 4096 x
+// 3584 25.7 against 24.8.)
+constexpr int kSumThreads = 512;
+
+__global__ void __launch_bounds__(kSumThreads)
 rmsnorm_dweight_kernel(const float* __restrict__ partial, int parts, int64_t cols,
                        void* __restrict__ dweight, int w_elem) {
-  __shared__ float sums[32][33];
+  __shared__ float sums[kSumThreads / 32][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (lane & 7);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial rows are written
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 10
-    for (int i = warp; i < parts; i += 32) s += partial[i * cols + c];
+    for (int i = threadIdx.x >> 3; i < parts; i += kSumThreads / 8) s += partial[i * cols + c];
   }
-  sums[warp][lane] = s;
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if (lane < 8) sums[warp][lane] = s;
   __syncthreads();
-  // warp w adds up column w's 32 sums
-  float v[1] = {sums[lane][warp]};
+  if (threadIdx.x < 8 && c < cols) {
+    float v[1] = {0.0f};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-  const int64_t cw = static_cast<int64_t>(blockIdx.x) * 32 + warp;
-  if (lane == 0 && cw < cols) store_any<1>(dweight, w_elem, cw, v);
+    for (int i = 0; i < kSumThreads / 32; ++i) v[0] += sums[i][threadIdx.x];
+    store_any<1>(dweight, w_elem, c, v);
+  }
 }
 
 // Runs of a row (of any length: wherever it starts), and threads for n each.
@@ -614,8 +620,8 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c) {
   if (e != cudaSuccess || (parts == 1 && bwd_in_registers(c.cols, c.elem))) return e;
   // launched while the backward drains; it waits for the partial rows itself
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((c.cols + 31) / 32));
-  cfg.blockDim = dim3(1024);
+  cfg.gridDim = dim3(static_cast<unsigned>((c.cols + 7) / 8));
+  cfg.blockDim = dim3(kSumThreads);
   cfg.stream = c.st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
