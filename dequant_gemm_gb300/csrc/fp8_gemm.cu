@@ -105,13 +105,10 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// acc += s * v, two at a time. Volatile, so that the additions stay where they
-// are written, between the issue of one tensor-memory load and the wait for
-// it: the compiler otherwise gathers them behind the last wait.
-template <int kN>
-__device__ __forceinline__ void scale_add(float* acc, const float (&v)[kN], float s) {
+// acc += s * v, two at a time.
+__device__ __forceinline__ void scale_add(float* acc, const float (&v)[16], float s) {
 #pragma unroll
-  for (int j = 0; j < kN; j += 2)
+  for (int j = 0; j < 16; j += 2)
     asm volatile(
         "{\n\t.reg .b64 a, b, c;\n\t"
         "mov.b64 a, {%2, %3};\n\t"
@@ -154,6 +151,13 @@ struct MatmulArgs {
 // of 168: the first four warps give theirs up.
 // Persistent: a pair takes the tiles c, c + G, ... in turn, tokens fastest,
 // and the copies and MMAs of the next tile start while one is written out.
+//
+// Measured: 4096 x 11008 x 4096 forward 153 us (2.4 PFLOP/s), 2048 x 4096 x
+// 11008 gradient 81 us, at the board's power limit (1376 W, 1950 MHz). A block
+// takes ~850 cycles against 512 of MMA: two buffers, each of which goes
+// through its MMAs, the commit, the totals warps' reads (~400 cycles) and the
+// hand-back across the pair. Tensor memory has room for no third buffer, and
+// narrower tiles re-read operand A from shared memory (N = 128: 168 us).
 constexpr int kPairStages = 4;
 constexpr int kPairBN = 256;
 constexpr int kTileBytes = 128 * 128;                  // 128 rows of one block
@@ -236,97 +240,31 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   auto tile_c = [&](int u) { return static_cast<int64_t>(u / p.m_units) * kPairBN; };
 
   if (warp < 4) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFewRegs));
-   if (warp == 0) {
-    // The whole warp runs the loops of warps 0 and 1 on uniform values and one
-    // elected lane issues, as in the 16-bit kernel.
-    int gs = 0, slot = 0;
-    uint32_t ph = 0;
-    bool stop = false;
-    for (int u = cid; u < p.units && !stop; u += ncl) {
-      const int32_t m = static_cast<int32_t>(tile_m(u));
-      const int32_t c = static_cast<int32_t>(tile_c(u)) + static_cast<int32_t>(rank) * 128;
-      for (int i = 0; i < p.rb; ++i, ++gs) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) { stop = true; break; }
-        int r = tc::mbar_wait_abortable(empty_bar(slot), ph ^ 1, abort_flag);
-        r = __shfl_sync(0xffffffffu, r, 0);
-        if (r != tc::kWaitDone) {
-          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleProducer);
-          stop = true;
-          break;
-        }
-        const uint32_t dst = base + slot * kPairStageBytes;
-        if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(full_bar(slot), kPairStageBytes);
-          tc::tma_load_2d(dst, &tm_a, i * 128, m, full_bar(slot));
-          if (kDx) tc::tma_load_2d(dst + kTileBytes, &tm_w, c, i * 128, full_bar(slot));
-          else tc::tma_load_2d(dst + kTileBytes, &tm_w, i * 128, c, full_bar(slot));
-        }
-        __syncwarp();
-        if (++slot == kPairStages) {
-          slot = 0;
-          ph ^= 1u;
-        }
-      }
-    }
-    // copies in flight after an abort land before the CTA exits: the even
-    // CTA's barrier also counts the peer's arrival, which may not come any more
-    // (then the wait runs to its limit)
-    if (*abort_flag && lane == 0)
-      for (int g = max(0, gs - kPairStages); g < gs; ++g)
-        tc::mbar_wait(full_bar(g % kPairStages), (g / kPairStages) & 1, 1ll << 24);
-   } else if (warp == 1) {
-    int slot = 0;
-    uint32_t ph = 0;
-    bool stop = false;
-    if (rank != 0) {
-      for (int u = cid; u < p.units && !stop; u += ncl)
-        for (int i = 0; i < p.rb; ++i) {
-          int r = tc::mbar_wait_abortable(full_bar(slot), ph, abort_flag);
-          r = __shfl_sync(0xffffffffu, r, 0);
-          if (r != tc::kWaitDone) {
-            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
-            stop = true;
-            break;
-          }
-          if (tc::elect_one()) tc::mbar_arrive_remote(tc::mapa(full_bar(slot), 0));
-          __syncwarp();
-          if (++slot == kPairStages) {
-            slot = 0;
-            ph ^= 1u;
-          }
-        }
-    } else {
-      const uint32_t idesc = idesc_f8_f32(256, kPairBN, false, kDx);
-      const uint64_t adesc0 = tc::sw128_kmajor_desc(base);
-      // input gradient: the weight tile's rows are the reduction, 128 columns
-      // (one swizzled atom wide) each, 8-row groups 1 KB apart
-      const uint64_t bdesc0 = kDx ? tc::sw128_mnmajor_desc(base + kTileBytes, 0, 1024)
-                                  : tc::sw128_kmajor_desc(base + kTileBytes);
-      constexpr uint32_t kBStep = kDx ? 32 * 128 / 16 : 2;   // 32 of the reduction
-      int g = 0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFewRegs));
+    if (warp == 0) {
+      // The whole warp runs the loops of warps 0 and 1 on uniform values and one
+      // elected lane issues, as in the 16-bit kernel.
+      int gs = 0, slot = 0;
+      uint32_t ph = 0;
+      bool stop = false;
       for (int u = cid; u < p.units && !stop; u += ncl) {
-        for (int i = 0; i < p.rb; ++i, ++g) {
-          const int b = g & 1;
-          // the operands first: the buffer is the one that is waited for
-          int r = tc::mbar_spin_abortable<true>(full_bar(slot), ph, abort_flag, p.mma_wait_limit);
-          if (r == tc::kWaitDone)
-            r = tc::mbar_spin_abortable<true>(read_bar(b), ((g >> 1) & 1) ^ 1, abort_flag, 1ll << 31);
+        const int32_t m = static_cast<int32_t>(tile_m(u));
+        const int32_t c = static_cast<int32_t>(tile_c(u)) + static_cast<int32_t>(rank) * 128;
+        for (int i = 0; i < p.rb; ++i, ++gs) {
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) { stop = true; break; }
+          int r = tc::mbar_wait_abortable(empty_bar(slot), ph ^ 1, abort_flag);
           r = __shfl_sync(0xffffffffu, r, 0);
           if (r != tc::kWaitDone) {
-            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
+            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleProducer);
             stop = true;
             break;
           }
-          tc::fence_after_sync();
-          const uint64_t off = static_cast<uint64_t>(slot * (kPairStageBytes >> 4));
+          const uint32_t dst = base + slot * kPairStageBytes;
           if (tc::elect_one()) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_f8_ss<2>(tmem + 256u * b, adesc0 + off + 2u * j, bdesc0 + off + kBStep * j, idesc,
-                           j != 0 ? 1u : 0u);
-            tc::mma_commit<2>(empty_bar(slot));
-            tc::mma_commit<2>(sum_bar(b));
+            tc::mbar_arrive_expect_tx(full_bar(slot), kPairStageBytes);
+            tc::tma_load_2d(dst, &tm_a, i * 128, m, full_bar(slot));
+            if (kDx) tc::tma_load_2d(dst + kTileBytes, &tm_w, c, i * 128, full_bar(slot));
+            else tc::tma_load_2d(dst + kTileBytes, &tm_w, i * 128, c, full_bar(slot));
           }
           __syncwarp();
           if (++slot == kPairStages) {
@@ -335,40 +273,106 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
       }
-      if (tc::elect_one()) tc::mma_commit<2>(drain_bar);
-      __syncwarp();
-      if (lane == 0 && !tc::mbar_wait(drain_bar, 0)) fail(kRoleMma);
-    }
-   } else {
-    // lane: block j of two tokens a step, one token a half-warp
-    const int j = lane & 15, t0 = 2 * (warp - 2) + (lane >> 4);
-    int ch = 0;
-    bool stop = false;
-    for (int u = cid; u < p.units && !stop; u += ncl) {
-      const int64_t m0 = tile_m(u), cb = tile_c(u) / 128 + (lane >> 4);
-      const int tokens = static_cast<int>(min(p.M - m0, static_cast<int64_t>(128)));
-      const float* src = p.a_scale + (m0 + t0) * p.rb + j;
-      const float* wsrc = p.w_scale + cb * p.ws_col + j * p.ws_red;
-      const bool w_in = cb < col_blocks;
-      for (int i = 0; i < p.rb; i += kScaleChunk, ++ch) {
-        int r = tc::mbar_wait_abortable(sempty_bar(ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag);
-        r = __shfl_sync(0xffffffffu, r, 0);
-        if (r != tc::kWaitDone) {
-          if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleProducer);
-          stop = true;
-          break;
+      // copies in flight after an abort land before the CTA exits: the even
+      // CTA's barrier also counts the peer's arrival, which may not come any more
+      // (then the wait runs to its limit)
+      if (*abort_flag && lane == 0)
+        for (int g = max(0, gs - kPairStages); g < gs; ++g)
+          tc::mbar_wait(full_bar(g % kPairStages), (g / kPairStages) & 1, 1ll << 24);
+    } else if (warp == 1) {
+      int slot = 0;
+      uint32_t ph = 0;
+      bool stop = false;
+      if (rank != 0) {
+        for (int u = cid; u < p.units && !stop; u += ncl)
+          for (int i = 0; i < p.rb; ++i) {
+            int r = tc::mbar_wait_abortable(full_bar(slot), ph, abort_flag);
+            r = __shfl_sync(0xffffffffu, r, 0);
+            if (r != tc::kWaitDone) {
+              if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
+              stop = true;
+              break;
+            }
+            if (tc::elect_one()) tc::mbar_arrive_remote(tc::mapa(full_bar(slot), 0));
+            __syncwarp();
+            if (++slot == kPairStages) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
+      } else {
+        const uint32_t idesc = idesc_f8_f32(256, kPairBN, false, kDx);
+        const uint64_t adesc0 = tc::sw128_kmajor_desc(base);
+        // input gradient: the weight tile's rows are the reduction, 128 columns
+        // (one swizzled atom wide) each, 8-row groups 1 KB apart
+        const uint64_t bdesc0 = kDx ? tc::sw128_mnmajor_desc(base + kTileBytes, 0, 1024)
+                                    : tc::sw128_kmajor_desc(base + kTileBytes);
+        constexpr uint32_t kBStep = kDx ? 32 * 128 / 16 : 2;   // 32 of the reduction
+        int g = 0;
+        for (int u = cid; u < p.units && !stop; u += ncl) {
+          for (int i = 0; i < p.rb; ++i, ++g) {
+            const int b = g & 1;
+            // the operands first: the buffer is the one that is waited for
+            int r = tc::mbar_spin_abortable<true>(full_bar(slot), ph, abort_flag, p.mma_wait_limit);
+            if (r == tc::kWaitDone)
+              r = tc::mbar_spin_abortable<true>(read_bar(b), ((g >> 1) & 1) ^ 1, abort_flag, 1ll << 31);
+            r = __shfl_sync(0xffffffffu, r, 0);
+            if (r != tc::kWaitDone) {
+              if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleMma);
+              stop = true;
+              break;
+            }
+            tc::fence_after_sync();
+            const uint64_t off = static_cast<uint64_t>(slot * (kPairStageBytes >> 4));
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_f8_ss<2>(tmem + 256u * b, adesc0 + off + 2u * j, bdesc0 + off + kBStep * j, idesc,
+                             j != 0 ? 1u : 0u);
+              tc::mma_commit<2>(empty_bar(slot));
+              tc::mma_commit<2>(sum_bar(b));
+            }
+            __syncwarp();
+            if (++slot == kPairStages) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
         }
-        const uint32_t dst = base + kPairOffScale + (ch & 1) * kScaleBytes + j * kScalePitch * 4;
-        const int n = i + j < p.rb ? tokens : 0;       // tokens to read in this lane's block
-#pragma unroll 2
-        for (int t = t0; t < 128; t += 4)
-          copy4(dst + 4 * t, src + i + static_cast<int64_t>(t < n ? t - t0 : 0) * p.rb, t < n);
-        if (warp == 2) copy4(dst + 4 * (128 + (lane >> 4)), wsrc + i * p.ws_red, n > 0 && w_in);
-        arrive_on_copies(sfull_bar(ch & 1));
+        if (tc::elect_one()) tc::mma_commit<2>(drain_bar);
+        __syncwarp();
+        if (lane == 0 && !tc::mbar_wait(drain_bar, 0)) fail(kRoleMma);
       }
+    } else {
+      // lane: block j of two tokens a step, one token a half-warp
+      const int j = lane & 15, t0 = 2 * (warp - 2) + (lane >> 4);
+      int ch = 0;
+      bool stop = false;
+      for (int u = cid; u < p.units && !stop; u += ncl) {
+        const int64_t m0 = tile_m(u), cb = tile_c(u) / 128 + (lane >> 4);
+        const int tokens = static_cast<int>(min(p.M - m0, static_cast<int64_t>(128)));
+        const float* src = p.a_scale + (m0 + t0) * p.rb + j;
+        const float* wsrc = p.w_scale + cb * p.ws_col + j * p.ws_red;
+        const bool w_in = cb < col_blocks;
+        for (int i = 0; i < p.rb; i += kScaleChunk, ++ch) {
+          int r = tc::mbar_wait_abortable(sempty_bar(ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag);
+          r = __shfl_sync(0xffffffffu, r, 0);
+          if (r != tc::kWaitDone) {
+            if (lane == 0 && r == tc::kWaitTimeout) fail(kRoleProducer);
+            stop = true;
+            break;
+          }
+          const uint32_t dst = base + kPairOffScale + (ch & 1) * kScaleBytes + j * kScalePitch * 4;
+          const int n = i + j < p.rb ? tokens : 0;       // tokens to read in this lane's block
+#pragma unroll 2
+          for (int t = t0; t < 128; t += 4)
+            copy4(dst + 4 * t, src + i + static_cast<int64_t>(t < n ? t - t0 : 0) * p.rb, t < n);
+          if (warp == 2) copy4(dst + 4 * (128 + (lane >> 4)), wsrc + i * p.ws_red, n > 0 && w_in);
+          arrive_on_copies(sfull_bar(ch & 1));
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");   // also after an abort
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");   // also after an abort
-   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairManyRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
@@ -408,9 +412,11 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
         tc::fence_after_sync();
-        // the next 16 columns are on their way while the last are added
-        float v[2][16];
-        tmem_ld16f(src + 256u * b, v[0]);
+        // 64 columns at a time (16 at a time, the next on their way while the last
+        // are added, ran 2% slower; loads of 32 columns spilled)
+        float v[4][16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld16f(src + 256u * b + 16u * k, v[k]);
         const float s = sa * sw;
         if (in == kScaleChunk - 1 || i + 1 == p.rb) {
           __syncwarp();
@@ -419,14 +425,14 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 7; ++c) {
-          tmem_ld16f(src + 256u * b + 16u * (c + 1), v[(c + 1) & 1]);
-          scale_add<16>(acc + 16 * c, v[c & 1], s);
-          tc::tmem_wait_ld();
-        }
+        for (int k = 0; k < 4; ++k) scale_add(acc + 16 * k, v[k], s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld16f(src + 256u * b + 64u + 16u * k, v[k]);
+        tc::tmem_wait_ld();
         tc::fence_before_sync();         // all read: the buffer is free
         if (lane == 0) arrive_relaxed(read_remote + 8u * b);
-        scale_add<16>(acc + 112, v[1], s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) scale_add(acc + 64 + 16 * k, v[k], s);
         b ^= 1u;
         sum_ph ^= b ^ 1u;
       }
