@@ -517,6 +517,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 //   scales (the tokens', [block][token], and the tile's weight scale),
 //   warps 4.. totals: a thread holds one output column for kBT / kGroups
 //   tokens, whose factors it reads as broadcasts.
+//
+// Measured (CUDA graph): 64 tokens, 18944 x 3584, 16.7 us (4.2 TB/s; a block
+// takes 0.37 us on 148 SMs, 6 TB/s of weight, and launch, first loads and the
+// exchange of totals 4 us); 1 token, 4096 x 4096, 5.7 us in splits of 4.
 template <int kBT>
 struct RowsCfg {
   static constexpr int kGroups = kBT >= 64 ? 2 : 1;      // token groups, four warps each
@@ -707,11 +711,11 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         for (int k = 0; k < 4; ++k) f[k] = lds128(sp + 4 * (C::kCols * part + c) + 16 * k);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          acc[c + 4 * k] = fmaf(v[4 * k] * w, f[k].x, acc[c + 4 * k]);
-          acc[c + 4 * k + 1] = fmaf(v[4 * k + 1] * w, f[k].y, acc[c + 4 * k + 1]);
-          acc[c + 4 * k + 2] = fmaf(v[4 * k + 2] * w, f[k].z, acc[c + 4 * k + 2]);
-          acc[c + 4 * k + 3] = fmaf(v[4 * k + 3] * w, f[k].w, acc[c + 4 * k + 3]);
+        for (int k = 0; k < 4; ++k) {   // the two scales first: their product may be all that is in range
+          acc[c + 4 * k] = fmaf(v[4 * k], f[k].x * w, acc[c + 4 * k]);
+          acc[c + 4 * k + 1] = fmaf(v[4 * k + 1], f[k].y * w, acc[c + 4 * k + 1]);
+          acc[c + 4 * k + 2] = fmaf(v[4 * k + 2], f[k].z * w, acc[c + 4 * k + 2]);
+          acc[c + 4 * k + 3] = fmaf(v[4 * k + 3], f[k].w * w, acc[c + 4 * k + 3]);
         }
       }
       tc::fence_before_sync();

@@ -3,7 +3,9 @@
 // dequantization. The format is stated in fp8.cuh.
 //
 // All kernels are streaming passes: 4 or 2 bytes read and 1 byte and a
-// little written per value (dequantize the reverse).
+// little written per value (dequantize the reverse). Measured, of the copy
+// bandwidth: 1 x 128 blocks of 4096 x 18944 bf16 39 us (0.89), 128 x 128 blocks
+// of 11008 x 4096 fp32 34 us (0.99).
 #include "fp8.cuh"
 
 namespace nf4 {
@@ -11,13 +13,14 @@ namespace {
 
 // 1 x 128 blocks: 16 lanes hold a block, 8 values each, so a half-warp's load
 // is a whole 256-byte (16-bit input) or 512-byte (fp32) run and its store a
-// whole 128-byte line of codes. kUnroll blocks per half-warp keep that many
+// whole 128-byte line of codes. kRowUnroll blocks per half-warp keep that many
 // loads in flight per lane.
 constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 4;
 
 // kWhole: rows of whole blocks, which then lie one after another and need no
-// row index (the 64-bit division by kb took longer than the block's bytes).
+// row index (with a 64-bit division by kb for each block the pass above took
+// 74 us).
 template <int kElem, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads)
 fp8_quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols, uint32_t kb,

@@ -149,6 +149,16 @@ def test_scales_of_any_size_multiply_as_they_are():
         check_product(nf4.nf4_fp8_matmul_fwd(a, w), a, w, False, 3)
 
 
+@pytest.mark.parametrize("M", [7, 40, 100, 300])
+def test_scales_whose_product_alone_is_in_range(M):
+    """Neither scale times a block's sum fits fp32; the two scales' product does."""
+    for sa, sw in ((1e-34, 1e34), (1e34, 1e-34)):
+        a = nf4.FP8Tensor(torch.full((M, 272), 448.0, device=DEV).to(F8), torch.full((M, 3), sa, device=DEV))
+        w = nf4.FP8Tensor(torch.full((144, 272), 448.0, device=DEV).to(F8),
+                          torch.full((2, 3), sw, device=DEV), 128)
+        check_product(nf4.nf4_fp8_matmul_fwd(a, w), a, w, False, 3)
+
+
 def test_empty_calls():
     w = nf4.nf4_fp8_quantize(make(32, 256, 5).to(DEV), block_rows=128)
     assert nf4.nf4_fp8_matmul_fwd(nf4.alloc_fp8(0, 256, DEV), w).shape == (0, 32)
