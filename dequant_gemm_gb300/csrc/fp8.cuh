@@ -35,6 +35,17 @@ __device__ __forceinline__ float fp8_inverse(float scale) {
   return scale == 0.0f ? 0.0f : __frcp_rn(scale);
 }
 
+// Programmatic dependent launch: lets the next kernel of the stream, if it was
+// launched so, be set up while this one runs; and waits until the kernels
+// before this one are complete. A kernel launched so reads and writes nothing
+// in global memory before the wait.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // max that returns NaN if either operand is NaN (fmaxf drops it).
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;

@@ -228,6 +228,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   tc::cluster_sync();                  // the peer's barriers exist before any arrival
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  let_next_start();
+  wait_for_previous();
 
   auto fail = [&](uint32_t role) {
     report_status(p.status, kStatusTimeout, kDx ? kSiteFp8Dx : kSiteFp8Fwd, role);
@@ -595,6 +597,8 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   tc::fence_after_sync();
   cluster_arrive();
   const uint32_t tmem = *tmem_slot;
+  let_next_start();
+  wait_for_previous();
 
   auto fail = [&](uint32_t role) {
     report_status(p.status, kStatusTimeout, kDx ? kSiteFp8Dx : kSiteFp8Fwd, role);
@@ -790,6 +794,23 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   }
 }
 
+// Launch attributes of both kernels: a cluster along x, and programmatic launch
+// (the set-up, and the waiting for the last tiles of the kernel before, overlap).
+struct LaunchAttrs {
+  cudaLaunchAttribute a[2];
+
+  void set(cudaLaunchConfig_t* cfg, int cluster) {
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    a[0].val.clusterDim.y = 1;
+    a[0].val.clusterDim.z = 1;
+    a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = a;
+    cfg->numAttrs = 2;
+  }
+};
+
 // Launch shape of a rows call: splits of the reduction, and its time in 0.01
 // us, start-up left out. Measured at 128 tokens a tile on the decoder shapes:
 // 0.46 us a block, 1.5 us a round for the last block and the reduction.
@@ -800,7 +821,7 @@ struct RowsPlan {
 
 template <bool kDx, int kBT>
 cudaLaunchConfig_t rows_config(int splits, int64_t row_tiles, int64_t m_tiles, cudaStream_t st,
-                               cudaLaunchAttribute* attr) {
+                               LaunchAttrs* attrs) {
   using C = RowsCfg<kBT>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(row_tiles),
@@ -808,12 +829,7 @@ cudaLaunchConfig_t rows_config(int splits, int64_t row_tiles, int64_t m_tiles, c
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = static_cast<unsigned>(splits);
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attrs->set(&cfg, splits);
   return cfg;
 }
 
@@ -832,8 +848,8 @@ RowsCapacity rows_capacity(const Fp8Call& c) {
     cudaFuncSetAttribute(fp8_rows_kernel<kDx, kBT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          RowsCfg<kBT>::kSmem);
     for (int i = 0; i < 4; ++i) {
-      cudaLaunchAttribute attr;
-      const cudaLaunchConfig_t cfg = rows_config<kDx, kBT>(1 << i, c.num_sms, 1, c.st, &attr);
+      LaunchAttrs attrs;
+      const cudaLaunchConfig_t cfg = rows_config<kDx, kBT>(1 << i, c.num_sms, 1, c.st, &attrs);
       int clusters = 0;
       if (cudaOccupancyMaxActiveClusters(&clusters, fp8_rows_kernel<kDx, kBT>, &cfg) != cudaSuccess) {
         cudaGetLastError();
@@ -880,8 +896,8 @@ cudaError_t launch_rows(const Fp8Call& c, const MatmulArgs& a, int64_t red) {
                  static_cast<uint64_t>(c.N), static_cast<uint64_t>(c.K), 128, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = rows_config<kDx, kBT>(splits, row_tiles, m_tiles, c.st, &attr);
+  LaunchAttrs attrs;
+  const cudaLaunchConfig_t cfg = rows_config<kDx, kBT>(splits, row_tiles, m_tiles, c.st, &attrs);
   return cudaLaunchKernelEx(&cfg, fp8_rows_kernel<kDx, kBT>, tm_a, tm_w, a);
 }
 
@@ -913,13 +929,8 @@ cudaError_t launch_pair(const Fp8Call& c, const MatmulArgs& args, int64_t red) {
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = c.st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  LaunchAttrs attrs;
+  attrs.set(&cfg, 2);
   return cudaLaunchKernelEx(&cfg, fp8_pair_kernel<kDx>, tm_a, tm_w, tm_out, a);
 }
 

@@ -25,6 +25,7 @@ template <int kElem, bool kWhole>
 __global__ void __launch_bounds__(kRowThreads)
 fp8_quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols, uint32_t kb,
                          uint8_t* __restrict__ codes, float* __restrict__ scale) {
+  let_next_start();
   const int sub = threadIdx.x & 15;
   const int64_t groups = rows * kb;
   const int64_t g0 = (static_cast<int64_t>(blockIdx.x) * (kRowThreads / 16) + (threadIdx.x >> 4)) * kRowUnroll;
@@ -70,6 +71,7 @@ fp8_quantize_tiles_kernel(const void* __restrict__ x, int64_t rows, int64_t cols
                           uint8_t* __restrict__ codes, float* __restrict__ scale) {
   constexpr int kSteps = kFp8Block * kFp8Block / (8 * kTileThreads);   // 8
   __shared__ float part[kTileThreads / 32];
+  let_next_start();
   const int64_t rb = blockIdx.x / kb, cb = blockIdx.x % kb;
   const int64_t c = cb * kFp8Block + 8 * (threadIdx.x & 15);
   const int64_t r0 = rb * kFp8Block + (threadIdx.x >> 4);

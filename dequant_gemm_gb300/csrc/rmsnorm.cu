@@ -230,6 +230,7 @@ rmsnorm_fwd_kernel(const FwdArgs p) {
   const int64_t row = blockIdx.x, row0 = row * p.cols, total = gridDim.x * p.cols;
   const int cols = static_cast<int>(p.cols), step = blockDim.x * 8;
   const int c0 = static_cast<int>(threadIdx.x) * 8 - (kShift ? static_cast<int>(row0 & 7) : 0);
+  let_next_start();
   float v[kNC][8];
 #pragma unroll
   for (int i = 0; i < kNC; ++i)
@@ -515,7 +516,7 @@ rmsnorm_dweight_kernel(const float* __restrict__ partial, int parts, int64_t col
   __shared__ float sums[kSumThreads / 32][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (lane & 7);
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partial rows are written
+  wait_for_previous();                               // the partial rows are written
   float s = 0.0f;
   if (c < cols) {
 #pragma unroll 10
