@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(kRowThreads)
 fp8_quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols, uint32_t kb,
                          uint8_t* __restrict__ codes, float* __restrict__ scale) {
   let_next_start();
+  wait_for_previous();
   const int sub = threadIdx.x & 15;
   const int64_t groups = rows * kb;
   const int64_t g0 = (static_cast<int64_t>(blockIdx.x) * (kRowThreads / 16) + (threadIdx.x >> 4)) * kRowUnroll;
@@ -72,6 +73,7 @@ fp8_quantize_tiles_kernel(const void* __restrict__ x, int64_t rows, int64_t cols
   constexpr int kSteps = kFp8Block * kFp8Block / (8 * kTileThreads);   // 8
   __shared__ float part[kTileThreads / 32];
   let_next_start();
+  wait_for_previous();
   const int64_t rb = blockIdx.x / kb, cb = blockIdx.x % kb;
   const int64_t c = cb * kFp8Block + 8 * (threadIdx.x & 15);
   const int64_t r0 = rb * kFp8Block + (threadIdx.x >> 4);
@@ -111,6 +113,8 @@ template <int kElem>
 __global__ void __launch_bounds__(256)
 fp8_dequantize_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scale,
                       int64_t cols, int64_t chunks, int kb, int block_rows, void* __restrict__ out) {
+  let_next_start();
+  wait_for_previous();
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (t >= chunks) return;
   const int64_t i = 8 * t, r = i / cols, c = i - r * cols;
@@ -136,19 +140,13 @@ cudaError_t launch_fp8_quantize(const void* x, int x_elem, int64_t rows, int64_t
     constexpr int kElem = decltype(elem)::value;
     if (block_rows == 1) {
       const int64_t per_cta = kRowThreads / 16 * kRowUnroll;
-      const unsigned grid = static_cast<unsigned>((rows * kb + per_cta - 1) / per_cta);
-      if (cols % kFp8Block == 0)
-        fp8_quantize_rows_kernel<kElem, true>
-            <<<grid, kRowThreads, 0, st>>>(x, rows, cols, static_cast<uint32_t>(kb), codes, scale);
-      else
-        fp8_quantize_rows_kernel<kElem, false>
-            <<<grid, kRowThreads, 0, st>>>(x, rows, cols, static_cast<uint32_t>(kb), codes, scale);
-    } else {
-      const int64_t rb = (rows + kFp8Block - 1) / kFp8Block;
-      fp8_quantize_tiles_kernel<kElem><<<static_cast<unsigned>(rb * kb), kTileThreads, 0, st>>>(
-          x, rows, cols, static_cast<int>(kb), codes, scale);
+      return launch_next(cols % kFp8Block == 0 ? fp8_quantize_rows_kernel<kElem, true>
+                                               : fp8_quantize_rows_kernel<kElem, false>,
+                         (rows * kb + per_cta - 1) / per_cta, kRowThreads, st, x, rows, cols, kb, codes,
+                         scale);
     }
-    return cudaGetLastError();
+    return launch_next(fp8_quantize_tiles_kernel<kElem>, (rows + kFp8Block - 1) / kFp8Block * kb,
+                       kTileThreads, st, x, rows, cols, kb, codes, scale);
   };
   if (x_elem == kElemF32) return go(std::integral_constant<int, kElemF32>{});
   if (x_elem == kElemBf16) return go(std::integral_constant<int, kElemBf16>{});
@@ -161,9 +159,8 @@ cudaError_t launch_fp8_dequantize(const uint8_t* codes, const float* scale, int6
   const int64_t kb = (cols + kFp8Block - 1) / kFp8Block, chunks = rows * cols / 8;
   auto go = [&](auto elem) {
     constexpr int kElem = decltype(elem)::value;
-    fp8_dequantize_kernel<kElem><<<static_cast<unsigned>((chunks + 255) / 256), 256, 0, st>>>(
-        codes, scale, cols, chunks, static_cast<int>(kb), block_rows, out);
-    return cudaGetLastError();
+    return launch_next(fp8_dequantize_kernel<kElem>, (chunks + 255) / 256, 256, st, codes, scale, cols,
+                       chunks, kb, block_rows, out);
   };
   if (out_elem == kElemF32) return go(std::integral_constant<int, kElemF32>{});
   if (out_elem == kElemBf16) return go(std::integral_constant<int, kElemBf16>{});

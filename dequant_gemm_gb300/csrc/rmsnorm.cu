@@ -231,6 +231,7 @@ rmsnorm_fwd_kernel(const FwdArgs p) {
   const int cols = static_cast<int>(p.cols), step = blockDim.x * 8;
   const int c0 = static_cast<int>(threadIdx.x) * 8 - (kShift ? static_cast<int>(row0 & 7) : 0);
   let_next_start();
+  wait_for_previous();
   float v[kNC][8];
 #pragma unroll
   for (int i = 0; i < kNC; ++i)
@@ -279,6 +280,8 @@ rmsnorm_fwd_kernel(const FwdArgs p) {
 template <int kVec>
 __global__ void __launch_bounds__(512) rmsnorm_fwd_long_kernel(const FwdArgs p) {
   __shared__ float part[32];
+  let_next_start();
+  wait_for_previous();
   const int64_t row = blockIdx.x, step = static_cast<int64_t>(blockDim.x) * kVec;
   float ss = 0.0f;
   for (int64_t c = threadIdx.x * kVec; c < p.cols; c += step) {
@@ -325,6 +328,7 @@ struct BwdArgs {
 template <int kVec>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_long_kernel(const BwdArgs p) {
   __shared__ float part[2][32];
+  wait_for_previous();
   const int64_t step = static_cast<int64_t>(blockDim.x) * kVec;
   float* acc = p.partial + blockIdx.x * p.cols;
   int k = 0;
@@ -420,6 +424,7 @@ struct Raw {
 // 5119 48 us. The rows staged in shared memory by bulk copies instead took 31 us.
 template <int kElem, bool kShift, int kNC, bool kAhead, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_bwd_kernel(const BwdArgs p) {
+  wait_for_previous();
   using R = Raw<kElem>;
   __shared__ float part[2][32];
   const int cols = static_cast<int>(p.cols), step = blockDim.x * 8;
@@ -550,37 +555,39 @@ bool bwd_in_registers(int64_t cols, int elem) {
 
 template <int kX, int kRes>
 cudaError_t launch_fwd(const NormFwdCall& c, const FwdArgs& a) {
-  const unsigned grid = static_cast<unsigned>(c.rows);
   // four runs a thread, whose loads are in flight together, in CTAs small
   // enough that several rows share an SM. By the row's length alone: a row's
   // sum, and with it the row's result, does not depend on how many rows the
   // call has.
   const int64_t runs = runs_of(c.cols);
   if (c.cols % 8 != 0)
-    rmsnorm_fwd_kernel<kX, kRes, true, 2><<<grid, threads_for(runs, 2), 0, c.st>>>(a);
-  else if (runs <= 256)
-    rmsnorm_fwd_kernel<kX, kRes, false, 2><<<grid, threads_for(runs, 2), 0, c.st>>>(a);
-  else
-    rmsnorm_fwd_kernel<kX, kRes, false, 4><<<grid, threads_for(runs, 4), 0, c.st>>>(a);
-  return cudaGetLastError();
+    return launch_next(rmsnorm_fwd_kernel<kX, kRes, true, 2>, c.rows, threads_for(runs, 2), c.st, a);
+  if (runs <= 256)
+    return launch_next(rmsnorm_fwd_kernel<kX, kRes, false, 2>, c.rows, threads_for(runs, 2), c.st, a);
+  return launch_next(rmsnorm_fwd_kernel<kX, kRes, false, 4>, c.rows, threads_for(runs, 4), c.st, a);
 }
 
 template <int kElem, bool kShift>
 cudaError_t launch_bwd(const NormBwdCall& c, const BwdArgs& a, unsigned parts) {
   const int64_t runs = runs_of(c.cols);
-  if (!bwd_in_registers(c.cols, kElem)) {
-    rmsnorm_bwd_long_kernel<kShift ? 1 : 8><<<parts, 512, 0, c.st>>>(a);
-  } else if constexpr (kElem == kElemF32) {
+  if (!bwd_in_registers(c.cols, kElem))
+    return launch_next(rmsnorm_bwd_long_kernel<kShift ? 1 : 8>, parts, 512, c.st, a);
+  if constexpr (kElem == kElemF32) {
     // the next row on its way needs 32 more registers a thread than 1024
     // threads can have
-    if (runs <= 640) rmsnorm_bwd_kernel<kElem, kShift, 1, true, 640><<<parts, threads_for(runs, 1), 0, c.st>>>(a);
-    else rmsnorm_bwd_kernel<kElem, kShift, 1, false, 1024><<<parts, threads_for(runs, 1), 0, c.st>>>(a);
-  } else if (runs <= 1024) {
-    rmsnorm_bwd_kernel<kElem, kShift, 1, true, 1024><<<parts, threads_for(runs, 1), 0, c.st>>>(a);
-  } else if constexpr (!kShift) {
-    rmsnorm_bwd_kernel<kElem, false, 4, false, 512><<<parts, threads_for(runs, 4), 0, c.st>>>(a);
+    if (runs <= 640)
+      return launch_next(rmsnorm_bwd_kernel<kElem, kShift, 1, true, 640>, parts, threads_for(runs, 1),
+                         c.st, a);
+    return launch_next(rmsnorm_bwd_kernel<kElem, kShift, 1, false, 1024>, parts, threads_for(runs, 1),
+                       c.st, a);
+  } else {
+    if constexpr (!kShift)
+      if (runs > 1024)
+        return launch_next(rmsnorm_bwd_kernel<kElem, false, 4, false, 512>, parts, threads_for(runs, 4),
+                           c.st, a);
+    return launch_next(rmsnorm_bwd_kernel<kElem, kShift, 1, true, 1024>, parts, threads_for(runs, 1),
+                       c.st, a);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -588,12 +595,9 @@ cudaError_t launch_bwd(const NormBwdCall& c, const BwdArgs& a, unsigned parts) {
 cudaError_t launch_rmsnorm_fwd(const NormFwdCall& c) {
   const FwdArgs a = {c.x, c.residual, c.weight, c.h, c.y, c.scale, c.rstd, c.cols,
                      c.x_elem, c.h_elem, c.w_elem, c.y_elem, c.y_fp8 ? 1 : 0, c.eps};
-  if (!fwd_in_registers(c.cols)) {
-    const unsigned grid = static_cast<unsigned>(c.rows);
-    if (c.cols % 8 == 0) rmsnorm_fwd_long_kernel<8><<<grid, 512, 0, c.st>>>(a);
-    else rmsnorm_fwd_long_kernel<1><<<grid, 512, 0, c.st>>>(a);
-    return cudaGetLastError();
-  }
+  if (!fwd_in_registers(c.cols))
+    return launch_next(c.cols % 8 == 0 ? rmsnorm_fwd_long_kernel<8> : rmsnorm_fwd_long_kernel<1>, c.rows,
+                       512, c.st, a);
   const int res = !c.residual ? 0 : c.h_elem == c.x_elem ? 1 : 2;
   auto go = [&](auto x) {
     constexpr int kX = decltype(x)::value;
@@ -624,18 +628,8 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c) {
                         : c.elem == kElemBf16 ? go(std::integral_constant<int, kElemBf16>{})
                                               : go(std::integral_constant<int, kElemF16>{});
   if (e != cudaSuccess || (parts == 1 && bwd_in_registers(c.cols, c.elem))) return e;
-  // launched while the backward drains; it waits for the partial rows itself
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((c.cols + 7) / 8));
-  cfg.blockDim = dim3(kSumThreads);
-  cfg.stream = c.st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel, static_cast<const float*>(c.partial),
-                            static_cast<int>(parts), c.cols, c.dweight, c.w_elem);
+  return launch_next(rmsnorm_dweight_kernel, (c.cols + 7) / 8, kSumThreads, c.st, c.partial,
+                     static_cast<int>(parts), c.cols, c.dweight, c.w_elem);
 }
 
 }  // namespace nf4
