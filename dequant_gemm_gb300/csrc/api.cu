@@ -408,7 +408,8 @@ nf4_status nf4_rmsnorm_fwd(const void* x, int32_t x_elem, const void* residual, 
 
 int64_t nf4_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
-  return nf4::rmsnorm_bwd_parts(rows, cols) * cols * static_cast<int64_t>(sizeof(float));
+  // of any type: the 16-bit types have more rows at once than fp32
+  return nf4::rmsnorm_bwd_parts(rows, cols, nf4::kElemBf16) * cols * static_cast<int64_t>(sizeof(float));
 }
 
 nf4_status nf4_rmsnorm_bwd(const void* dy, const void* h, const void* dh, int32_t elem,

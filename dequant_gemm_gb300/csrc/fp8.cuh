@@ -234,12 +234,12 @@ struct NormBwdCall {
   const float* rstd;       // [rows]
   void* dx;                // [rows, cols] of elem
   void* dweight;           // [cols] of w_elem
-  float* partial;          // rmsnorm_bwd_parts(rows, cols) x cols
+  float* partial;          // rmsnorm_bwd_parts(rows, cols, elem) x cols
   int64_t rows, cols;
   int num_sms;
   cudaStream_t st;
 };
-int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols);
+int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols, int elem);
 cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c);
 
 }  // namespace nf4

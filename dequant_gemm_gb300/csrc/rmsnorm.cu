@@ -93,6 +93,55 @@ __device__ __forceinline__ void trim_run(int col, int cols, float (&v)[8]) {
     if (col + j < 0 || col + j >= cols) v[j] = 0.0f;
 }
 
+// A run as it lies in memory (16 or 32 bytes), so that a row on its way costs
+// no more registers than it has bytes.
+template <int kElem>
+struct Raw {
+  static constexpr int kWords = 2 * Elem<kElem>::kBytes;
+  uint32_t w[kWords];
+
+  template <bool kShift>
+  __device__ __forceinline__ void load(const void* p, int64_t at, int col, int cols, int64_t total) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = 0u;
+    if (!any_of_run<kShift>(col, cols)) return;
+    if (!kShift || at + 8 <= total) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * Elem<kElem>::kBytes);
+#pragma unroll
+      for (int j = 0; j < kWords / 4; ++j) {
+        const uint4 u = q[j];
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+      }
+    } else {                         // the tensor's last run
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j >= 0 && col + j < cols) {
+          if constexpr (kElem == kElemF32) w[j] = static_cast<const uint32_t*>(p)[at + j];
+          else w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at + j]) << (16 * (j & 1));
+        }
+    }
+  }
+  // As trim_run.
+  template <bool kShift>
+  __device__ __forceinline__ void trim(int col, int cols) {
+    if (!kShift || whole_run<kShift>(col, cols)) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < 0 || col + j >= cols) {
+        if constexpr (kElem == kElemF32) w[j] = 0u;
+        else w[j >> 1] &= (j & 1) ? 0xffffu : 0xffff0000u;
+      }
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (kElem == kElemF32) return __uint_as_float(w[j]);
+    const float2 f = unpack2<kElem>(w[j >> 1]);
+    return (j & 1) ? f.y : f.x;
+  }
+};
+
 // Eight consecutive elements of a vector over the columns, zeros outside it.
 // Unaligned with kShift: single elements at indexes held within the vector, so
 // that the loads need no guards and go out together, or for fp32 the three
@@ -220,8 +269,8 @@ __device__ __forceinline__ void write_y(const FwdArgs& p, int64_t row, int64_t c
 // elements, blockDim.x runs apart (so that 16 lanes hold a block of the 8-bit
 // output). Bound by HBM: 8192 x 4096 bf16 with an fp32 residual to e4m3 in 60 us
 // (6.1 TB/s, 0.92 of the copy bandwidth; read twice it took 90). Odd lengths
-// keep the 16-byte accesses (kShift): the norm of 4096 x 5119 takes 50 us, with
-// single elements a lane 62.
+// keep the 16-byte accesses (kShift): 4096 x 5119 fp32 53 us (6.3 TB/s), bf16 34
+// (4.9 TB/s, by the edges' and the unaligned weight's instructions).
 template <int kX, int kRes, bool kShift, int kNC>
 __global__ void __launch_bounds__(1024)
 rmsnorm_fwd_kernel(const FwdArgs p) {
@@ -233,18 +282,37 @@ rmsnorm_fwd_kernel(const FwdArgs p) {
   let_next_start();
   wait_for_previous();
   float v[kNC][8];
-#pragma unroll
-  for (int i = 0; i < kNC; ++i)
-    load_run<kShift>(p.x, kX, row0 + c0 + i * step, c0 + i * step, cols, total, v[i]);
-  if constexpr (kRes != 0) {
-    float r[kNC][8];
+  if constexpr (!kShift) {
 #pragma unroll
     for (int i = 0; i < kNC; ++i)
-      load_run<kShift>(p.residual, kH, row0 + c0 + i * step, c0 + i * step, cols, total, r[i]);
+      load_run<false>(p.x, kX, row0 + c0 + i * step, c0 + i * step, cols, total, v[i]);
+    if constexpr (kRes != 0) {
+      float r[kNC][8];
+#pragma unroll
+      for (int i = 0; i < kNC; ++i)
+        load_run<false>(p.residual, kH, row0 + c0 + i * step, c0 + i * step, cols, total, r[i]);
+#pragma unroll
+      for (int i = 0; i < kNC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = round_to(v[i][j] + r[i][j], kH);
+    }
+  } else {
+    // As they lie in memory first: with conversions in these loads' branches
+    // each is waited for before the next.
+    Raw<kX> x[kNC];
+    Raw<kH> r[kNC];
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) x[i].template load<true>(p.x, row0 + c0 + i * step, c0 + i * step, cols, total);
+#pragma unroll
+    for (int i = 0; i < kNC; ++i)
+      if (kRes) r[i].template load<true>(p.residual, row0 + c0 + i * step, c0 + i * step, cols, total);
 #pragma unroll
     for (int i = 0; i < kNC; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = round_to(v[i][j] + r[i][j], kH);
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = x[i].at(j);
+        if constexpr (kRes != 0) v[i][j] = round_to(v[i][j] + r[i].at(j), kH);
+      }
   }
   float ss = 0.0f;
 #pragma unroll
@@ -364,64 +432,15 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_long_kernel(const BwdArgs p) 
   }
 }
 
-// A run as it lies in memory (16 or 32 bytes), so that a row on its way costs
-// no more registers than it has bytes.
-template <int kElem>
-struct Raw {
-  static constexpr int kWords = 2 * Elem<kElem>::kBytes;
-  uint32_t w[kWords];
-
-  template <bool kShift>
-  __device__ __forceinline__ void load(const void* p, int64_t at, int col, int cols, int64_t total) {
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = 0u;
-    if (!any_of_run<kShift>(col, cols)) return;
-    if (!kShift || at + 8 <= total) {
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * Elem<kElem>::kBytes);
-#pragma unroll
-      for (int j = 0; j < kWords / 4; ++j) {
-        const uint4 u = q[j];
-        w[4 * j] = u.x;
-        w[4 * j + 1] = u.y;
-        w[4 * j + 2] = u.z;
-        w[4 * j + 3] = u.w;
-      }
-    } else {                         // the tensor's last run
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col + j >= 0 && col + j < cols) {
-          if constexpr (kElem == kElemF32) w[j] = static_cast<const uint32_t*>(p)[at + j];
-          else w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at + j]) << (16 * (j & 1));
-        }
-    }
-  }
-  // As trim_run.
-  template <bool kShift>
-  __device__ __forceinline__ void trim(int col, int cols) {
-    if (!kShift || whole_run<kShift>(col, cols)) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + j < 0 || col + j >= cols) {
-        if constexpr (kElem == kElemF32) w[j] = 0u;
-        else w[j >> 1] &= (j & 1) ? 0xffffu : 0xffff0000u;
-      }
-  }
-  __device__ __forceinline__ float at(int j) const {
-    if constexpr (kElem == kElemF32) return __uint_as_float(w[j]);
-    const float2 f = unpack2<kElem>(w[j >> 1]);
-    return (j & 1) ? f.y : f.x;
-  }
-};
-
 // Rows of up to kNC runs a thread, in registers: gridDim.x CTAs take the rows
 // in turn, the next row's loads under way while this one is reduced (kAhead),
 // each thread's share of dw in registers until the CTA is done. That wants a
 // thread's columns to be the same in all rows of its CTA: with kShift the
 // rows' offsets repeat every 8 rows, and gridDim.x is a multiple of 8 (or
 // every CTA has one row). One CTA alone writes dw itself.
-// Measured with dh and the sum of the partial rows: 4096 x 3584 bf16 25 us (21
+// Measured with dh and the sum of the partial rows: 4096 x 3584 bf16 24 us (21
 // of it here, 5.6 TB/s; in two passes over memory 92), 8192 x 4096 48 us; 4096 x
-// 5119 48 us. The rows staged in shared memory by bulk copies instead took 31 us.
+// 5119 49 us. The rows staged in shared memory by bulk copies instead took 31 us.
 template <int kElem, bool kShift, int kNC, bool kAhead, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_bwd_kernel(const BwdArgs p) {
   wait_for_previous();
@@ -546,7 +565,7 @@ int threads_for(int64_t runs, int n) {
 }
 
 // Whether rows are held in registers: up to 1024 threads of 4 runs (forward,
-// 2 with odd lengths, whose addresses cost registers) or 1 run (gradients; 4
+// 2 with odd lengths) or 1 run (gradients; 4
 // in 512 threads for 16-bit types of even length).
 bool fwd_in_registers(int64_t cols) { return runs_of(cols) <= (cols % 8 == 0 ? 4096 : 2048); }
 bool bwd_in_registers(int64_t cols, int elem) {
@@ -556,10 +575,13 @@ bool bwd_in_registers(int64_t cols, int elem) {
 template <int kX, int kRes>
 cudaError_t launch_fwd(const NormFwdCall& c, const FwdArgs& a) {
   // four runs a thread, whose loads are in flight together, in CTAs small
-  // enough that several rows share an SM. By the row's length alone: a row's
-  // sum, and with it the row's result, does not depend on how many rows the
-  // call has.
+  // enough that several rows share an SM; one where odd lengths cost
+  // instructions and more warps hide them (4096 x 5119 bf16 34 us, with two runs
+  // 48; 4096 x 1023 8.4 and 10.4). By the row's length alone: a row's sum, and
+  // with it the row's result, does not depend on how many rows the call has.
   const int64_t runs = runs_of(c.cols);
+  if (c.cols % 8 != 0 && runs <= 1024)
+    return launch_next(rmsnorm_fwd_kernel<kX, kRes, true, 1>, c.rows, threads_for(runs, 1), c.st, a);
   if (c.cols % 8 != 0)
     return launch_next(rmsnorm_fwd_kernel<kX, kRes, true, 2>, c.rows, threads_for(runs, 2), c.st, a);
   if (runs <= 256)
@@ -574,9 +596,9 @@ cudaError_t launch_bwd(const NormBwdCall& c, const BwdArgs& a, unsigned parts) {
     return launch_next(rmsnorm_bwd_long_kernel<kShift ? 1 : 8>, parts, 512, c.st, a);
   if constexpr (kElem == kElemF32) {
     // the next row on its way needs 32 more registers a thread than 1024
-    // threads can have
-    if (runs <= 640)
-      return launch_next(rmsnorm_bwd_kernel<kElem, kShift, 1, true, 640>, parts, threads_for(runs, 1),
+    // threads can have (4096 x 5119: 64 us with it, 78 without)
+    if (runs <= 672)
+      return launch_next(rmsnorm_bwd_kernel<kElem, kShift, 1, true, 672>, parts, threads_for(runs, 1),
                          c.st, a);
     return launch_next(rmsnorm_bwd_kernel<kElem, kShift, 1, false, 1024>, parts, threads_for(runs, 1),
                        c.st, a);
@@ -610,16 +632,18 @@ cudaError_t launch_rmsnorm_fwd(const NormFwdCall& c) {
   return go(std::integral_constant<int, kElemF16>{});
 }
 
-// Rows of the workspace, one per CTA of the backward: as many CTAs as run at
-// once (about 1024 threads an SM), a multiple of 8 (rmsnorm_bwd_kernel).
-int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols) {
-  return std::min<int64_t>(rows, cols <= 1024 ? 1216 : cols <= 2048 ? 608 : cols <= 4096 ? 304 : 152);
+// CTAs of the backward, and rows of its workspace: as many as run at once, so
+// that none waits for another's end (a multiple of 8: rmsnorm_bwd_kernel). An
+// SM's registers hold 1024 threads of 64 (16-bit types) or 800 of 80 (fp32).
+int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols, int elem) {
+  const int64_t per_sm = std::clamp((elem == kElemF32 ? 800 : 1024) / threads_for(runs_of(cols), 1), 1, 8);
+  return std::min(rows, 152 * per_sm);
 }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c) {
   const BwdArgs a = {c.dy, c.h, c.dh, c.weight, c.rstd, c.dx, c.dweight, c.partial, c.rows, c.cols,
                      c.elem, c.w_elem};
-  const unsigned parts = static_cast<unsigned>(rmsnorm_bwd_parts(c.rows, c.cols));
+  const unsigned parts = static_cast<unsigned>(rmsnorm_bwd_parts(c.rows, c.cols, c.elem));
   auto go = [&](auto elem) {
     constexpr int kElem = decltype(elem)::value;
     return c.cols % 8 == 0 ? launch_bwd<kElem, false>(c, a, parts) : launch_bwd<kElem, true>(c, a, parts);
