@@ -46,8 +46,9 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Launches a kernel so (besides what it saves on the device, such a launch was
-// measured to take the host 3.2 us where a plain one took 4.1).
+// Launches a kernel so. On the host such a launch is no dearer than a plain one
+// (a product's, with its cluster attribute, 3.2 us for 4.1; a quantizer's 3.0 for
+// 3.1).
 template <typename... Params, typename... Args>
 cudaError_t launch_next(void (*kernel)(Params...), int64_t grid, int threads, cudaStream_t st,
                         Args... args) {

@@ -152,8 +152,8 @@ struct MatmulArgs {
 // Persistent: a pair takes the tiles c, c + G, ... in turn, tokens fastest,
 // and the copies and MMAs of the next tile start while one is written out.
 //
-// Measured: 4096 x 11008 x 4096 forward 153 us (2.4 PFLOP/s), 2048 x 4096 x
-// 11008 gradient 81 us, at the board's power limit (1376 W, 1950 MHz). A block
+// Measured: 4096 x 11008 x 4096 forward 150 us (2.5 PFLOP/s), 2048 x 4096 x
+// 11008 gradient 79 us, at the board's power limit (1376 W, 1950 MHz). A block
 // takes ~850 cycles against 512 of MMA: two buffers, each of which goes
 // through its MMAs, the commit, the totals warps' reads (~400 cycles) and the
 // hand-back across the pair. Tensor memory has room for no third buffer, and
@@ -520,9 +520,9 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 //   warps 4.. totals: a thread holds one output column for kBT / kGroups
 //   tokens, whose factors it reads as broadcasts.
 //
-// Measured (CUDA graph): 64 tokens, 18944 x 3584, 16.7 us (4.2 TB/s; a block
+// Measured (CUDA graph): 64 tokens, 18944 x 3584, 15.6 us (4.5 TB/s; a block
 // takes 0.37 us on 148 SMs, 6 TB/s of weight, and launch, first loads and the
-// exchange of totals 4 us); 1 token, 4096 x 4096, 5.7 us in splits of 4.
+// exchange of totals 4 us); 1 token, 4096 x 4096, 4.9 us in splits of 4.
 template <int kBT>
 struct RowsCfg {
   static constexpr int kGroups = kBT >= 64 ? 2 : 1;      // token groups, four warps each
