@@ -578,7 +578,8 @@ cudaError_t launch_fwd(const NormFwdCall& c, const FwdArgs& a) {
   // enough that several rows share an SM; one where odd lengths cost
   // instructions and more warps hide them (4096 x 5119 bf16 34 us, with two runs
   // 48; 4096 x 1023 8.4 and 10.4). By the row's length alone: a row's sum, and
-  // with it the row's result, does not depend on how many rows the call has.
+  // with it the row's result, does not depend on how many rows the call has (at
+  // odd lengths on its place modulo 8, which shifts its runs).
   const int64_t runs = runs_of(c.cols);
   if (c.cols % 8 != 0 && runs <= 1024)
     return launch_next(rmsnorm_fwd_kernel<kX, kRes, true, 1>, c.rows, threads_for(runs, 1), c.st, a);

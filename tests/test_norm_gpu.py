@@ -163,3 +163,46 @@ def test_offsets_beyond_32_bits():
     dx8, dw8 = nf4.nf4_rmsnorm_bwd(dy[-8:].contiguous(), x[-8:].contiguous(), w, r)
     assert torch.equal(dx[-8:], dx8) and not dx[:-8].any()
     assert ((dw - dw8).abs() <= 24 * 2.0 ** -24 * (dy[-8:].float() * x[-8:].float() * r[:, None]).abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows, cols", [(5, 2047), (4, 4097), (3, 8185), (3, 8187), (3, 16377), (2, 16379)])
+def test_forward_at_the_borders_of_odd_lengths(rows, cols, dtype):
+    """One and two runs a thread, and rows read twice: 1024 and 2048 runs."""
+    test_forward(rows, cols, dtype, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows, cols", [(1300, 129), (1000, 1023), (1250, 1024), (500, 2047), (310, 5119),
+                                        (160, 5363), (160, 5371), (9, 8185), (9, 8187)])
+def test_backward_with_more_rows_than_ctas(rows, cols, dtype):
+    """Rows beyond the CTAs that run at once, at lengths next to where their
+    number or the threads' runs change."""
+    test_backward(rows, cols, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("cols", [13, 1023, 5119, 8187])
+def test_rows_do_not_see_their_neighbours(cols, dtype):
+    """An odd length's 16-byte accesses reach into the rows beside it: what is
+    there, finite or NaN, changes no bit of a row in its place (on which, modulo
+    8 rows, the order of an odd row's sums depends)."""
+    rows = 17
+    x, w = make(1, cols, 1, dtype).to(DEV), (1 + make(1, cols, 2, std=0.1)[0]).to(DEV)
+    res, dy, dh = (make(1, cols, s, dtype).to(DEV) for s in (3, 4, 5))
+
+    def run(neighbours):
+        def among(row):
+            full = torch.full((rows, cols), neighbours, dtype=row.dtype, device=DEV)
+            full[1::2] = row
+            return full
+
+        y, h, r = nf4.nf4_rmsnorm_fwd(among(x), w, among(res), save_rstd=True)
+        dx, dw = nf4.nf4_rmsnorm_bwd(among(dy), h, w, r, dh=among(dh))
+        return (y, h, r, dx), dw
+
+    (clean, _), (nans, dw) = run(3.0), run(float("nan"))
+    for many, one in zip(nans, clean):
+        assert many[0::2].isnan().all() and not one.isnan().any()
+        assert torch.equal(many[1::2], one[1::2])
+    assert dw.isnan().all()
