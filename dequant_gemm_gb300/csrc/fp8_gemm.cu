@@ -275,12 +275,15 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
       }
-      // copies in flight after an abort land before the CTA exits: the even
-      // CTA's barrier also counts the peer's arrival, which may not come any more
-      // (then the wait runs to its limit)
-      if (*abort_flag && lane == 0)
+      // Copies in flight land before the CTA exits. Always waited for (it costs
+      // nothing where the block's sums have been taken): another warp may abort
+      // after this one has issued its last copy, and read the flag as clear.
+      // After an abort the peer's arrival, which the even CTA's barrier also
+      // counts, may not come any more (then the wait runs to its limit).
+      if (lane == 0)
         for (int g = max(0, gs - kPairStages); g < gs; ++g)
           tc::mbar_wait(full_bar(g % kPairStages), (g / kPairStages) & 1, 1ll << 24);
+      __syncwarp();
     } else if (warp == 1) {
       int slot = 0;
       uint32_t ph = 0;
@@ -631,9 +634,10 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         ph ^= 1u;
       }
     }
-    if (*abort_flag && lane == 0)   // copies in flight land before the CTA exits
+    if (lane == 0)   // copies in flight land before the CTA exits, as in the pair kernel
       for (int g = max(0, i - C::kStages); g < i; ++g)
         tc::mbar_wait(full_bar(g % C::kStages), (g / C::kStages) & 1, 1ll << 24);
+    __syncwarp();
   } else if (warp == 1) {
     const uint32_t idesc = idesc_f8_f32(128, kBT, kDx, false);
     const uint64_t adesc0 = kDx ? tc::sw128_mnmajor_desc(base, 0, 1024) : tc::sw128_kmajor_desc(base);
