@@ -199,6 +199,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   const uint32_t drain_bar = bars + 8u * (2 * kPairStages + 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kPairOffBars + 8 * (2 * kPairStages + 9));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* copied = abort_flag + 1;             // stages that warp 0 has asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
@@ -275,15 +276,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           }
         }
       }
-      // Copies in flight land before the CTA exits. Always waited for (it costs
-      // nothing where the block's sums have been taken): another warp may abort
-      // after this one has issued its last copy, and read the flag as clear.
-      // After an abort the peer's arrival, which the even CTA's barrier also
-      // counts, may not come any more (then the wait runs to its limit).
-      if (lane == 0)
-        for (int g = max(0, gs - kPairStages); g < gs; ++g)
-          tc::mbar_wait(full_bar(g % kPairStages), (g / kPairStages) & 1, 1ll << 24);
-      __syncwarp();
+      if (lane == 0) *copied = gs;
     } else if (warp == 1) {
       int slot = 0;
       uint32_t ph = 0;
@@ -506,6 +499,14 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc<2>(tmem, 512);
+    // After an abort, copies in flight land before the CTA exits. The flag is
+    // looked at here, where no role can set it any more: the copying warp may
+    // be done before another aborts. The peer's arrival, which the even CTA's
+    // barrier also counts, may not have come (the wait then runs to its limit).
+    if (*abort_flag)
+#pragma unroll 1
+      for (int n = *copied, g = max(0, n - kPairStages); g < n; ++g)
+        tc::mbar_wait(full_bar(g % kPairStages), (g / kPairStages) & 1, 1ll << 24);
   }
 }
 
@@ -567,6 +568,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   const uint32_t drain_bar = bars + 8u * (2 * C::kStages + 2 * C::kBufs + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBars + 8 * C::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* copied = abort_flag + 1;             // stages that warp 0 has asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = static_cast<int>(gridDim.x);        // the cluster
@@ -634,10 +636,7 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         ph ^= 1u;
       }
     }
-    if (lane == 0)   // copies in flight land before the CTA exits, as in the pair kernel
-      for (int g = max(0, i - C::kStages); g < i; ++g)
-        tc::mbar_wait(full_bar(g % C::kStages), (g / C::kStages) & 1, 1ll << 24);
-    __syncwarp();
+    if (lane == 0) *copied = i;
   } else if (warp == 1) {
     const uint32_t idesc = idesc_f8_f32(128, kBT, kDx, false);
     const uint64_t adesc0 = kDx ? tc::sw128_mnmajor_desc(base, 0, 1024) : tc::sw128_kmajor_desc(base);
@@ -757,6 +756,10 @@ fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc<1>(tmem, C::kTmemCols);
+    if (*abort_flag)   // copies in flight land before the CTA exits, as in the pair kernel
+#pragma unroll 1
+      for (int n = *copied, g = max(0, n - C::kStages); g < n; ++g)
+        tc::mbar_wait(full_bar(g % C::kStages), (g / C::kStages) & 1, 1ll << 24);
   }
   // own tokens x 128 columns, four columns a thread
   for (int e = threadIdx.x; e < own * 32; e += C::kThreads) {
