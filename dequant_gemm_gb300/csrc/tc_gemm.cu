@@ -378,6 +378,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant
   const uint32_t drain_bar = lut_bar + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* copied = abort_flag + 1;   // stages that the copying warp has asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // A pair is the cluster (2, 1, 1): its CTAs hold rows 128 (2 r + rank) of
@@ -584,10 +585,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant
         }
       }
     }
-    if (*abort_flag && lane == 0) {  // let copies in flight land before the CTA exits
-      for (int g = max(0, gs - kStages); g < gs; ++g)
-        tc::mbar_wait(full_bar(g % kStages), (g / kStages) & 1);
-    }
+    if (lane == 0) *copied = gs;
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA --
     // The whole warp runs the loop on warp-uniform values and one elected
@@ -906,6 +904,14 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc<kCg>(tmem, C::kTmemAlloc);
+    // After an abort, copies in flight land before the CTA exits. The flag is
+    // looked at here, where no role can set it any more: the copying warp may
+    // be done before another aborts (and waiting there in every run cost the
+    // forward 1%).
+    if (*abort_flag)
+#pragma unroll 1
+      for (int n = *copied, g = max(0, n - kStages); g < n; ++g)
+        tc::mbar_wait(full_bar(g % kStages), (g / kStages) & 1);
   }
 }
 
