@@ -499,6 +499,8 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc<2>(tmem, 512);
+    // the last commit arrives in both CTAs: the odd one stays until it has
+    if (rank != 0) tc::mbar_wait(drain_bar, 0);
     // After an abort, copies in flight land before the CTA exits. The flag is
     // looked at here, where no role can set it any more: the copying warp may
     // be done before another aborts. The peer's arrival, which the even CTA's

@@ -904,6 +904,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tm_act, const __grid_constant
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc<kCg>(tmem, C::kTmemAlloc);
+    // the last commit arrives in both CTAs of a pair: the odd one stays until it has
+    if (kPair && rank != 0) tc::mbar_wait(drain_bar, 0);
     // After an abort, copies in flight land before the CTA exits. The flag is
     // looked at here, where no role can set it any more: the copying warp may
     // be done before another aborts (and waiting there in every run cost the
