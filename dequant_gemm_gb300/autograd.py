@@ -20,6 +20,8 @@ themselves (1 x 128 blocks) before they meet the weight.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import (FP8Tensor, NF4Weight, nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd,
@@ -101,6 +103,38 @@ class NF4Linear(torch.nn.Module):
                 f"{self.qdtype}")
 
 
+class _Once(torch.autograd.Function):
+    """A gradient g that depends on `inputs`, in a way that has no gradient."""
+
+    @staticmethod
+    def forward(ctx, g, *inputs):
+        return g.view_as(g)
+
+    @staticmethod
+    def backward(ctx, gg):
+        raise RuntimeError("the RMS norm's gradients can be taken once: they are not differentiable "
+                           "themselves (second-order gradients)")
+
+
+def _once(backward):
+    """A Function's backward whose results no later backward pass may go through.
+    Under create_graph they would be constants in autograd's eyes, and a loss on
+    them would lack, without an error, all that comes of the saved tensors; so
+    they get a graph to these (which have to be the Function's own inputs or
+    outputs) and to the incoming gradients, one that raises. (torch's
+    once_differentiable does so only where the incoming gradients need one, and
+    not on the way to the Function's inputs.)"""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        inputs = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+        return tuple(None if g is None else _Once.apply(g, *inputs) for g in out)
+    return run
+
+
 class RMSNormFunction(torch.autograd.Function):
     """(y, h) with h = x + residual and y = h / rms(h) * weight, y of x's type.
     Without a residual h is not returned (None)."""
@@ -111,14 +145,17 @@ class RMSNormFunction(torch.autograd.Function):
         rows = x.reshape(-1, shape[-1]).contiguous()
         res = None if residual is None else residual.reshape(rows.shape).contiguous()
         y, h, rstd = nf4_rmsnorm_fwd(rows, weight, res, eps=eps, save_rstd=True)
-        ctx.save_for_backward(h, weight, rstd)
+        h = x if residual is None else h.reshape(shape)
+        ctx.save_for_backward(h, weight, rstd)       # h: this Function's own input or output (_once)
         ctx.x_dtype = x.dtype
         ctx.with_residual = residual is not None
-        return y.reshape(shape), (h.reshape(shape) if residual is not None else None)
+        return y.reshape(shape), (h if residual is not None else None)
 
     @staticmethod
+    @_once
     def backward(ctx, gy, gh):
         h, weight, rstd = ctx.saved_tensors
+        h = h.reshape(-1, h.shape[-1]).contiguous()
         flat = lambda g: None if g is None else g.reshape(h.shape).to(h.dtype).contiguous()  # noqa: E731
         dx, dweight = nf4_rmsnorm_bwd(flat(gy), h, weight, rstd, dh=flat(gh))
         dx = dx.reshape(gy.shape)
@@ -168,19 +205,21 @@ class NormFP8LinearsFunction(torch.autograd.Function):
         res = None if residual is None else residual.reshape(rows.shape).contiguous()
         q, h, rstd = nf4_rmsnorm_fwd(rows, norm_weight, res, eps=eps, out_dtype=torch.float8_e4m3fn,
                                      save_rstd=True)
-        ctx.save_for_backward(h, norm_weight, rstd)
+        h = x if residual is None else h.reshape(shape)
+        ctx.save_for_backward(h, norm_weight, rstd)  # h: this Function's own input or output (_once)
         ctx.weights, ctx.x_dtype, ctx.shape = weights, x.dtype, shape
         ctx.with_residual = residual is not None
         ctx.set_materialize_grads(False)     # an output that nothing used costs no product
         ys = [nf4_fp8_matmul_fwd(q, w, out_dtype=out_dtype).reshape(*shape[:-1], w.rows)
               for w in weights]
-        if residual is None:
-            h = h.clone()            # an output may not be the input itself
-        return (h.reshape(shape), *ys)
+        # an output may not be the input itself
+        return (h.clone() if residual is None else h, *ys)
 
     @staticmethod
+    @_once
     def backward(ctx, gh, *gys):
         h, norm_weight, rstd = ctx.saved_tensors
+        h = h.reshape(-1, h.shape[-1]).contiguous()
         dy = None                    # the products' input gradients, summed in fp32
         for w, g in zip(ctx.weights, gys):
             if g is not None:

@@ -1,0 +1,79 @@
+"""The autograd wrappers' own logic on CPU tensors, with the library's calls
+replaced by their formulas in torch: reshapes, casts, which gradient goes where,
+second order."""
+import types
+
+import pytest
+import torch
+
+import dequant_gemm_gb300 as nf4
+from dequant_gemm_gb300 import autograd as ag
+
+EPS = 1e-6
+
+
+def norm_fwd(x, weight, residual=None, eps=EPS, out_dtype=None, save_rstd=False, out_h=None):
+    h = x if residual is None else (x.float() + residual.float()).to(residual.dtype)
+    hd = h.double()
+    rstd = torch.rsqrt(hd.square().mean(1) + eps)
+    y = hd * rstd[:, None] * weight.double()
+    return y.to(x.dtype if out_dtype in (None, torch.float8_e4m3fn) else out_dtype), h, rstd
+
+
+def norm_bwd(dy, h, weight, rstd, dh=None):
+    g, xh, r = dy.double() * weight.double(), h.double() * rstd[:, None], rstd[:, None]
+    dx = r * (g - xh * (g * xh).mean(1, keepdim=True)) + (0 if dh is None else dh.double())
+    return dx.to(h.dtype), (dy.double() * xh).sum(0).to(weight.dtype)
+
+
+@pytest.fixture
+def formulas(monkeypatch):
+    """The library's calls as formulas; a weight is a namespace with its dense values."""
+    def fwd(x, w, out=None, out_dtype=torch.float32, accumulate=False):
+        return (x.double() @ w.dense.double().t()).to(out_dtype)
+
+    def bwd(dy, w, out=None, out_dtype=torch.float32, accumulate=False):
+        dx = (dy.double() @ w.dense.double()).to(out_dtype)
+        return out.add_(dx) if accumulate else dx
+
+    for name in ("nf4_matmul_fwd", "nf4_fp8_matmul_fwd"):
+        monkeypatch.setattr(ag, name, fwd)
+    for name in ("nf4_matmul_bwd_dx", "nf4_fp8_matmul_bwd_dx"):
+        monkeypatch.setattr(ag, name, bwd)
+    monkeypatch.setattr(ag, "nf4_fp8_quantize", lambda x, block_rows=1: x)
+    monkeypatch.setattr(ag, "nf4_rmsnorm_fwd", norm_fwd)
+    monkeypatch.setattr(ag, "nf4_rmsnorm_bwd", norm_bwd)
+
+
+def rand(*shape, seed=0, dtype=torch.float32):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+def dense(rows, cols, seed):
+    return types.SimpleNamespace(rows=rows, cols=cols, dense=rand(rows, cols, seed=seed))
+
+
+@pytest.mark.parametrize("joined", [False, True])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_second_order_of_the_norm_is_refused(formulas, joined, with_residual):
+    """The norm's gradients have no gradient of their own: a loss on them raises,
+    also where another term gives it a graph and where the incoming gradient
+    is a constant; first-order use with a graph asked for is the plain result."""
+    x, w = rand(5, 32, seed=1).requires_grad_(), rand(32, seed=2).requires_grad_()
+    res = rand(5, 32, seed=3).requires_grad_() if with_residual else None
+
+    def loss():
+        if joined:
+            h, (y,) = ag.norm_fp8_linears(x, w, [dense(16, 32, 4)], residual=res, out_dtype=torch.float32)
+        else:
+            y, h = ag.rms_norm(x, w, res)
+        return (y * rand(*y.shape, seed=5)).sum() + x.pow(3).sum()
+
+    of = [x, w] + [res] * with_residual
+    first = torch.autograd.grad(loss(), of)
+    graph = torch.autograd.grad(loss(), of, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(first, graph))
+    for g in graph:
+        for t in of:
+            with pytest.raises(RuntimeError, match="once"):
+                torch.autograd.grad(g.square().sum(), t, retain_graph=True)

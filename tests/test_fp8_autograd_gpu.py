@@ -127,3 +127,21 @@ def test_short_mma_wait_takes_the_abort_path_and_recovers(M, dx):
         nf4.nf4_set_mma_wait_limit(0)
     assert status == 7 and (site & 0xffffffff) >> 28 == (5 if dx else 4) and (site >> 24) & 15 == 2
     assert torch.equal(fn(a, w), want) and nf4.nf4_poll_device_status_site() == (0, 0)
+
+
+@pytest.mark.parametrize("joined", [False, True])
+def test_second_order_of_the_norm_is_refused(joined):
+    """Gradients asked for with a graph are the plain ones; a loss on them raises."""
+    x, nw = rand(6, 256, seed=1).requires_grad_(True), (1 + rand(256, seed=2, std=0.1)).requires_grad_(True)
+    w = nf4.nf4_fp8_quantize(rand(128, 256, seed=3, std=0.02), block_rows=128)
+
+    def loss():
+        y = norm_fp8_linears(x, nw, [w], out_dtype=torch.float32)[1][0] if joined else rms_norm(x, nw)[0]
+        return (y * rand(*y.shape, seed=4)).sum() + x.pow(3).sum()
+
+    plain = torch.autograd.grad(loss(), [x, nw])
+    graph = torch.autograd.grad(loss(), [x, nw], create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(plain, graph))
+    for g in graph:
+        with pytest.raises(RuntimeError, match="once"):
+            torch.autograd.grad(g.square().sum(), [x, nw], allow_unused=True)
