@@ -169,9 +169,30 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     return RMSNormFunction.apply(x, weight, residual, eps)
 
 
+def _fp8_input_grad(gy, weight: FP8Tensor, x_dtype, shape):
+    q = nf4_fp8_quantize(gy.reshape(-1, weight.rows).contiguous())
+    out = torch.bfloat16 if x_dtype == torch.bfloat16 else torch.float32
+    return nf4_fp8_matmul_bwd_dx(q, weight, out_dtype=out).reshape(shape).to(x_dtype)
+
+
+class FP8InputGradFunction(torch.autograd.Function):
+    """FP8LinearFunction's gradient as a function of the incoming one, to which
+    it is linear; its own gradient is the product again."""
+
+    @staticmethod
+    def forward(ctx, gy, weight: FP8Tensor, x_dtype, shape):
+        ctx.weight, ctx.gy_dtype = weight, gy.dtype
+        return _fp8_input_grad(gy, weight, x_dtype, shape)
+
+    @staticmethod
+    def backward(ctx, v):
+        return FP8LinearFunction.apply(v, ctx.weight, ctx.gy_dtype), None, None, None
+
+
 class FP8LinearFunction(torch.autograd.Function):
     """y = x · value(weight)ᵀ, x [..., cols] (fp32, bf16 or fp16) rounded to 8
-    bits, y of `out_dtype` (fp32 or bf16); differentiable in x."""
+    bits, y of `out_dtype` (fp32 or bf16); differentiable in x, any number of
+    times."""
 
     @staticmethod
     def forward(ctx, x, weight: FP8Tensor, out_dtype=torch.bfloat16):
@@ -183,10 +204,9 @@ class FP8LinearFunction(torch.autograd.Function):
     def backward(ctx, gy):
         if not ctx.needs_input_grad[0]:
             return None, None, None
-        w = ctx.weight
-        q = nf4_fp8_quantize(gy.reshape(-1, w.rows).contiguous())
-        out = torch.bfloat16 if ctx.x_dtype == torch.bfloat16 else torch.float32
-        return nf4_fp8_matmul_bwd_dx(q, w, out_dtype=out).reshape(ctx.shape).to(ctx.x_dtype), None, None
+        # under create_graph the result is a function of gy
+        grad = FP8InputGradFunction.apply if torch.is_grad_enabled() else _fp8_input_grad
+        return grad(gy, ctx.weight, ctx.x_dtype, ctx.shape), None, None
 
 
 def fp8_linear(x: torch.Tensor, weight: FP8Tensor,

@@ -77,3 +77,24 @@ def test_second_order_of_the_norm_is_refused(formulas, joined, with_residual):
         for t in of:
             with pytest.raises(RuntimeError, match="once"):
                 torch.autograd.grad(g.square().sum(), t, retain_graph=True)
+
+
+@pytest.mark.parametrize("kind", ["fp8"])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_second_order_of_the_linear_layers(formulas, kind, out_dtype):
+    """y = x W^T; for loss = sum(y^2) / 2 the gradient of <dL/dx, v> is W^T (W v),
+    each product rounded as the wrappers round it. It does not depend on x."""
+    w = dense(24, 32, 4)
+    call = ag.fp8_linear if kind == "fp8" else ag.nf4_linear
+    x, v = (rand(2, 3, 32, seed=s, dtype=torch.bfloat16) for s in (1, 2))
+    x.requires_grad_()
+    y = call(x, w, out_dtype)
+    gx, = torch.autograd.grad(y.float().square().sum() / 2, x, create_graph=True)
+    plain, = torch.autograd.grad(call(x, w, out_dtype).float().square().sum() / 2, x)
+    assert torch.equal(gx, plain) and gx.dtype == x.dtype
+    got, = torch.autograd.grad(gx, x, v, create_graph=True)
+    once = (v.double() @ w.dense.double().t()).to(out_dtype)
+    twice = once if kind == "fp8" else once.to(torch.bfloat16)
+    assert torch.equal(got, (twice.double() @ w.dense.double()).bfloat16())
+    third, = torch.autograd.grad(got.float().sum(), x, allow_unused=True)
+    assert third is None or not third.any()

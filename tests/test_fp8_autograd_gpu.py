@@ -145,3 +145,13 @@ def test_second_order_of_the_norm_is_refused(joined):
     for g in graph:
         with pytest.raises(RuntimeError, match="once"):
             torch.autograd.grad(g.square().sum(), [x, nw], allow_unused=True)
+
+
+def test_second_order_of_fp8_linear():
+    """The gradient of <dL/dx, v> for L = sum(y^2) / 2 is dX(Y(v)), from the same calls."""
+    w = nf4.nf4_fp8_quantize(rand(384, 528, seed=1, std=0.02), block_rows=128)
+    x, v = rand(6, 528, seed=2, dtype=torch.bfloat16).requires_grad_(True), rand(6, 528, seed=3, dtype=torch.bfloat16)
+    gx, = torch.autograd.grad(fp8_linear(x, w).float().square().sum() / 2, x, create_graph=True)
+    got, = torch.autograd.grad(gx, x, v)
+    u = nf4.nf4_fp8_matmul_fwd(nf4.nf4_fp8_quantize(v), w, out_dtype=torch.bfloat16)
+    assert torch.equal(got, nf4.nf4_fp8_matmul_bwd_dx(nf4.nf4_fp8_quantize(u), w, out_dtype=torch.bfloat16))
