@@ -29,9 +29,31 @@ from . import (FP8Tensor, NF4Weight, nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd,
                nf4_rmsnorm_bwd, nf4_rmsnorm_fwd)
 
 
+def _nf4_input_grad(gy, weight: NF4Weight, x_dtype, lead):
+    gy2 = gy.reshape(-1, weight.rows).to(x_dtype).contiguous()
+    # a bf16 input gets its gradient straight from the kernel's bf16 output
+    out = torch.bfloat16 if x_dtype == torch.bfloat16 else torch.float32
+    gx = nf4_matmul_bwd_dx(gy2, weight, out_dtype=out)
+    return gx.reshape(*lead, weight.cols).to(x_dtype)
+
+
+class NF4InputGradFunction(torch.autograd.Function):
+    """NF4LinearFunction's gradient as a function of the incoming one, to which
+    it is linear; its own gradient is the product again."""
+
+    @staticmethod
+    def forward(ctx, gy, weight: NF4Weight, x_dtype, lead):
+        ctx.weight, ctx.gy_dtype = weight, gy.dtype
+        return _nf4_input_grad(gy, weight, x_dtype, lead)
+
+    @staticmethod
+    def backward(ctx, v):
+        return NF4LinearFunction.apply(v, ctx.weight, ctx.gy_dtype), None, None, None
+
+
 class NF4LinearFunction(torch.autograd.Function):
     """y = x · dequant(W)ᵀ for bf16 or fp16 x [..., cols] -> y [..., rows] of
-    `out_dtype` (fp32 or bf16)."""
+    `out_dtype` (fp32 or bf16); differentiable in x, any number of times."""
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, weight: NF4Weight,
@@ -51,12 +73,9 @@ class NF4LinearFunction(torch.autograd.Function):
     def backward(ctx, gy: torch.Tensor):
         if not ctx.needs_input_grad[0]:
             return None, None, None
-        w = ctx.weight
-        gy2 = gy.reshape(-1, w.rows).to(ctx.x_dtype).contiguous()
-        # a bf16 input gets its gradient straight from the kernel's bf16 output
-        out = torch.bfloat16 if ctx.x_dtype == torch.bfloat16 else torch.float32
-        gx = nf4_matmul_bwd_dx(gy2, w, out_dtype=out)
-        return gx.reshape(*ctx.lead, w.cols).to(ctx.x_dtype), None, None
+        # under create_graph the result is a function of gy
+        grad = NF4InputGradFunction.apply if torch.is_grad_enabled() else _nf4_input_grad
+        return grad(gy, ctx.weight, ctx.x_dtype, ctx.lead), None, None
 
 
 def nf4_linear(x: torch.Tensor, weight: NF4Weight,

@@ -12,6 +12,7 @@ from dequant_gemm_gb300 import autograd as ag
 EPS = 1e-6
 
 
+@torch.no_grad()          # as the library, which autograd does not see into
 def norm_fwd(x, weight, residual=None, eps=EPS, out_dtype=None, save_rstd=False, out_h=None):
     h = x if residual is None else (x.float() + residual.float()).to(residual.dtype)
     hd = h.double()
@@ -20,6 +21,7 @@ def norm_fwd(x, weight, residual=None, eps=EPS, out_dtype=None, save_rstd=False,
     return y.to(x.dtype if out_dtype in (None, torch.float8_e4m3fn) else out_dtype), h, rstd
 
 
+@torch.no_grad()
 def norm_bwd(dy, h, weight, rstd, dh=None):
     g, xh, r = dy.double() * weight.double(), h.double() * rstd[:, None], rstd[:, None]
     dx = r * (g - xh * (g * xh).mean(1, keepdim=True)) + (0 if dh is None else dh.double())
@@ -29,9 +31,11 @@ def norm_bwd(dy, h, weight, rstd, dh=None):
 @pytest.fixture
 def formulas(monkeypatch):
     """The library's calls as formulas; a weight is a namespace with its dense values."""
+    @torch.no_grad()
     def fwd(x, w, out=None, out_dtype=torch.float32, accumulate=False):
         return (x.double() @ w.dense.double().t()).to(out_dtype)
 
+    @torch.no_grad()
     def bwd(dy, w, out=None, out_dtype=torch.float32, accumulate=False):
         dx = (dy.double() @ w.dense.double()).to(out_dtype)
         return out.add_(dx) if accumulate else dx
@@ -79,7 +83,7 @@ def test_second_order_of_the_norm_is_refused(formulas, joined, with_residual):
                 torch.autograd.grad(g.square().sum(), t, retain_graph=True)
 
 
-@pytest.mark.parametrize("kind", ["fp8"])
+@pytest.mark.parametrize("kind", ["fp8", "nf4"])
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
 def test_second_order_of_the_linear_layers(formulas, kind, out_dtype):
     """y = x W^T; for loss = sum(y^2) / 2 the gradient of <dL/dx, v> is W^T (W v),
@@ -98,3 +102,14 @@ def test_second_order_of_the_linear_layers(formulas, kind, out_dtype):
     assert torch.equal(got, (twice.double() @ w.dense.double()).bfloat16())
     third, = torch.autograd.grad(got.float().sum(), x, allow_unused=True)
     assert third is None or not third.any()
+
+
+def test_second_order_of_nf4_linear_in_fp16(formulas):
+    """An fp16 input: the gradient's own gradient has the output's type again."""
+    w = dense(16, 64, 1)
+    x, v = (rand(3, 64, seed=s, dtype=torch.float16) for s in (2, 3))
+    x.requires_grad_()
+    gx, = torch.autograd.grad(ag.nf4_linear(x, w).square().sum() / 2, x, create_graph=True)
+    got, = torch.autograd.grad(gx, x, v)
+    once = (v.double() @ w.dense.double().t()).float().half()
+    assert torch.equal(got, (once.double() @ w.dense.double()).float().half())
