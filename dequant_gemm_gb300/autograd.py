@@ -84,6 +84,26 @@ def nf4_linear(x: torch.Tensor, weight: NF4Weight,
     return NF4LinearFunction.apply(x, weight, out_dtype)
 
 
+class _Frozen(torch.nn.Module):
+    """A layer whose buffers named in `_frozen` keep their types and bits when the
+    module is converted to another type (.to(dtype), .half() and the like, which
+    would round codes and scales): they only move."""
+    _frozen = ()
+
+    def _apply(self, fn, recurse=True):
+        kept = {n: self._buffers[n] for n in self._frozen if self._buffers.get(n) is not None}
+        as_bits = {n: t.view({1: torch.uint8, 4: torch.int32}[t.element_size()]) for n, t in kept.items()}
+        self._buffers.update(as_bits)        # whole numbers: not converted with floating-point types
+        try:
+            super()._apply(fn, recurse)
+            for n, t in as_bits.items():
+                moved = self._buffers[n]     # .type(dtype) converts whole numbers too
+                kept[n] = (moved if moved.dtype == t.dtype else t.to(moved.device)).view(kept[n].dtype)
+        finally:
+            self._buffers.update(kept)
+        return self
+
+
 class NF4Linear(torch.nn.Module):
     """A frozen linear layer (no bias) holding its weight quantized (NF4 by
     default; "fp4" or "int8" on request).
@@ -280,9 +300,11 @@ def norm_fp8_linears(x: torch.Tensor, norm_weight: torch.Tensor, weights, residu
     return h, ys
 
 
-class FP8Linear(torch.nn.Module):
+class FP8Linear(_Frozen):
     """A frozen linear layer (no bias) holding its weight in 8 bits, with a
-    scale for each 128 x 128 block. Codes and scales are buffers."""
+    scale for each 128 x 128 block. Codes and scales are buffers, which no
+    conversion of the module changes."""
+    _frozen = ("codes", "scale")
 
     def __init__(self, weight: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16):
         super().__init__()

@@ -113,3 +113,38 @@ def test_second_order_of_nf4_linear_in_fp16(formulas):
     got, = torch.autograd.grad(gx, x, v)
     once = (v.double() @ w.dense.double().t()).float().half()
     assert torch.equal(got, (once.double() @ w.dense.double()).float().half())
+
+
+def test_fp8_layer_keeps_its_buffers_types(monkeypatch):
+    """A model converted to another type, moved or saved: codes and scales are
+    neither parameters nor values of that type, and keep every bit."""
+    def quantize(x, block_rows=1, out=None):
+        assert block_rows == 128
+        q = nf4.alloc_fp8(*x.shape, x.device, 128)
+        q.codes.copy_(x), q.scale.copy_(rand(*q.scale.shape, seed=9))
+        return q
+
+    monkeypatch.setattr(ag, "nf4_fp8_quantize", quantize)
+    layer = ag.FP8Linear(rand(160, 256, seed=1))
+    codes, scale = layer.codes.view(torch.uint8).clone(), layer.scale.clone()
+    model = torch.nn.Sequential(layer, torch.nn.Linear(160, 8))
+
+    def same():
+        w = layer.quantized_weight()
+        return (w.codes.dtype == torch.float8_e4m3fn and torch.equal(w.codes.view(torch.uint8), codes)
+                and torch.equal(w.scale, scale) and w.block_rows == 128)
+
+    for convert in (lambda m: m.bfloat16(), lambda m: m.half(), lambda m: m.float(), lambda m: m.double(),
+                    lambda m: m.to(torch.bfloat16), lambda m: m.to("cpu", torch.float16),
+                    lambda m: m.type(torch.float32), lambda m: m.share_memory()):
+        convert(model)
+        assert same()
+    assert model[1].weight.dtype == torch.float32
+    state = {k: v.clone() for k, v in layer.state_dict().items()}
+    assert {k: v.dtype for k, v in state.items()} == {"codes": torch.float8_e4m3fn, "scale": torch.float32}
+    layer.codes.view(torch.uint8).zero_(), layer.scale.zero_()
+    layer.load_state_dict(state)
+    assert same()
+    meta = layer.to("meta")
+    assert meta.codes.device.type == "meta" and meta.codes.dtype == torch.float8_e4m3fn
+    assert meta.scale.dtype == torch.float32

@@ -155,3 +155,15 @@ def test_second_order_of_fp8_linear():
     got, = torch.autograd.grad(gx, x, v)
     u = nf4.nf4_fp8_matmul_fwd(nf4.nf4_fp8_quantize(v), w, out_dtype=torch.bfloat16)
     assert torch.equal(got, nf4.nf4_fp8_matmul_bwd_dx(nf4.nf4_fp8_quantize(u), w, out_dtype=torch.bfloat16))
+
+
+def test_fp8_layer_in_a_converted_model():
+    """A model taken to bf16, moved away and back: the layer gives the same bits."""
+    layer = FP8Linear(rand(384, 528, seed=1, std=0.02))
+    x = rand(5, 528, seed=2, dtype=torch.bfloat16)
+    want = layer(x)
+    model = torch.nn.Sequential(layer, torch.nn.Linear(384, 16, device=DEV))
+    for convert in (lambda m: m.bfloat16(), lambda m: m.half(), lambda m: m.cpu().to(DEV), lambda m: m.float()):
+        convert(model)
+        assert torch.equal(layer(x), want)
+    assert torch.equal(model.bfloat16()(x), model[1](want))
