@@ -104,12 +104,14 @@ class _Frozen(torch.nn.Module):
         return self
 
 
-class NF4Linear(torch.nn.Module):
+class NF4Linear(_Frozen):
     """A frozen linear layer (no bias) holding its weight quantized (NF4 by
     default; "fp4" or "int8" on request).
 
     The codes and scales are buffers: they move with the module and are saved
-    in its state dict, and no optimizer sees them."""
+    in its state dict, no optimizer sees them and no conversion of the module
+    changes them."""
+    _frozen = ("codes", "absmax_q", "absmax_scale")
 
     def __init__(self, weight: torch.Tensor, dtype: str = "nf4",
                  out_dtype: torch.dtype = torch.float32):

@@ -148,3 +148,24 @@ def test_fp8_layer_keeps_its_buffers_types(monkeypatch):
     meta = layer.to("meta")
     assert meta.codes.device.type == "meta" and meta.codes.dtype == torch.float8_e4m3fn
     assert meta.scale.dtype == torch.float32
+
+
+@pytest.mark.parametrize("dtype", ["nf4", "fp4", "int8"])
+def test_nf4_layer_keeps_its_buffers_types(monkeypatch, dtype):
+    """The same of the layer over 4-bit and int8 weights."""
+    def quantize(W, out=None, dtype="nf4"):
+        q = nf4.alloc_weight(*W.shape, W.device, dtype)
+        q.codes.copy_(torch.arange(q.codes.numel()) % 100), q.absmax_scale.copy_(rand(*q.absmax_scale.shape, seed=9))
+        if q.absmax_q is not None:
+            q.absmax_q.copy_(torch.arange(q.absmax_q.numel()) % 200)
+        return q
+
+    monkeypatch.setattr(ag, "nf4_quantize", quantize)
+    layer = ag.NF4Linear(rand(48, 128, seed=1), dtype=dtype)
+    before = {k: v.clone() for k, v in layer.state_dict().items()}
+    for convert in (lambda m: m.bfloat16(), lambda m: m.double(), lambda m: m.type(torch.float16), lambda m: m.to("cpu")):
+        convert(torch.nn.Sequential(layer))
+        now = layer.state_dict()
+        assert now.keys() == before.keys()
+        assert all(v.dtype == before[k].dtype and torch.equal(v, before[k]) for k, v in now.items())
+        assert layer.quantized_weight().absmax_scale is layer.absmax_scale
