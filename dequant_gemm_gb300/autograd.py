@@ -29,8 +29,20 @@ from . import (FP8Tensor, NF4Weight, nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd,
                nf4_rmsnorm_bwd, nf4_rmsnorm_fwd)
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and on a 16-byte boundary, as the kernels take it: a row slice
+    of an odd width, as autograd itself passes them, need not start on one."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _matrix(t: torch.Tensor, cols: int) -> torch.Tensor:
+    """t's rows of `cols` values as a matrix for the kernels."""
+    return _aligned(t.reshape(-1, cols))
+
+
 def _nf4_input_grad(gy, weight: NF4Weight, x_dtype, lead):
-    gy2 = gy.reshape(-1, weight.rows).to(x_dtype).contiguous()
+    gy2 = _aligned(gy.reshape(-1, weight.rows).to(x_dtype))
     # a bf16 input gets its gradient straight from the kernel's bf16 output
     out = torch.bfloat16 if x_dtype == torch.bfloat16 else torch.float32
     gx = nf4_matmul_bwd_dx(gy2, weight, out_dtype=out)
@@ -63,7 +75,7 @@ class NF4LinearFunction(torch.autograd.Function):
         if x.shape[-1] != weight.cols:
             raise ValueError(f"x must end in {weight.cols} features, got {tuple(x.shape)}")
         lead = x.shape[:-1]
-        y = nf4_matmul_fwd(x.reshape(-1, weight.cols).contiguous(), weight, out_dtype=out_dtype)
+        y = nf4_matmul_fwd(_matrix(x, weight.cols), weight, out_dtype=out_dtype)
         ctx.weight = weight
         ctx.lead = lead
         ctx.x_dtype = x.dtype
@@ -121,7 +133,7 @@ class NF4Linear(_Frozen):
         w = weight.detach()
         if w.dtype not in (torch.float32, torch.bfloat16):
             w = w.to(torch.float32)
-        q = nf4_quantize(w.contiguous(), dtype=dtype)
+        q = nf4_quantize(_aligned(w), dtype=dtype)
         self.register_buffer("codes", q.codes)
         if q.absmax_q is not None:
             self.register_buffer("absmax_q", q.absmax_q)
@@ -183,9 +195,9 @@ class RMSNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual=None, eps=1e-6):
         shape = x.shape
-        rows = x.reshape(-1, shape[-1]).contiguous()
-        res = None if residual is None else residual.reshape(rows.shape).contiguous()
-        y, h, rstd = nf4_rmsnorm_fwd(rows, weight, res, eps=eps, save_rstd=True)
+        rows = _matrix(x, shape[-1])
+        res = None if residual is None else _aligned(residual.reshape(rows.shape))
+        y, h, rstd = nf4_rmsnorm_fwd(rows, _aligned(weight), res, eps=eps, save_rstd=True)
         h = x if residual is None else h.reshape(shape)
         ctx.save_for_backward(h, weight, rstd)       # h: this Function's own input or output (_once)
         ctx.x_dtype = x.dtype
@@ -196,9 +208,9 @@ class RMSNormFunction(torch.autograd.Function):
     @_once
     def backward(ctx, gy, gh):
         h, weight, rstd = ctx.saved_tensors
-        h = h.reshape(-1, h.shape[-1]).contiguous()
-        flat = lambda g: None if g is None else g.reshape(h.shape).to(h.dtype).contiguous()  # noqa: E731
-        dx, dweight = nf4_rmsnorm_bwd(flat(gy), h, weight, rstd, dh=flat(gh))
+        h = _matrix(h, h.shape[-1])
+        flat = lambda g: None if g is None else _aligned(g.reshape(h.shape).to(h.dtype))  # noqa: E731
+        dx, dweight = nf4_rmsnorm_bwd(flat(gy), h, _aligned(weight), rstd, dh=flat(gh))
         dx = dx.reshape(gy.shape)
         return dx.to(ctx.x_dtype), dweight, (dx if ctx.with_residual else None), None
 
@@ -211,7 +223,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
 
 
 def _fp8_input_grad(gy, weight: FP8Tensor, x_dtype, shape):
-    q = nf4_fp8_quantize(gy.reshape(-1, weight.rows).contiguous())
+    q = nf4_fp8_quantize(_matrix(gy, weight.rows))
     out = torch.bfloat16 if x_dtype == torch.bfloat16 else torch.float32
     return nf4_fp8_matmul_bwd_dx(q, weight, out_dtype=out).reshape(shape).to(x_dtype)
 
@@ -238,7 +250,7 @@ class FP8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight: FP8Tensor, out_dtype=torch.bfloat16):
         ctx.weight, ctx.x_dtype, ctx.shape = weight, x.dtype, x.shape
-        q = nf4_fp8_quantize(x.reshape(-1, x.shape[-1]).contiguous())
+        q = nf4_fp8_quantize(_matrix(x, x.shape[-1]))
         return nf4_fp8_matmul_fwd(q, weight, out_dtype=out_dtype).reshape(*x.shape[:-1], weight.rows)
 
     @staticmethod
@@ -262,10 +274,10 @@ class NormFP8LinearsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, norm_weight, residual, eps, out_dtype, *weights):
         shape = x.shape
-        rows = x.reshape(-1, shape[-1]).contiguous()
-        res = None if residual is None else residual.reshape(rows.shape).contiguous()
-        q, h, rstd = nf4_rmsnorm_fwd(rows, norm_weight, res, eps=eps, out_dtype=torch.float8_e4m3fn,
-                                     save_rstd=True)
+        rows = _matrix(x, shape[-1])
+        res = None if residual is None else _aligned(residual.reshape(rows.shape))
+        q, h, rstd = nf4_rmsnorm_fwd(rows, _aligned(norm_weight), res, eps=eps,
+                                     out_dtype=torch.float8_e4m3fn, save_rstd=True)
         h = x if residual is None else h.reshape(shape)
         ctx.save_for_backward(h, norm_weight, rstd)  # h: this Function's own input or output (_once)
         ctx.weights, ctx.x_dtype, ctx.shape = weights, x.dtype, shape
@@ -280,15 +292,15 @@ class NormFP8LinearsFunction(torch.autograd.Function):
     @_once
     def backward(ctx, gh, *gys):
         h, norm_weight, rstd = ctx.saved_tensors
-        h = h.reshape(-1, h.shape[-1]).contiguous()
+        h = _matrix(h, h.shape[-1])
         dy = None                    # the products' input gradients, summed in fp32
         for w, g in zip(ctx.weights, gys):
             if g is not None:
-                q = nf4_fp8_quantize(g.reshape(-1, w.rows).contiguous())
+                q = nf4_fp8_quantize(_matrix(g, w.rows))
                 dy = nf4_fp8_matmul_bwd_dx(q, w, out=dy, accumulate=dy is not None)
         dy = torch.zeros_like(h) if dy is None else dy.to(h.dtype)
-        dh = None if gh is None else gh.reshape(h.shape).to(h.dtype).contiguous()
-        dx, dweight = nf4_rmsnorm_bwd(dy, h, norm_weight, rstd, dh=dh)
+        dh = None if gh is None else _aligned(gh.reshape(h.shape).to(h.dtype))
+        dx, dweight = nf4_rmsnorm_bwd(dy, h, _aligned(norm_weight), rstd, dh=dh)
         dx = dx.reshape(ctx.shape)
         return (dx.to(ctx.x_dtype), dweight, dx if ctx.with_residual else None, None, None,
                 *[None] * len(ctx.weights))
@@ -312,7 +324,7 @@ class FP8Linear(_Frozen):
         super().__init__()
         if weight.dim() != 2:
             raise ValueError("weight must be 2-D [out_features, in_features]")
-        q = nf4_fp8_quantize(weight.detach().contiguous(), block_rows=128)
+        q = nf4_fp8_quantize(_aligned(weight.detach()), block_rows=128)
         self.register_buffer("codes", q.codes)
         self.register_buffer("scale", q.scale)
         self.out_features, self.in_features = q.rows, q.cols

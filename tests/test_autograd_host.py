@@ -169,3 +169,61 @@ def test_nf4_layer_keeps_its_buffers_types(monkeypatch, dtype):
         assert now.keys() == before.keys()
         assert all(v.dtype == before[k].dtype and torch.equal(v, before[k]) for k, v in now.items())
         assert layer.quantized_weight().absmax_scale is layer.absmax_scale
+
+
+def unaligned(*shape, seed=0, dtype=torch.float32):
+    """A contiguous tensor that starts off a 16-byte boundary, as a row slice may."""
+    n = 1
+    for s in shape:
+        n *= s
+    t = rand(n + 1, seed=seed, dtype=dtype)[1:].view(shape)
+    assert t.is_contiguous() and t.data_ptr() % 16
+    return t
+
+
+@pytest.mark.parametrize("cols, dtype", [(100, torch.bfloat16), (41, torch.float32)])
+def test_norm_takes_tensors_off_the_16_byte_grid(formulas, monkeypatch, cols, dtype):
+    """Row slices of odd widths, and gradients that come as slices of a larger
+    one, reach the kernels on 16-byte boundaries, whatever their offset."""
+    def strict(fn):
+        def call(*args, **kw):
+            for t in (*args, *kw.values()):
+                assert not isinstance(t, torch.Tensor) or t.data_ptr() % 16 == 0 and t.is_contiguous()
+            return fn(*args, **kw)
+        return call
+
+    for name in ("nf4_rmsnorm_fwd", "nf4_rmsnorm_bwd", "nf4_fp8_quantize", "nf4_matmul_fwd", "nf4_matmul_bwd_dx"):
+        monkeypatch.setattr(ag, name, strict(getattr(ag, name)))
+    x, res = unaligned(6, cols, seed=1, dtype=dtype), unaligned(6, cols, seed=2)
+    w = unaligned(cols, seed=3)
+    gy, gh = unaligned(6, cols, seed=4, dtype=dtype), unaligned(6, cols, seed=5)
+    got, want = [], []
+    for out, tensors in ((got, (x, w, res, gy, gh)), (want, [t.clone() for t in (x, w, res, gy, gh)])):
+        x_, w_, r_ = (t.detach().requires_grad_() for t in tensors[:3])
+        y, h = ag.rms_norm(x_, w_, r_)
+        y2, _ = ag.rms_norm(x_, w_)
+        out += [y, h, y2, *torch.autograd.grad([y, h, y2], [x_, w_, r_], [tensors[3], tensors[4], tensors[3]])]
+        h, ys = ag.norm_fp8_linears(x_, w_, [dense(33, cols, 6), dense(9, cols, 7)], residual=r_, out_dtype=torch.float32)
+        g = unaligned(6, 33, seed=8)
+        out += [h, *ys, *torch.autograd.grad([h, ys[0], ys[1]], [x_, w_, r_], [tensors[4], g, g[:, :9]])]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_linear_layers_take_tensors_off_the_16_byte_grid(formulas, monkeypatch):
+    def strict(t):
+        assert t.data_ptr() % 16 == 0 and t.is_contiguous()
+        return t
+
+    quantize, fwd, bwd = ag.nf4_fp8_quantize, ag.nf4_matmul_fwd, ag.nf4_matmul_bwd_dx
+    monkeypatch.setattr(ag, "nf4_fp8_quantize", lambda x, **kw: quantize(strict(x), **kw))
+    monkeypatch.setattr(ag, "nf4_matmul_fwd", lambda x, w, **kw: fwd(strict(x), w, **kw))
+    monkeypatch.setattr(ag, "nf4_matmul_bwd_dx", lambda x, w, **kw: bwd(strict(x), w, **kw))
+    w = dense(50, 64, 4)
+    for call in (ag.fp8_linear, ag.nf4_linear):
+        x = unaligned(5, 64, seed=1, dtype=torch.bfloat16).requires_grad_()
+        g = unaligned(5, 50, seed=2, dtype=torch.bfloat16)
+        y = call(x, w, torch.bfloat16)
+        gx, = torch.autograd.grad(y, x, g)
+        x2 = x.detach().clone().requires_grad_()
+        y2 = call(x2, w, torch.bfloat16)
+        assert torch.equal(y, y2) and torch.equal(gx, torch.autograd.grad(y2, x2, g.clone())[0])

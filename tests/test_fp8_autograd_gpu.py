@@ -167,3 +167,29 @@ def test_fp8_layer_in_a_converted_model():
         convert(model)
         assert torch.equal(layer(x), want)
     assert torch.equal(model.bfloat16()(x), model[1](want))
+
+
+@pytest.mark.parametrize("cols, dtype", [(100, torch.bfloat16), (5001, torch.float32)])
+def test_norm_of_row_slices_of_odd_widths(cols, dtype):
+    """x[1:] starts off a 16-byte boundary, and so do gradients that come back as
+    slices: the same bits as of copies, forward and backward."""
+    x, s, w = rand(9, cols, seed=1, dtype=dtype), rand(9, cols, seed=2), 1 + rand(cols + 1, seed=3, std=0.1)
+    gy, gh = rand(9, cols, seed=4, dtype=dtype), rand(9, cols, seed=5)
+    got = []
+    for part in (lambda t: t[1:], lambda t: t[1:].clone()):
+        x_, s_, w_ = (part(t).detach().requires_grad_() for t in (x, s, w))
+        y, h = rms_norm(x_, w_, s_)
+        got.append([y, h, *torch.autograd.grad([y, h], [x_, s_, w_], [part(gy), part(gh)])])
+    assert x[1:].data_ptr() % 16 and all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_gradients_as_slices_of_a_concatenation():
+    """torch.cat hands its parts' gradients back as slices, here 200 bytes in."""
+    x, w = rand(1, 100, seed=1).requires_grad_(True), torch.ones(100, device=DEV)
+    parts = [rms_norm((x * k), w)[0].bfloat16() for k in (1.0, 2.0, 3.0)]
+    torch.cat(parts).float().square().sum().backward()
+    assert x.grad.isfinite().all()
+    lead = rand(3, 528, seed=2, dtype=torch.bfloat16).requires_grad_(True)
+    fw = nf4.nf4_fp8_quantize(rand(144, 528, seed=3, std=0.02), block_rows=128)
+    torch.cat([fp8_linear(lead[:1], fw).float(), fp8_linear(lead[1:], fw).float()]).sum().backward()
+    assert lead.grad.isfinite().all()
