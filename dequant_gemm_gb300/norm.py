@@ -4,7 +4,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (ELEM, _call_on, _require, _require_cuda_device, _same_device, lib)
+from . import (ELEM, NF4Error, _call_on, _require, _require_cuda_device, _same_device, lib)
 from .fp8 import FP8_BLOCK, FP8_DTYPE, FP8Tensor
 
 
@@ -53,6 +53,16 @@ def _like(t, h) -> bool:
             and t.is_contiguous() and t.device == h.device)
 
 
+def _refused(error: NF4Error, **tensors):
+    """Raises ValueError with the name of the operand that a call was refused for
+    where that is its alignment, else the call's own error."""
+    for name, t in tensors.items():
+        if error.status == 3 and t is not None and t.data_ptr() % 16:
+            raise ValueError(f"{name} must start on a 16-byte boundary (a row slice of an odd width "
+                             f"need not: clone it)") from error
+    raise error
+
+
 def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
                     eps: float = 1e-6, out_dtype: torch.dtype | None = None,
                     save_rstd: bool = False, out_h: torch.Tensor | None = None):
@@ -64,7 +74,8 @@ def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
     torch.float8_e4m3fn, which makes y an FP8Tensor in 1 x 128 blocks (cols a
     multiple of 16). rstd (fp32 [rows]) is what the backward needs, None
     unless save_rstd. out_h: where to write h; the residual itself may be
-    given, to update the stream in place."""
+    given, to update the stream in place. Every tensor is contiguous and starts
+    on a 16-byte boundary, which a row slice of an odd width need not."""
     if not _plain_matrix(x, weight) or residual is not None and not (
             isinstance(residual, torch.Tensor) and residual.shape == x.shape
             and (residual.dtype is x.dtype or residual.dtype is torch.float32)
@@ -99,9 +110,12 @@ def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
     else:
         y = _empty((rows, cols), dtype=out_dtype, device=device)
         y_ptr, y_elem, scale_ptr = y.data_ptr(), ELEM[out_dtype], None
-    _call_on(device.index, "nf4_rmsnorm_fwd", x.data_ptr(), ELEM[x.dtype], res_ptr, ELEM[h.dtype],
-             weight.data_ptr(), ELEM[weight.dtype], rows, cols, eps, h_ptr, y_ptr, y_elem, scale_ptr,
-             None if rstd is None else rstd.data_ptr())
+    try:
+        _call_on(device.index, "nf4_rmsnorm_fwd", x.data_ptr(), ELEM[x.dtype], res_ptr, ELEM[h.dtype],
+                 weight.data_ptr(), ELEM[weight.dtype], rows, cols, eps, h_ptr, y_ptr, y_elem, scale_ptr,
+                 None if rstd is None else rstd.data_ptr())
+    except NF4Error as error:
+        _refused(error, x=x, weight=weight, residual=residual, out_h=out_h)
     return y, h, rstd
 
 
@@ -111,7 +125,8 @@ def nf4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rst
     type, the gradient of x and of the residual alike, dweight of weight's. dy
     is the gradient of y and dh (optional) the one that reaches h from the
     residual stream, both of h's type; h and rstd as the forward returned
-    them. An 8-bit y passes its gradient through."""
+    them. An 8-bit y passes its gradient through. Every tensor is contiguous
+    and (rstd apart) starts on a 16-byte boundary."""
     if not _plain_matrix(h, weight):
         _check_norm(h, "h", weight)
     rows, cols = h.shape
@@ -129,8 +144,11 @@ def nf4_rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rst
     dx, dweight = torch.empty_like(h), torch.empty_like(weight)
     size = lib().nf4_rmsnorm_bwd_workspace(rows, cols)
     work = _empty(size, dtype=torch.uint8, device=device)
-    _call_on(device.index, "nf4_rmsnorm_bwd", dy.data_ptr(), h.data_ptr(),
-             None if dh is None else dh.data_ptr(), ELEM[h.dtype], weight.data_ptr(),
-             ELEM[weight.dtype], rstd.data_ptr(), rows, cols, dx.data_ptr(), dweight.data_ptr(),
-             work.data_ptr(), size)
+    try:
+        _call_on(device.index, "nf4_rmsnorm_bwd", dy.data_ptr(), h.data_ptr(),
+                 None if dh is None else dh.data_ptr(), ELEM[h.dtype], weight.data_ptr(),
+                 ELEM[weight.dtype], rstd.data_ptr(), rows, cols, dx.data_ptr(), dweight.data_ptr(),
+                 work.data_ptr(), size)
+    except NF4Error as error:
+        _refused(error, dy=dy, h=h, weight=weight, dh=dh)
     return dx, dweight
