@@ -201,7 +201,7 @@ class RMSNormFunction(torch.autograd.Function):
         h = x if residual is None else h.reshape(shape)
         ctx.save_for_backward(h, weight, rstd)       # h: this Function's own input or output (_once)
         ctx.x_dtype = x.dtype
-        ctx.with_residual = residual is not None
+        ctx.res_shape = None if residual is None else residual.shape
         return y.reshape(shape), (h if residual is not None else None)
 
     @staticmethod
@@ -212,7 +212,7 @@ class RMSNormFunction(torch.autograd.Function):
         flat = lambda g: None if g is None else _aligned(g.reshape(h.shape).to(h.dtype))  # noqa: E731
         dx, dweight = nf4_rmsnorm_bwd(flat(gy), h, _aligned(weight), rstd, dh=flat(gh))
         dx = dx.reshape(gy.shape)
-        return dx.to(ctx.x_dtype), dweight, (dx if ctx.with_residual else None), None
+        return dx.to(ctx.x_dtype), dweight, (dx.reshape(ctx.res_shape) if ctx.res_shape else None), None
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
@@ -281,7 +281,7 @@ class NormFP8LinearsFunction(torch.autograd.Function):
         h = x if residual is None else h.reshape(shape)
         ctx.save_for_backward(h, norm_weight, rstd)  # h: this Function's own input or output (_once)
         ctx.weights, ctx.x_dtype, ctx.shape = weights, x.dtype, shape
-        ctx.with_residual = residual is not None
+        ctx.res_shape = None if residual is None else residual.shape
         ctx.set_materialize_grads(False)     # an output that nothing used costs no product
         ys = [nf4_fp8_matmul_fwd(q, w, out_dtype=out_dtype).reshape(*shape[:-1], w.rows)
               for w in weights]
@@ -302,7 +302,7 @@ class NormFP8LinearsFunction(torch.autograd.Function):
         dh = None if gh is None else _aligned(gh.reshape(h.shape).to(h.dtype))
         dx, dweight = nf4_rmsnorm_bwd(dy, h, _aligned(norm_weight), rstd, dh=dh)
         dx = dx.reshape(ctx.shape)
-        return (dx.to(ctx.x_dtype), dweight, dx if ctx.with_residual else None, None, None,
+        return (dx.to(ctx.x_dtype), dweight, dx.reshape(ctx.res_shape) if ctx.res_shape else None, None, None,
                 *[None] * len(ctx.weights))
 
 

@@ -227,3 +227,22 @@ def test_linear_layers_take_tensors_off_the_16_byte_grid(formulas, monkeypatch):
         x2 = x.detach().clone().requires_grad_()
         y2 = call(x2, w, torch.bfloat16)
         assert torch.equal(y, y2) and torch.equal(gx, torch.autograd.grad(y2, x2, g.clone())[0])
+
+
+@pytest.mark.parametrize("joined", [False, True])
+def test_residual_in_another_shape(formulas, joined):
+    """A stream held as [tokens, width] beside x [batch, length, width]: its
+    gradient has its own shape."""
+    x, s, w = rand(2, 3, 32, seed=1, dtype=torch.bfloat16), rand(6, 32, seed=2), rand(32, seed=3)
+    got = []
+    for stream in (s, s.view(2, 3, 32)):
+        x_, s_, w_ = (t.detach().clone().requires_grad_() for t in (x, stream, w))
+        if joined:
+            h, (y,) = ag.norm_fp8_linears(x_, w_, [dense(16, 32, 4)], residual=s_, out_dtype=torch.float32)
+        else:
+            y, h = ag.rms_norm(x_, w_, s_)
+        assert h.shape == x.shape
+        (h.square().sum() + y.float().sum()).backward()
+        got.append([x_.grad, s_.grad.view(6, 32), w_.grad])
+        assert s_.grad.shape == stream.shape
+    assert all(torch.equal(a, b) for a, b in zip(*got))
