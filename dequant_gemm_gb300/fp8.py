@@ -29,7 +29,9 @@ _empty, _byref = torch.empty, ctypes.byref
 class FP8Tensor:
     """codes float8_e4m3fn [rows, cols], scale float32
     [ceil(rows / block_rows), ceil(cols / 128)]; block_rows is 1 (activations,
-    gradients) or 128 (weights). Plain tensors; save them with torch.save."""
+    gradients) or 128 (weights). Plain tensors; save them with torch.save.
+    Scales may have either sign; a product multiplies two of them first, which
+    has to stay 0 or of magnitude 2^-126 to 2^128."""
     codes: torch.Tensor
     scale: torch.Tensor
     block_rows: int = 1

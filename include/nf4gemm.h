@@ -259,8 +259,12 @@ nf4_status nf4_matmul_fwd_group(const void* X, int32_t x_elem, int64_t M, const 
  *   q = e4m3(fl32(x * fl32(1 / s))), to nearest even, saturating;
  *   value = q * s.
  * A block with a < 2^-117 has s = 0 and zero codes. A NaN or an infinity
- * makes its whole block NaN. Scales given by the caller may be any fp32
- * values; they multiply the block's products as they are.
+ * makes its whole block NaN. Scales given by the caller may have either sign;
+ * the products form sx * sw of two blocks in fp32 first and multiply the
+ * block's sum by it, so that sx * sw has to be 0 or of magnitude 2^-126 to
+ * 2^128 (beyond it is infinite, and NaN with a sum of 0; below it loses bits).
+ * Scales that nf4_fp8_quantize writes keep to that where the two blocks' largest
+ * magnitudes multiply to 2^-108 (3e-33) at least, and to 2^145 at most.
  * ------------------------------------------------------------------------ */
 typedef struct nf4_fp8_tensor {
   const uint8_t* codes;         /* [rows * cols], 16-byte aligned                           */
