@@ -214,6 +214,14 @@ def _same_device(device: torch.device, **tensors):
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _written(*tensors):
+    """Counts a call's writes into tensors that it was given, as torch does for
+    its own: a backward pass that saved one of them then raises."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _require_cuda_device(device: torch.device):
     """Checked last, after every shape and device-equality check, so that the
     host-side checks can be exercised on CPU tensors."""
@@ -285,6 +293,8 @@ def nf4_quantize(W: torch.Tensor, out: NF4Weight | None = None,
         _check("nf4_quantize_ex", lib().nf4_quantize_ex(
             _ptr(W), ELEM[W.dtype], rows, cols, BLOCKSIZE, DTYPES[dtype], _ptr(q.codes),
             _ptr(q.absmax_q), _ptr(q.absmax_scale), _stream(W.device)))
+    if out is not None:
+        _written(out.codes, out.absmax_q, out.absmax_scale)
     return q
 
 
@@ -308,6 +318,8 @@ def nf4_dequantize(w: NF4Weight, out: torch.Tensor | None = None,
     with torch.cuda.device(w.device):
         _check("nf4_dequantize_ex", lib().nf4_dequantize_ex(ctypes.byref(s), _ptr(y), ELEM[out_dtype],
                                                            _stream(w.device)))
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -336,6 +348,8 @@ def _matmul(name: str, fn: str, A: torch.Tensor, w: NF4Weight, width: int, out_c
         _check(fn, getattr(lib(), fn)(_ptr(A), ELEM[A.dtype], M, ctypes.byref(s), _ptr(y),
                                       ELEM[out_dtype], ACCUMULATE if accumulate else 0,
                                       _stream(A.device)))
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -380,6 +394,7 @@ def nf4_matmul_fwd_group(X: torch.Tensor, ws, outs=None, out_dtype: torch.dtype 
     elif accumulate:
         raise ValueError("accumulate=True needs the output tensors to add to (outs=)")
     _require_cuda_device(X.device)
+    given = outs or ()
     if outs is None:
         outs = [torch.empty(M, w.rows, dtype=out_dtype, device=X.device) for w in ws]
     structs = (nf4_weight * len(ws))(*[w.c_struct() for w in ws])
@@ -390,6 +405,7 @@ def nf4_matmul_fwd_group(X: torch.Tensor, ws, outs=None, out_dtype: torch.dtype 
                                           ctypes.cast(ptrs, ctypes.c_void_p),
                                           ELEM[out_dtype], ACCUMULATE if accumulate else 0,
                                           _stream(X.device)))
+    _written(*given)
     return outs
 
 

@@ -15,7 +15,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (ACCUMULATE, ELEM, _call_on, _require, _require_cuda_device, _same_device,
+from . import (ACCUMULATE, ELEM, _call_on, _require, _require_cuda_device, _same_device, _written,
                nf4_fp8_tensor)
 
 FP8_BLOCK = 128
@@ -117,6 +117,8 @@ def nf4_fp8_quantize(x: torch.Tensor, block_rows: int = 1,
                       block_rows)
     _call_on(device.index, "nf4_fp8_quantize", x.data_ptr(), ELEM[x.dtype], rows, cols, block_rows,
              q.codes.data_ptr(), q.scale.data_ptr())
+    if out is not None:
+        _written(out.codes, out.scale)
     return q
 
 
@@ -137,6 +139,8 @@ def nf4_fp8_dequantize(q: FP8Tensor, out: torch.Tensor | None = None,
     _require_cuda_device(q.device)
     y = out if out is not None else torch.empty(q.codes.shape, dtype=out_dtype, device=q.device)
     _call_on(q.device.index, "nf4_fp8_dequantize", _byref(q.c_struct()), y.data_ptr(), ELEM[out_dtype])
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -200,6 +204,8 @@ def _matmul(name: str, fn: str, a: FP8Tensor, w: FP8Tensor, dx: bool, out, out_d
              _byref(nf4_fp8_tensor(ac.data_ptr(), ascale.data_ptr(), M, red, 1)),
              _byref(nf4_fp8_tensor(wc.data_ptr(), wscale.data_ptr(), rows, cols, FP8_BLOCK)),
              y.data_ptr(), elem, ACCUMULATE if accumulate else 0)
+    if out is not None:
+        _written(out)
     return y
 
 

@@ -4,7 +4,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (ELEM, NF4Error, _call_on, _require, _require_cuda_device, _same_device, lib)
+from . import (ELEM, NF4Error, _call_on, _require, _require_cuda_device, _same_device,
+               _written, lib)
 from .fp8 import FP8_BLOCK, FP8_DTYPE, FP8Tensor
 
 
@@ -116,6 +117,8 @@ def nf4_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
                  None if rstd is None else rstd.data_ptr())
     except NF4Error as error:
         _refused(error, x=x, weight=weight, residual=residual, out_h=out_h)
+    if out_h is not None:
+        _written(out_h)
     return y, h, rstd
 
 
