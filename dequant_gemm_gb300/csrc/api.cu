@@ -401,7 +401,6 @@ nf4_status nf4_rmsnorm_fwd(const void* x, int32_t x_elem, const void* residual, 
   c.rows = rows;
   c.cols = cols;
   c.eps = eps;
-  c.num_sms = d->num_sms;
   c.st = static_cast<cudaStream_t>(stream);
   return launched(nf4::launch_rmsnorm_fwd(c));
 }
@@ -409,7 +408,8 @@ nf4_status nf4_rmsnorm_fwd(const void* x, int32_t x_elem, const void* residual, 
 int64_t nf4_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
   // of any type: the 16-bit types have more rows at once than fp32
-  return nf4::rmsnorm_bwd_parts(rows, cols, nf4::kElemBf16) * cols * static_cast<int64_t>(sizeof(float));
+  return nf4::rmsnorm_bwd_parts(rows, cols, nf4::kElemBf16, nf4::kGb300Sms) * cols *
+         static_cast<int64_t>(sizeof(float));
 }
 
 nf4_status nf4_rmsnorm_bwd(const void* dy, const void* h, const void* dh, int32_t elem,

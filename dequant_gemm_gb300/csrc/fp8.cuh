@@ -220,7 +220,6 @@ struct NormFwdCall {
   float* rstd;             // null or [rows]
   int64_t rows, cols;
   float eps;
-  int num_sms;
   cudaStream_t st;
 };
 cudaError_t launch_rmsnorm_fwd(const NormFwdCall& c);
@@ -235,12 +234,16 @@ struct NormBwdCall {
   const float* rstd;       // [rows]
   void* dx;                // [rows, cols] of elem
   void* dweight;           // [cols] of w_elem
-  float* partial;          // rmsnorm_bwd_parts(rows, cols, elem) x cols
+  float* partial;          // rmsnorm_bwd_parts(rows, cols, elem, kGb300Sms) x cols
   int64_t rows, cols;
   int num_sms;
   cudaStream_t st;
 };
-int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols, int elem);
+// Partial rows of the weight's gradient on a GPU (or a part of one) of `sms` SMs;
+// the workspace, whose size is asked for without a device, has room for a whole
+// GB300's.
+constexpr int kGb300Sms = 152;
+int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols, int elem, int sms);
 cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c);
 
 }  // namespace nf4

@@ -536,8 +536,8 @@ struct RowsCfg {
   static constexpr int kTotalWarps = 4 * kGroups;
   static constexpr int kThreads = 32 * (4 + kTotalWarps);
   static constexpr int kStageBytes = kTileBytes + kBT * 128;
-  // what fits beside the inbox: 8 to 10 weight tiles in flight, far above the
-  // 35 KB an SM needs to keep HBM busy
+  // what fits beside the inbox: 7 to 10 weight tiles of 16 KB in flight up to 64
+  // tokens, 4 at 128, above the 35 KB an SM needs to keep HBM busy
   static constexpr int kStages = kBT == 128 ? 4 : kBT == 64 ? 7 : kBT == 32 ? 8 : 10;
   static constexpr int kBufs = kBT == 128 ? 4 : 8;
   static constexpr int kTmemCols = kBufs * kBT;          // 128, 256, 512, 512
@@ -822,7 +822,8 @@ struct LaunchAttrs {
 
 // Launch shape of a rows call: splits of the reduction, and its time in 0.01
 // us, start-up left out. Measured at 128 tokens a tile on the decoder shapes:
-// 0.46 us a block, 1.5 us a round for the last block and the reduction.
+// 0.46 us a block, 1.5 us a round for the last block and the reduction (up to 64
+// tokens a block takes 0.37 us, which the estimate does not tell apart).
 struct RowsPlan {
   int splits;
   int64_t cost;

@@ -636,15 +636,16 @@ cudaError_t launch_rmsnorm_fwd(const NormFwdCall& c) {
 // CTAs of the backward, and rows of its workspace: as many as run at once, so
 // that none waits for another's end (a multiple of 8: rmsnorm_bwd_kernel). An
 // SM's registers hold 1024 threads of 64 (16-bit types) or 800 of 80 (fp32).
-int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols, int elem) {
+int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols, int elem, int sms) {
   const int64_t per_sm = std::clamp((elem == kElemF32 ? 800 : 1024) / threads_for(runs_of(cols), 1), 1, 8);
-  return std::min(rows, 152 * per_sm);
+  return std::min(rows, std::max<int64_t>(8, sms * per_sm / 8 * 8));
 }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdCall& c) {
   const BwdArgs a = {c.dy, c.h, c.dh, c.weight, c.rstd, c.dx, c.dweight, c.partial, c.rows, c.cols,
                      c.elem, c.w_elem};
-  const unsigned parts = static_cast<unsigned>(rmsnorm_bwd_parts(c.rows, c.cols, c.elem));
+  const unsigned parts =
+      static_cast<unsigned>(rmsnorm_bwd_parts(c.rows, c.cols, c.elem, std::min(c.num_sms, kGb300Sms)));
   auto go = [&](auto elem) {
     constexpr int kElem = decltype(elem)::value;
     return c.cols % 8 == 0 ? launch_bwd<kElem, false>(c, a, parts) : launch_bwd<kElem, true>(c, a, parts);
