@@ -152,8 +152,8 @@ struct MatmulArgs {
 // Persistent: a pair takes the tiles c, c + G, ... in turn, tokens fastest,
 // and the copies and MMAs of the next tile start while one is written out.
 //
-// Measured: 4096 x 11008 x 4096 forward 150 us (2.5 PFLOP/s), 2048 x 4096 x
-// 11008 gradient 79 us, at the board's power limit (1376 W, 1950 MHz). A block
+// Measured: 4096 x 11008 x 4096 forward 150-154 us (2.4 PFLOP/s), 2048 x 4096 x
+// 11008 gradient 80 us, at the board's power limit (1376 W, 1950 MHz). A block
 // takes ~850 cycles against 512 of MMA: two buffers, each of which goes
 // through its MMAs, the commit, the totals warps' reads (~400 cycles) and the
 // hand-back across the pair. Tensor memory has room for no third buffer, and
