@@ -246,3 +246,30 @@ def test_residual_in_another_shape(formulas, joined):
         got.append([x_.grad, s_.grad.view(6, 32), w_.grad])
         assert s_.grad.shape == stream.shape
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_checkpointed_gradients(formulas, with_residual):
+    """Recomputed in the backward pass (torch.utils.checkpoint) and with saved
+    tensors packed away: the same gradients."""
+    from torch.utils.checkpoint import checkpoint
+
+    x, w, s = rand(2, 3, 32, seed=1), rand(32, seed=2), rand(2, 3, 32, seed=3)
+    weights = [dense(16, 32, 4), dense(32, 32, 5)]
+
+    def block(x, w, s):
+        h, (a, b) = ag.norm_fp8_linears(x, w, weights, residual=s, out_dtype=torch.float32)
+        y, h = ag.rms_norm(b, w, h if with_residual else None)
+        return a.sum() + y.square().sum() + (0 if h is None else h.square().sum())
+
+    def grads(run):
+        t = [v.clone().requires_grad_() for v in (x, w, s)]
+        args = (t[0], t[1], t[2] if with_residual else None)
+        return torch.autograd.grad(run(*args), [v for v in args if v is not None])
+
+    want = grads(block)
+    with torch.autograd.graph.save_on_cpu():
+        packed = grads(block)
+    again = grads(lambda *a: checkpoint(block, *a, use_reentrant=False))
+    for got in (packed, again):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
