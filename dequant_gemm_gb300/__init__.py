@@ -1,6 +1,7 @@
 """GB300-native NF4 quantization and fused NF4-dequant matmul, with 8-bit
-floating point products (``fp8.py``) and the RMS norm between them
-(``norm.py``).
+floating point products (``fp8.py``), the RMS norm between them (``norm.py``),
+the gated feed-forward block (``gated.py``) and products with 4-bit weights in
+groups (``int4.py``).
 
 A thin Python binding over the C ABI of ``libnf4gemm.so`` (declared in
 ``include/nf4gemm.h``): the functions below only allocate outputs with
@@ -35,6 +36,8 @@ EXPORTS = ("nf4_quantize", "nf4_quantize_ex", "nf4_dequantize", "nf4_dequantize_
            "nf4_matmul_bwd_dx", "nf4_matmul_fwd_ex", "nf4_matmul_bwd_dx_ex", "nf4_matmul_fwd_group",
            "nf4_fp8_quantize", "nf4_fp8_dequantize", "nf4_fp8_matmul_fwd", "nf4_fp8_matmul_bwd_dx",
            "nf4_rmsnorm_fwd", "nf4_rmsnorm_bwd", "nf4_rmsnorm_bwd_workspace",
+           "nf4_fp8_gated_fwd", "nf4_fp8_gated_bwd", "nf4_fp8_gated_bwd_dx", "nf4_int4_quantize",
+           "nf4_int4_dequantize", "nf4_int4_matmul_fwd", "nf4_int4_gated_fwd",
            "nf4_poll_device_status", "nf4_poll_device_status_site", "nf4_codebook",
            "nf4_codebook_of", "nf4_set_mma_wait_limit", "nf4_last_cuda_error",
            "nf4_status_string")
@@ -67,6 +70,12 @@ class nf4_fp8_tensor(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("block_rows", ctypes.c_int32)]
 
 
+class nf4_int4_weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("group", ctypes.c_int32),
+                ("scale_elem", ctypes.c_int32)]
+
+
 _lib = None
 _lib_lock = threading.Lock()
 
@@ -86,6 +95,7 @@ def lib() -> ctypes.CDLL:
             vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
             W = ctypes.POINTER(nf4_weight)
             Q = ctypes.POINTER(nf4_fp8_tensor)
+            I = ctypes.POINTER(nf4_int4_weight)
             f32 = ctypes.c_float
             sig = {
                 "nf4_quantize": [vp, i64, i64, i32, vp, vp, vp, vp],
@@ -104,6 +114,13 @@ def lib() -> ctypes.CDLL:
                 "nf4_rmsnorm_fwd": [vp, i32, vp, i32, vp, i32, i64, i64, f32, vp, vp, i32, vp, vp,
                                     vp],
                 "nf4_rmsnorm_bwd": [vp, vp, vp, i32, vp, i32, vp, i64, i64, vp, vp, vp, i64, vp],
+                "nf4_fp8_gated_fwd": [Q, Q, Q, i32, vp, i32, vp, vp, vp, vp],
+                "nf4_fp8_gated_bwd": [vp, i32, vp, vp, i64, i64, i32, vp, vp, vp, vp, vp],
+                "nf4_fp8_gated_bwd_dx": [Q, Q, Q, Q, vp, i32, i32, vp],
+                "nf4_int4_quantize": [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp],
+                "nf4_int4_dequantize": [I, vp, i32, vp],
+                "nf4_int4_matmul_fwd": [vp, i32, i64, I, vp, i32, i32, vp],
+                "nf4_int4_gated_fwd": [vp, i32, i64, I, I, i32, vp, i32, vp],
                 "nf4_poll_device_status": [vp],
                 "nf4_poll_device_status_site": [vp, vp],
                 "nf4_codebook": [vp],
@@ -447,7 +464,8 @@ def describe_site(site: int) -> str:
     if site == 0:
         return "none"
     kernel = {1: "small-M forward", 2: "tensor-core forward", 3: "tensor-core input gradient",
-              4: "8-bit forward", 5: "8-bit input gradient"}
+              4: "8-bit forward", 5: "8-bit input gradient", 6: "8-bit gated forward",
+              7: "8-bit gated input gradient"}
     role = {1: "copy producer", 2: "MMA issuer", 3: "dequantizing warp", 4: "epilogue"}
     u = site & 0xffffffff
     return (f"{kernel.get(u >> 28, u >> 28)}, {role.get((u >> 24) & 15, (u >> 24) & 15)}, "
@@ -465,3 +483,6 @@ def nf4_codebook(dtype: str = "nf4") -> torch.Tensor:
 from .fp8 import (FP8_BLOCK, FP8Tensor, alloc_fp8, nf4_fp8_dequantize,  # noqa: E402
                   nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd, nf4_fp8_quantize)
 from .norm import nf4_rmsnorm_bwd, nf4_rmsnorm_fwd  # noqa: E402
+from .gated import ACTIVATIONS, nf4_fp8_gated_bwd, nf4_fp8_gated_bwd_dx, nf4_fp8_gated_fwd  # noqa: E402
+from .int4 import (INT4_GROUPS, Int4Weight, nf4_int4_dequantize, nf4_int4_gated_fwd,  # noqa: E402
+                   nf4_int4_matmul_fwd, nf4_int4_quantize)

@@ -6,6 +6,7 @@
 
 #include "common.cuh"
 #include "fp8.cuh"
+#include "gated.cuh"
 
 namespace {
 
@@ -271,6 +272,77 @@ nf4_status fp8_matmul(bool dx, const nf4_fp8_tensor* a, const nf4_fp8_tensor* w,
   return launched(nf4::launch_fp8_matmul(c));
 }
 
+bool valid_activation(int32_t a) { return a == NF4_SILU || a == NF4_GELU_TANH; }
+
+// The two weights of a gated block on 8-bit operands.
+nf4_status check_gated_weights(const nf4_fp8_tensor* gate, const nf4_fp8_tensor* up) {
+  if (nf4_status s = check_fp8(gate, nf4::kFp8Block)) return s;
+  if (nf4_status s = check_fp8(up, nf4::kFp8Block)) return s;
+  if (gate->rows != up->rows || gate->cols != up->cols || (gate->rows % 16) != 0) return NF4_ERR_SHAPE;
+  if (gate->rows > INT32_MAX || gate->cols > INT32_MAX) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// Shape of a 4-bit weight in groups.
+nf4_status check_int4(const nf4_int4_weight* w) {
+  if (!w) return NF4_ERR_NULL;
+  if (w->group != 32 && w->group != 64 && w->group != 128) return NF4_ERR_BLOCKSIZE;
+  if (w->scale_elem != NF4_BF16 && w->scale_elem != NF4_F16) return NF4_ERR_SHAPE;
+  if (w->rows < 0 || w->cols < 0 || (w->cols % w->group) != 0) return NF4_ERR_SHAPE;
+  return NF4_OK;
+}
+
+nf4_status check_int4_ptrs(const nf4_int4_weight* w) {
+  if (!w->codes || !w->scale) return NF4_ERR_NULL;
+  if (!aligned16(w->codes) || !aligned2(w->scale)) return NF4_ERR_ALIGN;
+  return NF4_OK;
+}
+
+// The shared body of the 4-bit products; `up` null: a plain product.
+nf4_status int4_matmul(const void* X, int32_t x_elem, int64_t M, const nf4_int4_weight* w,
+                       const nf4_int4_weight* up, int32_t activation, void* Y, int32_t y_elem,
+                       int32_t flags, void* stream) {
+  if (nf4_status s = check_int4(w)) return s;
+  if (up && (up->group != w->group || up->scale_elem != w->scale_elem || up->rows != w->rows ||
+             up->cols != w->cols))
+    return NF4_ERR_SHAPE;
+  if (x_elem != NF4_BF16 && x_elem != NF4_F16) return NF4_ERR_SHAPE;
+  if (!valid_elem(y_elem) || (flags & ~NF4_ACCUMULATE) != 0) return NF4_ERR_SHAPE;
+  if (M < 0 || M > INT32_MAX || w->rows > INT32_MAX || w->cols > INT32_MAX) return NF4_ERR_SHAPE;
+  if (M == 0 || w->rows == 0) return NF4_OK;
+  if (!Y) return NF4_ERR_NULL;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (w->cols == 0) {   // an empty sum, and act(0) * 0: the output is 0 (or unchanged)
+    if ((flags & NF4_ACCUMULATE) != 0) return NF4_OK;
+    return launched(cudaMemsetAsync(Y, 0, static_cast<size_t>(M) * w->rows * elem_bytes(y_elem), st));
+  }
+  if (!X) return NF4_ERR_NULL;
+  if (nf4_status s = check_int4_ptrs(w)) return s;
+  if (up)
+    if (nf4_status s = check_int4_ptrs(up)) return s;
+  if (!aligned16(X) || !aligned_to(Y, elem_bytes(y_elem))) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  nf4::Int4Call c = {};
+  c.x = X;
+  c.x_f16 = x_elem == NF4_F16;
+  c.M = M;
+  c.w[0] = *w;
+  c.w[1] = up ? *up : *w;
+  c.gated = up != nullptr;
+  c.curve = nf4::curve_of(activation);
+  c.y = Y;
+  c.y_elem = y_elem;
+  c.accumulate = (flags & NF4_ACCUMULATE) != 0;
+  c.num_sms = d->num_sms;
+  c.device = d->ordinal;
+  c.st = st;
+  return launched(nf4::launch_int4_matmul(c));
+}
+
 }  // namespace
 
 extern "C" {
@@ -448,6 +520,159 @@ nf4_status nf4_rmsnorm_bwd(const void* dy, const void* h, const void* dh, int32_
   return launched(nf4::launch_rmsnorm_bwd(c));
 }
 
+nf4_status nf4_fp8_gated_fwd(const nf4_fp8_tensor* X, const nf4_fp8_tensor* gate,
+                             const nf4_fp8_tensor* up, int32_t activation, void* y, int32_t y_elem,
+                             float* scale, void* g, void* u, void* stream) {
+  if (nf4_status s = check_fp8(X, 1)) return s;
+  if (nf4_status s = check_gated_weights(gate, up)) return s;
+  if (!valid_activation(activation)) return NF4_ERR_SHAPE;
+  if (!scale && y_elem != NF4_F32 && y_elem != NF4_BF16) return NF4_ERR_SHAPE;
+  if (X->cols != gate->cols || X->rows > INT32_MAX) return NF4_ERR_SHAPE;
+  const int64_t M = X->rows, N = gate->rows;
+  if (M == 0 || N == 0) return NF4_OK;
+  if (!y || (g == nullptr) != (u == nullptr)) return NF4_ERR_NULL;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (X->cols == 0) {   // empty sums: G = U = 0, and so is Y
+    const size_t n = static_cast<size_t>(M) * N;
+    cudaError_t e = cudaMemsetAsync(y, 0, n * (scale ? 1 : elem_bytes(y_elem)), st);
+    if (e == cudaSuccess && scale) e = cudaMemsetAsync(scale, 0, M * ((N + 127) / 128) * sizeof(float), st);
+    if (e == cudaSuccess && g) e = cudaMemsetAsync(g, 0, 2 * n, st);
+    if (e == cudaSuccess && u) e = cudaMemsetAsync(u, 0, 2 * n, st);
+    return launched(e);
+  }
+  if (nf4_status s = check_fp8_ptrs(X)) return s;
+  if (nf4_status s = check_fp8_ptrs(gate)) return s;
+  if (nf4_status s = check_fp8_ptrs(up)) return s;
+  if (!aligned16(y) || !aligned4(scale) || !aligned16(g) || !aligned16(u)) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  nf4::GatedFwdCall c = {};
+  c.a = X->codes;
+  c.a_scale = X->scale;
+  c.wg = gate->codes;
+  c.wu = up->codes;
+  c.wg_scale = gate->scale;
+  c.wu_scale = up->scale;
+  c.M = M;
+  c.N = N;
+  c.K = X->cols;
+  c.curve = nf4::curve_of(activation);
+  c.y = y;
+  c.y_fp8 = scale != nullptr;
+  c.y_bf16 = y_elem == NF4_BF16;
+  c.scale = scale;
+  c.g = g;
+  c.u = u;
+  c.num_sms = d->num_sms;
+  c.status = d->status;
+  c.wait_limit = g_mma_wait_limit.load(std::memory_order_relaxed);
+  c.device = d->ordinal;
+  c.st = st;
+  return launched(nf4::launch_gated_fwd(c));
+}
+
+nf4_status nf4_fp8_gated_bwd(const void* dy, int32_t dy_elem, const void* g, const void* u,
+                             int64_t rows, int64_t cols, int32_t activation, uint8_t* dg,
+                             float* dg_scale, uint8_t* du, float* du_scale, void* stream) {
+  if (!valid_elem(dy_elem) || !valid_activation(activation)) return NF4_ERR_SHAPE;
+  if (rows < 0 || cols < 0 || (cols % 16) != 0) return NF4_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (!dy || !g || !u || !dg || !dg_scale || !du || !du_scale) return NF4_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(g) || !aligned16(u) || !aligned16(dg) || !aligned16(du) ||
+      !aligned4(dg_scale) || !aligned4(du_scale))
+    return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  return launched(nf4::launch_gated_bwd(dy, dy_elem, g, u, rows, cols, nf4::curve_of(activation), dg, dg_scale,
+                                        du, du_scale, static_cast<cudaStream_t>(stream)));
+}
+
+nf4_status nf4_fp8_gated_bwd_dx(const nf4_fp8_tensor* dG, const nf4_fp8_tensor* dU,
+                                const nf4_fp8_tensor* gate, const nf4_fp8_tensor* up, void* dX,
+                                int32_t dx_elem, int32_t flags, void* stream) {
+  if (nf4_status s = check_fp8(dG, 1)) return s;
+  if (nf4_status s = check_fp8(dU, 1)) return s;
+  if (nf4_status s = check_gated_weights(gate, up)) return s;
+  if (dx_elem != NF4_F32 && dx_elem != NF4_BF16) return NF4_ERR_SHAPE;
+  if ((flags & ~NF4_ACCUMULATE) != 0) return NF4_ERR_SHAPE;
+  const int64_t M = dG->rows, N = gate->rows, K = gate->cols;
+  if (dU->rows != M || dG->cols != N || dU->cols != N || M > INT32_MAX) return NF4_ERR_SHAPE;
+  if (M == 0 || K == 0) return NF4_OK;
+  if (!dX) return NF4_ERR_NULL;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    if ((flags & NF4_ACCUMULATE) != 0) return NF4_OK;
+    return launched(cudaMemsetAsync(dX, 0, static_cast<size_t>(M) * K * elem_bytes(dx_elem), st));
+  }
+  for (const nf4_fp8_tensor* t : {dG, dU, gate, up})
+    if (nf4_status s = check_fp8_ptrs(t)) return s;
+  if (!aligned16(dX)) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  nf4::GatedDxCall c = {};
+  c.dg = dG->codes;
+  c.du = dU->codes;
+  c.dg_scale = dG->scale;
+  c.du_scale = dU->scale;
+  c.wg = gate->codes;
+  c.wu = up->codes;
+  c.wg_scale = gate->scale;
+  c.wu_scale = up->scale;
+  c.M = M;
+  c.N = N;
+  c.K = K;
+  c.out = dX;
+  c.out_bf16 = dx_elem == NF4_BF16;
+  c.accumulate = (flags & NF4_ACCUMULATE) != 0;
+  c.num_sms = d->num_sms;
+  c.status = d->status;
+  c.wait_limit = g_mma_wait_limit.load(std::memory_order_relaxed);
+  c.device = d->ordinal;
+  c.st = st;
+  return launched(nf4::launch_gated_dx(c));
+}
+
+nf4_status nf4_int4_quantize(const void* W, int32_t w_elem, int64_t rows, int64_t cols,
+                             int32_t group, int32_t scale_elem, uint8_t* codes, void* scale,
+                             uint8_t* zero, void* stream) {
+  const nf4_int4_weight w = {codes, scale, zero, rows, cols, group, scale_elem};
+  if (nf4_status s = check_int4(&w)) return s;
+  if (!valid_elem(w_elem)) return NF4_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return NF4_OK;
+  if (!W) return NF4_ERR_NULL;
+  if (nf4_status s = check_int4_ptrs(&w)) return s;
+  if (!aligned16(W)) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  return launched(nf4::launch_int4_quantize(W, w_elem, rows, cols, group, scale_elem == NF4_BF16, codes, scale,
+                                            zero, static_cast<cudaStream_t>(stream)));
+}
+
+nf4_status nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int32_t out_elem, void* stream) {
+  if (nf4_status s = check_int4(w)) return s;
+  if (!valid_elem(out_elem)) return NF4_ERR_SHAPE;
+  if (w->rows == 0 || w->cols == 0) return NF4_OK;
+  if (nf4_status s = check_int4_ptrs(w)) return s;
+  if (!out) return NF4_ERR_NULL;
+  if (!aligned16(out)) return NF4_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if (nf4_status s = current_device(&d)) return s;
+  return launched(nf4::launch_int4_dequantize(*w, out, out_elem, static_cast<cudaStream_t>(stream)));
+}
+
+nf4_status nf4_int4_matmul_fwd(const void* X, int32_t x_elem, int64_t M, const nf4_int4_weight* w,
+                               void* Y, int32_t y_elem, int32_t flags, void* stream) {
+  return int4_matmul(X, x_elem, M, w, nullptr, NF4_SILU, Y, y_elem, flags, stream);
+}
+
+nf4_status nf4_int4_gated_fwd(const void* X, int32_t x_elem, int64_t M, const nf4_int4_weight* gate,
+                              const nf4_int4_weight* up, int32_t activation, void* Y, int32_t y_elem,
+                              void* stream) {
+  if (!gate || !up) return NF4_ERR_NULL;
+  if (!valid_activation(activation)) return NF4_ERR_SHAPE;
+  return int4_matmul(X, x_elem, M, gate, up, activation, Y, y_elem, 0, stream);
+}
+
 nf4_status nf4_poll_device_status_site(void* stream, int32_t* site) {
   if (site) *site = 0;
   DeviceInfo* d = nullptr;
@@ -495,7 +720,8 @@ const char* nf4_status_string(nf4_status status) {
     case NF4_ERR_NULL: return "a required pointer is NULL (or a pointer the data type leaves unused is not)";
     case NF4_ERR_SHAPE: return "unsupported or negative shape, data type, element type or flag";
     case NF4_ERR_ALIGN: return "a pointer is not 16-byte aligned";
-    case NF4_ERR_BLOCKSIZE: return "blocksize must be 64, dq_group 256 (4-bit) or 0 (int8)";
+    case NF4_ERR_BLOCKSIZE:
+      return "blocksize must be 64, dq_group 256 (4-bit) or 0 (int8); block_rows 1 or 128; group 32, 64 or 128";
     case NF4_ERR_DEVICE: return "no current CUDA device, or it is not sm_103";
     case NF4_ERR_LAUNCH: return "the CUDA runtime rejected a launch or the stream holds an error";
     case NF4_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait ran out";

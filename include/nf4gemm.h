@@ -340,6 +340,118 @@ nf4_status nf4_rmsnorm_bwd(const void* dy, const void* h, const void* dh, int32_
                            int64_t cols, void* dx, void* dweight, void* workspace,
                            int64_t workspace_bytes, void* stream);
 
+/* --------------------------------------------------------------------------
+ * The gated feed-forward block on 8-bit operands: both projections, the
+ * activation and the product in one kernel, and its gradients.
+ *   act(g) = g sigma(p(g)), sigma(p) = 1 / (1 + exp(-p)), with
+ *   NF4_SILU       p(g) = g
+ *   NF4_GELU_TANH  p(g) = 2 sqrt(2 / pi) (g + 0.044715 g^3), which is
+ *                  g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2
+ * taken in fp32. g = -infinity gives NaN (the limit is -0).
+ * ------------------------------------------------------------------------ */
+typedef enum nf4_activation {
+  NF4_SILU = 0,
+  NF4_GELU_TANH = 1
+} nf4_activation;
+
+/* G = value(X) value(gate)^T, U = value(X) value(up)^T, Y = act(G) * U.
+ *   X        [M, cols] with block_rows 1; gate, up [rows, cols] with
+ *            block_rows 128, rows % 16 == 0
+ *   y        device [M, rows] of y_elem NF4_F32 or NF4_BF16 (output); with
+ *            scale not NULL, e4m3 codes in 1 x 128 blocks instead, as the next
+ *            product reads them (y_elem is then ignored)
+ *   scale    device fp32 [M * ceil(rows / 128)] (output, 4-byte aligned), or NULL
+ *   g, u     device bf16 [M, rows] (outputs): G and U rounded once, what
+ *            nf4_fp8_gated_bwd reads; both or neither (NULL)
+ * The sums are those of nf4_fp8_matmul_fwd; Y is taken from the fp32 G and U
+ * and rounded once. Bitwise repeatable. An activation other than the two is
+ * NF4_ERR_SHAPE. */
+nf4_status nf4_fp8_gated_fwd(const nf4_fp8_tensor* X, const nf4_fp8_tensor* gate,
+                             const nf4_fp8_tensor* up, int32_t activation, void* y, int32_t y_elem,
+                             float* scale, void* g, void* u, void* stream);
+
+/* The gradients of G and U from that of Y (an 8-bit Y passes its gradient
+ * through):
+ *   dG = dY * U * act'(G),  dU = dY * act(G)
+ *   act'(g) = s + g s (1 - s) p'(g),  s = sigma(p(g))
+ * in fp32, then quantized in 1 x 128 blocks as nf4_fp8_quantize does.
+ *   dy device [rows, cols] of dy_elem (any of the three), g and u device bf16
+ *   [rows, cols], cols % 16 == 0; dg, du device codes [rows * cols] and
+ *   dg_scale, du_scale device fp32 [rows * ceil(cols / 128)] (outputs, scales
+ *   4-byte aligned) */
+nf4_status nf4_fp8_gated_bwd(const void* dy, int32_t dy_elem, const void* g, const void* u,
+                             int64_t rows, int64_t cols, int32_t activation, uint8_t* dg,
+                             float* dg_scale, uint8_t* du, float* du_scale, void* stream);
+
+/* The block's input gradient, dX = value(dG) value(gate) + value(dU) value(up):
+ * dG, dU [M, rows] with block_rows 1, gate and up as above, dX device
+ * [M, cols] of dx_elem NF4_F32 or NF4_BF16; flags as nf4_fp8_matmul_bwd_dx.
+ * One sum over both weights, rounded once. */
+nf4_status nf4_fp8_gated_bwd_dx(const nf4_fp8_tensor* dG, const nf4_fp8_tensor* dU,
+                                const nf4_fp8_tensor* gate, const nf4_fp8_tensor* up, void* dX,
+                                int32_t dx_elem, int32_t flags, void* stream);
+
+/* --------------------------------------------------------------------------
+ * Uniform 4-bit weights with a 16-bit scale, and a zero point, for each group
+ * along a row, and products of few tokens with them.
+ *
+ * Storage format (row-major, contiguous), W [rows = N, cols = K], groups of
+ * `group` = 32, 64 or 128 consecutive values of a row, cols % group == 0:
+ *  - codes: uint8 [rows * cols / 2], element 2j in the high nibble of byte j
+ *  - scale: fp16 or bf16 (scale_elem) [rows * cols / group]
+ *  - zero:  uint8 [rows * cols / group], values 0 to 15; NULL: 8 everywhere
+ *  - w = (code - zero) * scale. A zero point above 15 makes its group's values
+ *    unspecified.
+ * ------------------------------------------------------------------------ */
+typedef struct nf4_int4_weight {
+  const uint8_t* codes;         /* 16-byte aligned                          */
+  const void* scale;            /* 2-byte aligned                           */
+  const uint8_t* zero;          /* any alignment, or NULL                   */
+  int64_t rows;
+  int64_t cols;
+  int32_t group;                /* 32, 64 or 128                            */
+  int32_t scale_elem;           /* NF4_BF16 or NF4_F16                      */
+} nf4_int4_weight;
+
+/* Quantize W [rows, cols] of w_elem (NF4_F32, NF4_BF16 or NF4_F16), finite,
+ * to nearest. Per group, every step in fp32 with one IEEE rounding:
+ *   with zero points (zero not NULL):
+ *     lo = min(0, min w), hi = max(0, max w), s = rnd((hi - lo) / 15),
+ *     z = clamp(rint(-lo / s), 0, 15), code = clamp(rint(w / s) + z, 0, 15)
+ *   without:
+ *     s = rnd(max |w| / 7), code = clamp(rint(w / s) + 8, 0, 15)
+ * rnd rounds to scale_elem, rint half to even; where s = 0 every code is the
+ * zero point (0 with zero points). The group's range must fit scale_elem
+ * (fp16: max |w| / 7, or (hi - lo) / 15, below 65504).
+ * cols % group != 0, another group or element type: NF4_ERR_BLOCKSIZE for the
+ * group, NF4_ERR_SHAPE otherwise. */
+nf4_status nf4_int4_quantize(const void* W, int32_t w_elem, int64_t rows, int64_t cols,
+                             int32_t group, int32_t scale_elem, uint8_t* codes, void* scale,
+                             uint8_t* zero, void* stream);
+
+/* The values of w, each rounded once to out_elem (NF4_F32, NF4_BF16 or
+ * NF4_F16): out device [rows, cols]. */
+nf4_status nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int32_t out_elem, void* stream);
+
+/* Y = X * value(w)^T for few tokens: X device [M, cols] of x_elem NF4_BF16 or
+ * NF4_F16, Y device [M, rows] of y_elem (NF4_F32, NF4_BF16 or NF4_F16; aligned
+ * to its elements), any rows. flags: NF4_ACCUMULATE adds to Y's contents.
+ * (code - zero) and X enter the tensor cores exactly, in X's type; the sums of
+ * a group are fp32, multiplied by the scale in fp32 and added up in fp32, in a
+ * fixed order; Y is rounded once. Any M: the weight is read once for every 16
+ * tokens, so that many tokens are better served by nf4_int4_dequantize and a
+ * library product. */
+nf4_status nf4_int4_matmul_fwd(const void* X, int32_t x_elem, int64_t M, const nf4_int4_weight* w,
+                               void* Y, int32_t y_elem, int32_t flags, void* stream);
+
+/* The gated block for few tokens, in one kernel: Y = act(X value(gate)^T) *
+ * (X value(up)^T); gate and up have the same rows, cols, group and
+ * scale_elem (NF4_ERR_SHAPE otherwise), each with or without zero points.
+ * Otherwise as nf4_int4_matmul_fwd, activations as nf4_fp8_gated_fwd. */
+nf4_status nf4_int4_gated_fwd(const void* X, int32_t x_elem, int64_t M, const nf4_int4_weight* gate,
+                              const nf4_int4_weight* up, int32_t activation, void* Y, int32_t y_elem,
+                              void* stream);
+
 /* Synchronizes `stream`, then reports and clears the device status word of
  * the current device: NF4_ERR_DEVICE_TIMEOUT if any kernel's bounded wait ran
  * out since the last poll, NF4_ERR_LAUNCH if the stream holds a CUDA error,
@@ -350,6 +462,7 @@ nf4_status nf4_poll_device_status(void* stream);
  * first timeout since the last poll happened (0 when there was none):
  *   bits 28-31  kernel: 1 small-M forward, 2 tensor-core forward,
  *               3 tensor-core input gradient, 4 8-bit forward, 5 8-bit
+ *               input gradient, 6 8-bit gated forward, 7 8-bit gated
  *               input gradient
  *   bits 24-27  role: 1 copy producer, 2 MMA issuer, 3 dequantizing /
  *               computing warp, 4 epilogue
