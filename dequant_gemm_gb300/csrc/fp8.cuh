@@ -17,7 +17,7 @@
 namespace nf4 {
 
 // Kernel numbers of report_status (see nf4_poll_device_status_site).
-constexpr uint32_t kSiteFp8Fwd = 4, kSiteFp8Dx = 5;
+constexpr uint32_t kSiteFp8Fwd = 4, kSiteFp8Dx = 5, kSiteGatedFwd = 6, kSiteGatedDx = 7;
 
 constexpr int kFp8Block = NF4_FP8_BLOCK;      // 128
 constexpr float kE4m3Max = 448.0f;
