@@ -311,7 +311,7 @@ nf4_status int4_matmul(const void* X, int32_t x_elem, int64_t M, const nf4_int4_
     return NF4_ERR_SHAPE;
   if (x_elem != NF4_BF16 && x_elem != NF4_F16) return NF4_ERR_SHAPE;
   if (!valid_elem(y_elem) || (flags & ~NF4_ACCUMULATE) != 0) return NF4_ERR_SHAPE;
-  if (M < 0 || M > INT32_MAX || w->rows > INT32_MAX || w->cols > INT32_MAX) return NF4_ERR_SHAPE;
+  if (M < 0 || M > INT32_MAX || w->rows > INT32_MAX || w->cols > NF4_INT4_MAX_COLS) return NF4_ERR_SHAPE;
   if (M == 0 || w->rows == 0) return NF4_OK;
   if (!Y) return NF4_ERR_NULL;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -84,25 +84,32 @@ int4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint16_t* __res
 // into the mantissa, the same number with the zero point is subtracted, and
 // (q - z) x is exact in the fp32 sum; a group's sums are multiplied by its scale
 // in fp32 and added to the row's.
-//  * A warp has 16 rows and takes 128-wide chunks of them, kChunks neighbouring
-//    ones a round: lane (g, t) loads 16 bytes (32 codes) of rows g and g + 8 a
-//    chunk, straight into registers; while a chunk is multiplied, the same chunk
-//    of the next round is on its way.
-//  * The order of k within a chunk is free as long as both operands agree. Bits
-//    of a code word are taken in pairs 16 bits apart, (e1, e5), (e0, e4),
-//    (e3, e7), (e2, e6) for elements e0 to e7 of 4 bytes, and the tokens are
-//    staged in shared memory in that order, 16 bytes a lane.
-//  * The four lanes of a row feed one MMA, so that they have to hold codes of one
-//    group. With groups of 64 and 32 they exchange words first (2 and 4 shuffles
-//    for 32 codes; loads of 8 and 4 bytes instead would take 2 and 4 times the
-//    load instructions).
-//  * A CTA of 8 warps is kParts parts of the reduction x 8 / kParts row groups;
-//    with few rows and long reductions a cluster of up to 8 CTAs splits the
-//    reduction further. Every warp leaves its sums in shared memory of the CTA
-//    that owns the rows, which adds them in a fixed order: repeatable, no
-//    workspace.
-constexpr int kWarps = 8;
+//  * One CTA of 16 warps an SM, persistent: the tokens' slice of the reduction is
+//    staged in shared memory once, then row tiles pass by. Of a tile, a warp has
+//    16 rows and one of 2^parts_log parts of the slice; a cluster of up to 8 CTAs
+//    splits the reduction where the rows are few or the tokens' slice is large.
+//  * A warp streams its own codes, boxes of 16 rows x 256 values, by asynchronous
+//    copies into two slots of its own: no warp waits for another. A box goes into
+//    registers whole (ldmatrix: word t of row g is lane (g, t)'s, which is the
+//    operand's layout whatever the group), so that its slot is copied to again
+//    before it is multiplied, across row tiles too.
+//  * The order of k within an MMA is free as long as both operands agree. Bits of a
+//    code word are taken in pairs 16 bits apart, (e1, e5), (e0, e4), (e3, e7),
+//    (e2, e6) for elements e0 to e7 of 4 bytes, and the tokens are staged in that
+//    order, 16 bytes a lane.
+//  * Scales and zero points are loaded two boxes ahead, each by one lane of a row's
+//    four, packed into a word (the scale's fp32 bits leave the low 13 free) and
+//    handed to the others by shuffles.
+//  * Every warp leaves its sums of a tile in shared memory of the CTA that owns the
+//    rows, which adds them in a fixed order: repeatable, no workspace.
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kBoxBytes = 16 * 128;            // 16 rows x 256 codes
+constexpr int kBoxCodes = 256;
+constexpr int kMostSmem = 227 * 1024;
+constexpr int ring_bytes(int mats) { return kWarps * 2 * kBoxBytes * mats; }
+constexpr int sums_bytes(int mats, int tokens) { return kWarps * 16 * 4 * mats * tokens; }
+constexpr int staged_bytes(int tokens) { return kBoxCodes * 2 * tokens; }            // a box's tokens
 
 struct Int4Args {
   const uint16_t* x;             // [M, K]
@@ -111,10 +118,11 @@ struct Int4Args {
   const uint8_t* zero[2];        // or null
   int64_t M, N, K;
   int groups;                    // of a row
-  int rounds;                    // of a row
-  int window;                    // rounds whose tokens are staged at once
-  int inbox;                     // bytes of shared memory for them
-  int parts_log, splits, m_tiles;
+  int boxes;                     // of a row
+  int tokens, m_tiles;           // of a tile; tiles
+  int parts_log, splits;
+  int row_tiles, row_step;       // all; clusters that share a token tile
+  int off_sums;                  // byte offset in shared memory
   bool scale_bf16;
   Curve curve;
   void* y;
@@ -136,25 +144,36 @@ __device__ __forceinline__ void store_sum(void* y, int elem, int64_t i, float v,
   }
 }
 
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p, bool in) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (in)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+__device__ __forceinline__ uint4 lds_words(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 
+// 16 bytes from global to shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// d = a b, or (kAdd) d += a b
 template <bool kF16>
-__device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool add) {
+  const float c[4] = {add ? d[0] : 0.0f, add ? d[1] : 0.0f, add ? d[2] : 0.0f, add ? d[3] : 0.0f};
   if constexpr (kF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // Codes 4 bits wide in bits 0-3 and 16-19 of w as two numbers less the zero
@@ -162,7 +181,8 @@ __device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], ui
 template <bool kF16>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zz) {
   constexpr uint32_t kOne = kF16 ? 0x64006400u : 0x43004300u;     // 1024, 128
-  const uint32_t v = (w & 0x000f000fu) | kOne;
+  uint32_t v;                                  // (w & mask) | one: written out, it takes two instructions
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w), "n"(0x000f000f), "r"(kOne));
   if constexpr (kF16) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&zz));
     return *reinterpret_cast<const uint32_t*>(&d);
@@ -173,258 +193,275 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zz) {
   }
 }
 
-// The four lanes' words of a row, exchanged so that word w of every lane is of
-// the chunk's group w kPer / 4 (kPer groups a chunk).
-template <int kPer>
-__device__ __forceinline__ void exchange(uint4& q, int t) {
-  if constexpr (kPer >= 2) {
-    const bool low = t < 2;
-    const uint32_t a = __shfl_xor_sync(0xffffffffu, low ? q.z : q.x, 2);
-    const uint32_t b = __shfl_xor_sync(0xffffffffu, low ? q.w : q.y, 2);
-    if (low) {
-      q.z = a;
-      q.w = b;
-    } else {
-      q.x = a;
-      q.y = b;
-    }
-  }
-  if constexpr (kPer == 4) {
-    const bool even = (t & 1) == 0;
-    const uint32_t a = __shfl_xor_sync(0xffffffffu, even ? q.y : q.x, 1);
-    const uint32_t b = __shfl_xor_sync(0xffffffffu, even ? q.w : q.z, 1);
-    if (even) {
-      q.y = a;
-      q.w = b;
-    } else {
-      q.x = a;
-      q.z = b;
-    }
-  }
-}
-
-// Lane and word that hold the run of 8 values kk (a multiple of 8) of a chunk:
-// the inverse of exchange().
-template <int kPer>
-__device__ __forceinline__ int run_slot(int kk) {       // 4 word + lane
-  const int run = kk >> 3;                               // 0 to 15
-  if constexpr (kPer == 1) return 4 * (run & 3) + (run >> 2);
-  else if constexpr (kPer == 2) return 4 * (2 * (run >> 3) + (run & 1)) + ((run >> 2) & 1) + (run & 2);
-  else return 4 * (run >> 2) + (run & 3);
-}
-
 template <bool kF16, int kGroup, int kMats, int kNT>
-__global__ void __launch_bounds__(kThreads, 2) int4_matmul_kernel(const __grid_constant__ Int4Args p) {
-  constexpr int kPer = 128 / kGroup;           // groups of a chunk
-  constexpr int kChunks = 4 / kMats;           // of a round
-  extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_constant__ Int4Args p) {
+  constexpr int kBoxGroups = kBoxCodes / kGroup;               // 2, 4 or 8
+  constexpr int kLoads = kBoxGroups / 2;                       // scales a lane loads of a box
+  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int parts = 1 << p.parts_log, part = warp & (parts - 1), rgroup = warp >> p.parts_log;
-  const int rows_cta = 16 * (kWarps >> p.parts_log);
-  const int rank = static_cast<int>(blockIdx.x) % p.splits;
-  const int tile = static_cast<int>(blockIdx.x) / p.splits;
-  const int64_t m0 = static_cast<int64_t>(tile % p.m_tiles) * (8 * kNT);
-  const int64_t row0 = static_cast<int64_t>(tile / p.m_tiles) * rows_cta;
-  const int mt = static_cast<int>(min(static_cast<int64_t>(8 * kNT), p.M - m0));
-  const int r_first = static_cast<int>(static_cast<int64_t>(p.rounds) * rank / p.splits);
-  const int r_last = static_cast<int>(static_cast<int64_t>(p.rounds) * (rank + 1) / p.splits);
+  const int parts = 1 << p.parts_log, part = warp & (parts - 1);
+  const int rows_tile = 16 * (kWarps >> p.parts_log), row_warp = 16 * (warp >> p.parts_log);
+  const int rank = static_cast<int>(blockIdx.x) % p.splits, cluster = static_cast<int>(blockIdx.x) / p.splits;
+  const int64_t m0 = static_cast<int64_t>(cluster % p.m_tiles) * p.tokens;
+  const int mt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.M - m0));
+  const int tile0 = cluster / p.m_tiles;
+  // this CTA's boxes of a row, and this warp's
+  const int s0 = static_cast<int>(static_cast<int64_t>(p.boxes) * rank / p.splits);
+  const int s1 = static_cast<int>(static_cast<int64_t>(p.boxes) * (rank + 1) / p.splits);
+  const int b0 = s0 + (s1 - s0) * part / parts, nb = s0 + (s1 - s0) * (part + 1) / parts - b0;
+  const uint32_t ring = tc::smem_addr(smem) + warp * (2 * kMats * kBoxBytes);
   let_next_start();
-  if (p.splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   wait_for_previous();
 
-  // rows past the end read the last one; their sums are dropped
-  const int64_t ra = min(row0 + 16 * rgroup + g, p.N - 1), rb = min(row0 + 16 * rgroup + g + 8, p.N - 1);
-  uint4 q[kMats][kChunks][2];
-  uint32_t sz[kMats][2][kPer], next_sz[kMats][2][kPer];    // scale, zero point in bits 16 and up
-  auto load_chunk = [&](int r, int i) {
-    const int64_t k = (static_cast<int64_t>(r) * kChunks + i) * 128 + 32 * t;
-#pragma unroll
-    for (int mat = 0; mat < kMats; ++mat) {
-      q[mat][i][0] = load_codes(p.codes[mat] + (ra * p.K + k) / 2, k < p.K);
-      q[mat][i][1] = load_codes(p.codes[mat] + (rb * p.K + k) / 2, k < p.K);
-    }
+  // What is copied next. Box j of the warp's stream goes into slot j & 1: lane l
+  // copies 16 bytes, chunk l % 8 (swizzled by the row), of rows l / 8 + 0, 4, 8
+  // and 12. Of chunks and rows past the end the slot keeps what it held: any bits
+  // are numbers, which meet zero scales and tokens or are dropped with their rows.
+  int next_tile = tile0, next_left = 0;        // boxes left in the tile
+  int64_t code_at = 0, scale_at = 0;           // this lane's first byte and scale
+  int rows_left = 0, bytes_left = 0, groups_left = 0;
+  const int64_t pitch = p.K / 2;
+  // lanes t = 0, 1 load the scales of row g, 2, 3 those of row g + 8, half a box's each
+  const int lane_group = kLoads * (t & 1);
+  const uint32_t copy_to = (lane >> 3) * 128;
+  // the swizzle of rows l / 8 + 0 and + 8, and of those + 4 and + 12
+  const uint32_t swizzle0 = 16 * ((lane & 7) ^ (lane >> 3)), swizzle4 = swizzle0 ^ 64;
+  auto start_tile = [&] {
+    next_left = next_tile < p.row_tiles ? nb : 0;
+    const int64_t row0 = static_cast<int64_t>(next_tile) * rows_tile + row_warp;
+    code_at = (row0 + (lane >> 3)) * pitch + static_cast<int64_t>(b0) * 128 + 16 * (lane & 7);
+    rows_left = static_cast<int>(min(p.N - row0, static_cast<int64_t>(16))) - (lane >> 3);
+    bytes_left = static_cast<int>(pitch) - b0 * 128 - 16 * (lane & 7);
+    groups_left = p.groups - b0 * kBoxGroups - lane_group;
+    scale_at = min(row0 + g + 8 * (t >> 1), p.N - 1) * p.groups + b0 * kBoxGroups + lane_group;
   };
-  // lane t loads those of the round's chunk t, which the others take by shuffles
-  auto load_scales = [&](int r, uint32_t (&to)[kMats][2][kPer]) {
+  auto copy_box = [&](uint32_t slot) {         // (address of the slot)
+    if (next_left > 0) {
+      const int rows = bytes_left > 0 ? rows_left : 0;
+#pragma unroll
+      for (int mat = 0; mat < kMats; ++mat) {
+        const uint8_t* src = p.codes[mat] + code_at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * i < rows)
+            copy16(slot + mat * kBoxBytes + copy_to + i * 512 + (i & 1 ? swizzle4 : swizzle0), src + i * 4 * pitch);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  uint32_t raw_s[kMats][kLoads], raw_z[kMats][kLoads], later_s[kMats][kLoads], later_z[kMats][kLoads];
+  auto load_scales = [&](uint32_t (&rs)[kMats][kLoads], uint32_t (&rz)[kMats][kLoads]) {
 #pragma unroll
     for (int mat = 0; mat < kMats; ++mat)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int at = (r * kChunks + t % kChunks) * kPer + j;
-          const int64_t i = (h ? rb : ra) * p.groups + at;
-          uint32_t v = 0x80000u;
-          if (at < p.groups) {
-            v = __ldg(p.scale[mat] + i);
-            v |= p.zero[mat] ? static_cast<uint32_t>(__ldg(p.zero[mat] + i)) << 16 : 0x80000u;
-          }
-          to[mat][h][j] = v;
+      for (int j = 0; j < kLoads; ++j) {
+        rs[mat][j] = 0u;
+        rz[mat][j] = 8u;
+        if (next_left > 0 && j < groups_left) {
+          rs[mat][j] = __ldg(p.scale[mat] + scale_at + j);
+          if (p.zero[mat]) rz[mat][j] = __ldg(p.zero[mat] + scale_at + j);
         }
+      }
   };
+  auto advance = [&] {
+    code_at += 128;
+    bytes_left -= 128;
+    groups_left -= kBoxGroups;
+    scale_at += kBoxGroups;
+    if (--next_left == 0) {
+      next_tile += p.row_step;
+      start_tile();
+    }
+  };
+  start_tile();
+  load_scales(raw_s, raw_z);
+  copy_box(ring);
+  advance();
+  load_scales(later_s, later_z);
+  copy_box(ring + kMats * kBoxBytes);
+  advance();
 
-  float acc[kMats][kNT][4] = {};
-  const uint4* xs = reinterpret_cast<const uint4*>(smem);
-  for (int w0 = r_first; w0 < r_last; w0 += p.window) {
-    const int w1 = min(w0 + p.window, r_last);
-    int r = w0 + part;
-    if (r < w1) {
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) load_chunk(r, i);
-      load_scales(r, sz);
-    }
-    // the window's tokens, [chunk][word][token][lane]
-    const int runs = (w1 - w0) * kChunks * 16;
-    for (int i = threadIdx.x; i < runs * mt; i += kThreads) {
+  // the slice's tokens, [run of 8 / 4][token][run % 4]
+  {
+    const int runs = (s1 - s0) * (kBoxCodes / 8);
+    for (int i = threadIdx.x; i < runs * p.tokens; i += kThreads) {
       const int tok = i / runs, run = i - tok * runs;
-      const int64_t k = static_cast<int64_t>(w0) * kChunks * 128 + 8 * run;
+      const int64_t k = static_cast<int64_t>(s0) * kBoxCodes + 8 * run;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (k < p.K) v = __ldg(reinterpret_cast<const uint4*>(p.x + (m0 + tok) * p.K + k));
-      const int slot = run_slot<kPer>((8 * run) & 127);
-      reinterpret_cast<uint4*>(smem)[(((run >> 4) * 4 + (slot >> 2)) * mt + tok) * 4 + (slot & 3)] =
-          make_uint4(__byte_perm(v.x, v.z, 0x7632), __byte_perm(v.x, v.z, 0x5410),
-                     __byte_perm(v.y, v.w, 0x7632), __byte_perm(v.y, v.w, 0x5410));
+      if (k < p.K && tok < mt) v = __ldg(reinterpret_cast<const uint4*>(p.x + (m0 + tok) * p.K + k));
+      reinterpret_cast<uint4*>(smem + ring_bytes(kMats))[((run >> 2) * p.tokens + tok) * 4 + (run & 3)] =
+          make_uint4(__byte_perm(v.x, v.z, 0x7632), __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.y, v.w, 0x7632),
+                     __byte_perm(v.y, v.w, 0x5410));
     }
-    __syncthreads();
-    for (; r < w1; r += parts) {
-      const bool more = r + parts < w1;
-      if (more) load_scales(r + parts, next_sz);
+  }
+  __syncthreads();
+
+  const int own = rows_tile / p.splits, own_log = 31 - __clz(own);
+  const uint32_t inbox = tc::smem_addr(smem) + p.off_sums;
+  // lanes 8 j .. 8 j + 7 give the rows of matrix j, chunk 4 c + j of a box's rows
+  const uint32_t lm = (lane & 7) * 128 + 16 * ((lane >> 3) ^ (lane & 7));
+  // A lane whose column of the MMA has no token reads another's: the column's sums
+  // are dropped.
+  const uint32_t x_lane = tc::smem_addr(smem) + ring_bytes(kMats) + 16 * (4 * (g % min(p.tokens, 8)) + t);
+  const uint32_t x_word = 64u * p.tokens;
+  uint32_t slot = ring;
+  for (int tile = tile0; tile < p.row_tiles; tile += p.row_step) {
+    float acc[kMats][kNT][4] = {};
+#pragma unroll 1
+    for (int b = 0; b < nb; ++b) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      uint32_t q[kMats][2][2][4];              // [weight][chunk][row half][word]
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const uint4* xc = xs + ((r - w0) * kChunks + i) * 16 * mt + 4 * g + t;
+      for (int mat = 0; mat < kMats; ++mat)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            ldmatrix4(slot + mat * kBoxBytes + h * 1024 + (c ? lm ^ 64u : lm), q[mat][c][h]);
+      // this box's scales as fp32 bits with the zero point below
+      uint32_t sz[kMats][kLoads];
+#pragma unroll
+      for (int mat = 0; mat < kMats; ++mat)
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          sz[mat][j] = __float_as_uint(scale_value(raw_s[mat][j], p.scale_bf16)) | raw_z[mat][j];
+          raw_s[mat][j] = later_s[mat][j];
+          raw_z[mat][j] = later_z[mat][j];
+        }
+      __syncwarp();
+      load_scales(later_s, later_z);
+      copy_box(slot);
+      advance();
+      slot = 2 * ring + kMats * kBoxBytes - slot;              // the other one
+      const uint32_t xb = x_lane + (b0 - s0 + b) * (8 * x_word);
+#pragma unroll
+      for (int j = 0; j < kBoxGroups; ++j) {
+        uint32_t za[kMats], zb[kMats];
+        float sa[kMats], sb[kMats];
 #pragma unroll
         for (int mat = 0; mat < kMats; ++mat) {
-          exchange<kPer>(q[mat][i][0], t);
-          exchange<kPer>(q[mat][i][1], t);
+          const int from = (lane & 28) + j / kLoads;
+          const uint32_t va = __shfl_sync(0xffffffffu, sz[mat][j % kLoads], from);
+          const uint32_t vb = __shfl_sync(0xffffffffu, sz[mat][j % kLoads], from + 2);
+          constexpr uint32_t kOne = kF16 ? 0x64u : 0x43u;
+          za[mat] = __byte_perm(va, kOne, 0x4040);
+          zb[mat] = __byte_perm(vb, kOne, 0x4040);
+          sa[mat] = __uint_as_float(va & 0xffffff00u);
+          sb[mat] = __uint_as_float(vb & 0xffffff00u);
         }
+        float sum[kMats][kNT][4];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          uint32_t za[kMats], zb[kMats];
-          float sa[kMats], sb[kMats];
+        for (int i = 0; i < 8 / kBoxGroups; ++i) {
+          const int w = j * (8 / kBoxGroups) + i;              // of the box's 8 words a lane
+          uint4 x[kNT];
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) x[nt] = lds_words(xb + w * x_word + 512 * nt);
 #pragma unroll
           for (int mat = 0; mat < kMats; ++mat) {
-            const uint32_t va = __shfl_sync(0xffffffffu, sz[mat][0][j], (lane & 28) + i);
-            const uint32_t vb = __shfl_sync(0xffffffffu, sz[mat][1][j], (lane & 28) + i);
-            constexpr uint32_t kOne = kF16 ? 0x64006400u : 0x43004300u;
-            za[mat] = kOne + (va >> 16) * 0x10001u;
-            zb[mat] = kOne + (vb >> 16) * 0x10001u;
-            sa[mat] = scale_value(va & 0xffffu, p.scale_bf16);
-            sb[mat] = scale_value(vb & 0xffffu, p.scale_bf16);
-          }
-          float sum[kMats][kNT][4] = {};
+            const uint32_t wa = q[mat][w >> 2][0][w & 3], wb = q[mat][w >> 2][1][w & 3];
 #pragma unroll
-          for (int w = j * (4 / kPer); w < (j + 1) * (4 / kPer); ++w) {
-            uint4 x[kNT];
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a[4] = {code_pair<kF16>(wa >> (8 * h), za[mat]), code_pair<kF16>(wb >> (8 * h), zb[mat]),
+                                     code_pair<kF16>(wa >> (8 * h + 4), za[mat]),
+                                     code_pair<kF16>(wb >> (8 * h + 4), zb[mat])};
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-              x[nt] = make_uint4(0u, 0u, 0u, 0u);
-              if (8 * nt + g < mt) x[nt] = xc[(w * mt + 8 * nt) * 4];
-            }
-#pragma unroll
-            for (int mat = 0; mat < kMats; ++mat) {
-              const uint4 &qa = q[mat][i][0], &qb = q[mat][i][1];
-              const uint32_t wa = w == 0 ? qa.x : w == 1 ? qa.y : w == 2 ? qa.z : qa.w;
-              const uint32_t wb = w == 0 ? qb.x : w == 1 ? qb.y : w == 2 ? qb.z : qb.w;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a[4] = {code_pair<kF16>(wa >> (8 * h), za[mat]), code_pair<kF16>(wb >> (8 * h), zb[mat]),
-                                       code_pair<kF16>(wa >> (8 * h + 4), za[mat]),
-                                       code_pair<kF16>(wb >> (8 * h + 4), zb[mat])};
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-                  mma_16<kF16>(sum[mat][nt], a, h ? x[nt].z : x[nt].x, h ? x[nt].w : x[nt].y);
-              }
+              for (int nt = 0; nt < kNT; ++nt)
+                mma_16<kF16>(sum[mat][nt], a, h ? x[nt].z : x[nt].x, h ? x[nt].w : x[nt].y, i + h > 0);
             }
           }
-#pragma unroll
-          for (int mat = 0; mat < kMats; ++mat)
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[mat][nt][e] = fmaf(e < 2 ? sa[mat] : sb[mat], sum[mat][nt][e], acc[mat][nt][e]);
         }
-        if (more) load_chunk(r + parts, i);
-      }
-      if (more)
 #pragma unroll
         for (int mat = 0; mat < kMats; ++mat)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) sz[mat][h][j] = next_sz[mat][h][j];
-    }
-    if (w1 < r_last) __syncthreads();        // the tokens may be overwritten
-  }
-
-  // every warp's sums to the CTA that owns the rows: [split, part][weight][token][row]
-  const int own = rows_cta / p.splits, own_log = 31 - __clz(own);
-  const uint32_t inbox = tc::smem_addr(smem) + p.inbox;
-  if (p.splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA runs
-#pragma unroll
-  for (int mat = 0; mat < kMats; ++mat)
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int tok = 8 * nt + 2 * t + (e & 1), row = 16 * rgroup + g + 8 * (e >> 1);
-        if (tok >= mt) continue;
-        const uint32_t at = inbox + 4u * ((((rank * parts + part) * kMats + mat) * mt + tok) * own + (row & (own - 1)));
-        if (p.splits > 1)
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, row >> own_log)), "f"(acc[mat][nt][e])
-                       : "memory");
-        else
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(acc[mat][nt][e]) : "memory");
+            for (int e = 0; e < 4; ++e)
+              acc[mat][nt][e] = fmaf(e < 2 ? sa[mat] : sb[mat], sum[mat][nt][e], acc[mat][nt][e]);
       }
-  if (p.splits > 1) tc::cluster_sync();
-  else __syncthreads();
-  const float* sums = reinterpret_cast<const float*>(smem + p.inbox);
-  for (int e = threadIdx.x; e < mt * own; e += kThreads) {
-    const int tok = e >> own_log, row = e & (own - 1);
-    const int64_t n = row0 + rank * own + row;
-    if (n >= p.N) continue;
-    float y[kMats] = {};
-    for (int k = 0; k < p.splits * parts; ++k)
+    }
+
+    // every warp's sums to the CTA that owns the rows: [split, part][weight][token][row].
+    // The wait: every CTA runs, and has read its last tile's sums.
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
-      for (int mat = 0; mat < kMats; ++mat) y[mat] += sums[((k * kMats + mat) * mt + tok) * own + row];
-    const float v = kMats == 2 ? gated(y[0], y[kMats - 1], p.curve) : y[0];
-    store_sum(p.y, p.y_elem, (m0 + tok) * p.N + n, v, p.accumulate);
+    for (int mat = 0; mat < kMats; ++mat)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = 8 * nt + 2 * t + (e & 1), row = row_warp + g + 8 * (e >> 1);
+          if (tok >= mt) continue;
+          const uint32_t at = inbox + 4u * ((((rank * parts + part) * kMats + mat) * mt + tok) * own + (row & (own - 1)));
+          if (p.splits > 1)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, row >> own_log)), "f"(acc[mat][nt][e])
+                         : "memory");
+          else
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(acc[mat][nt][e]) : "memory");
+        }
+    tc::cluster_sync();
+    const float* sums = reinterpret_cast<const float*>(smem + p.off_sums);
+    for (int e = threadIdx.x; e < mt * own; e += kThreads) {
+      const int tok = e >> own_log, row = e & (own - 1);
+      const int64_t n = static_cast<int64_t>(tile) * rows_tile + rank * own + row;
+      if (n >= p.N) continue;
+      float y[kMats] = {};
+      for (int k = 0; k < p.splits * parts; ++k)
+#pragma unroll
+        for (int mat = 0; mat < kMats; ++mat) y[mat] += sums[((k * kMats + mat) * mt + tok) * own + row];
+      const float v = kMats == 2 ? gated(y[0], y[kMats - 1], p.curve) : y[0];
+      store_sum(p.y, p.y_elem, (m0 + tok) * p.N + n, v, p.accumulate);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");       // the arrival of the last tile
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Launch shape of a call. Estimated time, in ns: a round (16 rows x 512 codes of
-// one weight or 256 of two, 4 KB a warp) takes 0.7 us alone and 1.43 us at HBM's
-// rate on a full GPU (16 warps an SM); a CTA stages its tokens at 40 bytes a ns
-// beside its neighbour; start and end take 1.5 us, a cluster 0.8 us more.
+// Launch shape of a call: tokens of a tile, parts of a slice, splits (the cluster)
+// and clusters for each token tile. Estimated time, in ns: a box a warp (32 KB an
+// SM and weight) takes 0.85 us, a tile 0.4 us more for its sums, 0.5 us in a
+// cluster; staging 60 bytes a ns.
 struct Int4Shape {
-  int parts_log, splits, window;
+  int tokens, parts_log, splits;
+  int64_t row_tiles, row_step, m_tiles;
 };
-constexpr int kMostStaged = 96 * 1024;        // two CTAs an SM, with their inboxes
 
-Int4Shape plan_int4(int64_t N, int rounds, int tokens, int mats, int64_t m_tiles, int sms) {
-  const int64_t round_bytes = static_cast<int64_t>(4 / mats) * 256 * tokens;
+Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)[4]) {
   Int4Shape best = {};
   int64_t best_cost = INT64_MAX;
-  for (int pl = 3; pl >= 0; --pl)
-    for (int s = 1; s <= 8 && s <= rounds && s <= 16 * (kWarps >> pl); s *= 2) {
-      const int64_t rows = 16 * (kWarps >> pl), ctas = (N + rows - 1) / rows * s * m_tiles;
-      const int64_t slice = (rounds + s - 1) / s, window = std::min<int64_t>(slice, kMostStaged / round_bytes);
-      const int64_t windows = (slice + window - 1) / window;
-      const int64_t each = (window + (1 << pl) - 1) >> pl;             // rounds of a warp and window
-      const int64_t slots = 2 * static_cast<int64_t>(sms), waves = (ctas + slots - 1) / slots;
-      const int64_t round = std::max<int64_t>(700, 1430 * std::min(ctas, slots) / slots);
-      const int64_t cost = waves * (windows * each * round + slice * round_bytes / 40 + (windows - 1) * 700 + 1500) +
-                           (s > 1 ? 800 : 0);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {pl, s, static_cast<int>(window)};
+  for (int tokens = 16; tokens >= 1; tokens /= 2) {
+    if (tokens > 1 && tokens / 2 >= M) continue;            // a smaller tile holds them all
+    const int mt = M >= tokens || tokens == 16 ? tokens : static_cast<int>(M);   // two column tiles hold 16
+    const int room = (kMostSmem - ring_bytes(mats) - sums_bytes(mats, mt)) / staged_bytes(mt);
+    for (int i = 0; i < 4 && (1 << i) <= boxes; ++i) {
+      const int s = 1 << i, slice = (boxes + s - 1) / s;
+      if (slice > room || ctas[i] < s) continue;
+      for (int pl = 0; pl <= 4; ++pl) {
+        const int64_t rows = 16 * (kWarps >> pl);
+        if (rows < s) continue;
+        Int4Shape sh = {mt, pl, s, (N + rows - 1) / rows, 0, (M + mt - 1) / mt};
+        const int64_t clusters = ctas[i] / s;
+        sh.row_step = std::min(sh.row_tiles, std::max<int64_t>(1, clusters / sh.m_tiles));
+        const int64_t waves = (sh.row_step * sh.m_tiles + clusters - 1) / clusters;
+        const int64_t passes = (sh.row_tiles + sh.row_step - 1) / sh.row_step;
+        const int64_t each = (slice + (1 << pl) - 1) >> pl;
+        const int64_t cost = waves * (passes * (each * 850 * mats + (s > 1 ? 900 : 400)) +
+                                      static_cast<int64_t>(slice) * staged_bytes(mt) / 60 + 2500);
+        if (cost < best_cost) {
+          best_cost = cost;
+          best = sh;
+        }
       }
     }
+    if (best_cost < INT64_MAX) break;                       // fewer tokens read the weight more often
+  }
   return best;
 }
 
 template <bool kF16, int kGroup, int kMats, int kNT>
-cudaError_t launch_int4_as(const Int4Call& c) {
+cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
   Int4Args a = {};
   a.x = static_cast<const uint16_t*>(c.x);
   for (int i = 0; i < 2; ++i) {
@@ -436,34 +473,31 @@ cudaError_t launch_int4_as(const Int4Call& c) {
   a.N = c.w[0].rows;
   a.K = c.w[0].cols;
   a.groups = static_cast<int>(a.K / kGroup);
-  constexpr int64_t kRound = 4 / kMats * 128;
-  a.rounds = static_cast<int>((a.K + kRound - 1) / kRound);
-  const int64_t m_tiles = (c.M + 8 * kNT - 1) / (8 * kNT);
-  const int tokens = static_cast<int>(std::min<int64_t>(c.M, 8 * kNT));
-  const Int4Shape shape = plan_int4(a.N, a.rounds, tokens, kMats, m_tiles, c.num_sms);
-  const int64_t rows = 16 * (kWarps >> shape.parts_log);
-  const int64_t grid = (a.N + rows - 1) / rows * m_tiles * shape.splits;
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  a.window = shape.window;
-  a.inbox = shape.window * (4 / kMats) * 256 * tokens;
+  a.boxes = static_cast<int>((a.K + kBoxCodes - 1) / kBoxCodes);
+  a.tokens = shape.tokens;
+  a.m_tiles = static_cast<int>(shape.m_tiles);
   a.parts_log = shape.parts_log;
   a.splits = shape.splits;
-  a.m_tiles = static_cast<int>(m_tiles);
+  a.row_tiles = static_cast<int>(shape.row_tiles);
+  a.row_step = static_cast<int>(shape.row_step);
+  const int slice = (a.boxes + shape.splits - 1) / shape.splits;
+  a.off_sums = ring_bytes(kMats) + slice * staged_bytes(shape.tokens);
   a.scale_bf16 = c.w[0].scale_elem == kElemBf16;
   a.curve = c.curve;
   a.y = c.y;
   a.y_elem = c.y_elem;
   a.accumulate = c.accumulate;
-  constexpr int kInbox = kWarps * 16 * kMats * 8 * kNT * 4;
   static std::once_flag once[kOnceDevices];
   once_per_device(once, c.device, [] {
     cudaFuncSetAttribute(int4_matmul_kernel<kF16, kGroup, kMats, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         kMostStaged + kInbox);
+                         kMostSmem);
   });
+  const int64_t grid = shape.row_step * shape.m_tiles * shape.splits;
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(a.inbox) + kWarps * 16 * kMats * tokens * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.off_sums) + sums_bytes(kMats, shape.tokens);
   cfg.stream = c.st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -473,8 +507,52 @@ cudaError_t launch_int4_as(const Int4Call& c) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = shape.splits > 1 ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, int4_matmul_kernel<kF16, kGroup, kMats, kNT>, a);
+}
+
+// CTAs that run at once in clusters of 1, 2, 4 and 8, one an SM (a cluster stays
+// within a group of SMs); the same for every kernel above.
+struct Int4Capacity {
+  int ctas[4];
+};
+
+Int4Capacity int4_capacity(const Int4Call& c) {
+  static std::once_flag once[kOnceDevices];
+  static Int4Capacity known[kOnceDevices];
+  Int4Capacity here = {};
+  auto find = [&] {
+    auto kernel = int4_matmul_kernel<false, 128, 1, 2>;
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+    for (int i = 0; i < 4; ++i) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1u << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(c.num_sms) << i);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kMostSmem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        clusters = i == 0 ? c.num_sms : 0;
+      }
+      here.ctas[i] = clusters << i;
+    }
+  };
+  if (c.device < 0 || c.device >= kOnceDevices) {
+    find();
+    return here;
+  }
+  once_per_device(once, c.device, [&] {
+    find();
+    known[c.device] = here;
+  });
+  return known[c.device];
 }
 
 template <typename F>
@@ -516,12 +594,16 @@ cudaError_t launch_int4_dequantize(const nf4_int4_weight& w, void* out, int out_
 }
 
 cudaError_t launch_int4_matmul(const Int4Call& c) {
+  const Int4Shape shape = plan_int4(c.M, c.w[0].rows, static_cast<int>((c.w[0].cols + kBoxCodes - 1) / kBoxCodes),
+                                    c.gated ? 2 : 1, int4_capacity(c).ctas);
+  if (shape.splits == 0) return cudaErrorInvalidConfiguration;
   return with_group(c.w[0].group, [&](auto g) {
     constexpr int kGroup = decltype(g)::value;
     auto go = [&](auto f16, auto mats) {
       constexpr bool kF16 = decltype(f16)::value;
       constexpr int kMats = decltype(mats)::value;
-      return c.M <= 8 ? launch_int4_as<kF16, kGroup, kMats, 1>(c) : launch_int4_as<kF16, kGroup, kMats, 2>(c);
+      return shape.tokens <= 8 ? launch_int4_as<kF16, kGroup, kMats, 1>(c, shape)
+                               : launch_int4_as<kF16, kGroup, kMats, 2>(c, shape);
     };
     if (c.x_f16) {
       if (c.gated) return go(std::true_type{}, std::integral_constant<int, 2>{});

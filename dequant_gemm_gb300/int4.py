@@ -19,6 +19,7 @@ from .gated import _activation
 from .norm import _refused, _require_matrix
 
 INT4_GROUPS = (32, 64, 128)
+INT4_MAX_COLS = 262144         # NF4_INT4_MAX_COLS
 _SCALES = {torch.bfloat16: ELEM[torch.bfloat16], torch.float16: ELEM[torch.float16]}
 _U8, _empty, _byref = torch.uint8, torch.empty, ctypes.byref
 
@@ -179,6 +180,8 @@ def _check_x(X, **weights):
     _require(X, "X", X.dtype)
     for name, w in weights.items():
         _check_int4(w, name, X.device)
+        if w.cols > INT4_MAX_COLS:
+            raise ValueError(f"{name}: {w.cols} columns; products take {INT4_MAX_COLS} at most (dequantize longer rows)")
         if X.dim() != 2 or X.shape[1] != w.cols:
             raise ValueError(f"X must be [M, {w.cols}]")
 
@@ -194,7 +197,7 @@ def nf4_int4_matmul_fwd(X: torch.Tensor, w: Int4Weight, out: torch.Tensor | None
     fp32, bf16 or fp16 [M, rows]. For few tokens: the weight is read once for
     every 16."""
     struct = _plain_int4(w, X.device) if _plain_x(X) else None
-    if struct is None or X.shape[1] != struct.cols:
+    if struct is None or X.shape[1] != struct.cols or struct.cols > INT4_MAX_COLS:
         _check_x(X, w=w)
         struct = w.c_struct()
     M = X.shape[0]
@@ -232,7 +235,7 @@ def nf4_int4_gated_fwd(X: torch.Tensor, gate: Int4Weight, up: Int4Weight, activa
     a = b = None
     if _plain_x(X):
         a, b = _plain_int4(gate, X.device), _plain_int4(up, X.device)
-    if a is None or b is None or X.shape[1] != a.cols:
+    if a is None or b is None or X.shape[1] != a.cols or a.cols > INT4_MAX_COLS:
         _check_x(X, gate=gate)
         _check_int4(up, "up", X.device)
         a, b = gate.c_struct(), up.c_struct()

@@ -105,6 +105,9 @@ typedef enum nf4_elem {
 /* Most weights one nf4_matmul_fwd_group call takes. */
 #define NF4_GROUP_MAX 4
 
+/* Longest rows that the products with 4-bit weights in groups take. */
+#define NF4_INT4_MAX_COLS 262144
+
 /* Values along a row that share a scale of the 8-bit floating point format. */
 #define NF4_FP8_BLOCK 128
 
@@ -435,7 +438,8 @@ nf4_status nf4_int4_dequantize(const nf4_int4_weight* w, void* out, int32_t out_
 
 /* Y = X * value(w)^T for few tokens: X device [M, cols] of x_elem NF4_BF16 or
  * NF4_F16, Y device [M, rows] of y_elem (NF4_F32, NF4_BF16 or NF4_F16; aligned
- * to its elements), any rows. flags: NF4_ACCUMULATE adds to Y's contents.
+ * to its elements), any rows, cols at most NF4_INT4_MAX_COLS (NF4_ERR_SHAPE
+ * beyond). flags: NF4_ACCUMULATE adds to Y's contents.
  * (code - zero) and X enter the tensor cores exactly, in X's type; the sums of
  * a group are fp32, multiplied by the scale in fp32 and added up in fp32, in a
  * fixed order; Y is rounded once. Any M: the weight is read once for every 16

@@ -104,6 +104,16 @@ def test_int4_refuses():
             nf4.nf4_int4_gated_fwd(x, w, up, **kw)
 
 
+def test_int4_products_refuse_longer_rows():
+    K = 262144 + 128
+    x, w = torch.zeros(1, K, dtype=BF16), int4(1, K)
+    for call in (nf4.nf4_int4_matmul_fwd, lambda x, w: nf4.nf4_int4_gated_fwd(x, w, w)):
+        with pytest.raises(ValueError, match="262144 at most"):
+            call(x, w)
+    assert nf4.lib().nf4_int4_matmul_fwd(P, 1, 1, w4(1, K), P, 0, 0, None) == 2
+    assert nf4.lib().nf4_int4_gated_fwd(P, 1, 1, w4(1, K), w4(1, K), 0, P, 0, None) == 2
+
+
 def q8(rows, cols, block_rows=1, codes=P, scale=P):
     return ctypes.byref(nf4.nf4_fp8_tensor(codes, scale, rows, cols, block_rows))
 

@@ -135,6 +135,21 @@ def test_gated(M, N, K, group):
             assert_near(y, f * u, e * (1 + UNIT[dt]) + UNIT[dt] * (f * u).abs() + TINY[dt] + 1e-38)
 
 
+@pytest.mark.parametrize("M, N, K", [(1, 20, 262144), (3, 40, 262144), (16, 20, 100352), (20, 33, 60000 // 128 * 128),
+                                     (1, 40000, 256), (12, 5000, 384), (300, 600, 256)])
+def test_longest_rows_and_many_tiles(M, N, K):
+    """Fewer tokens a tile where the reduction is long, several row tiles a CTA
+    where there are many rows."""
+    x = make(M, K, M + N, dtype=BF16).to(DEV)
+    a, b = weight(N, K, 128), weight(N, K, 128, seed=6)
+    ref, bound = product(x, a)
+    assert_near(nf4.nf4_int4_matmul_fwd(x, a), ref, bound + U24 * ref.abs())
+    (g, eg), (u, eu) = (ref, bound), product(x, b)
+    f, _ = on_gpu(o.act, g, "silu")
+    e = u.abs() * 1.13 * eg + (f.abs() + 1.13 * eg) * eu + relative(g, "silu") * 1.01 * (f * u).abs()
+    assert_near(nf4.nf4_int4_gated_fwd(x, a, b, out_dtype=F32), f * u, e * (1 + U24) + U24 * (f * u).abs() + 1e-38)
+
+
 @pytest.mark.parametrize("M", [1, 5, 16, 20])
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_one_hot_tokens_return_the_weight(M, group):
