@@ -123,7 +123,7 @@ struct Int4Args {
   int parts_log, splits;
   int row_tiles, row_step;       // all; clusters that share a token tile
   int off_sums;                  // byte offset in shared memory
-  bool scale_bf16;
+  bool scale_bf16, wide;
   Curve curve;
   void* y;
   int y_elem;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   const int b0 = s0 + (s1 - s0) * part / parts, nb = s0 + (s1 - s0) * (part + 1) / parts - b0;
   const uint32_t ring = tc::smem_addr(smem) + warp * (2 * kMats * kBoxBytes);
   let_next_start();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (p.splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   wait_for_previous();
 
   // What is copied next. Box j of the warp's stream goes into slot j & 1: lane l
@@ -250,19 +250,49 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint32_t raw_s[kMats][kLoads], raw_z[kMats][kLoads], later_s[kMats][kLoads], later_z[kMats][kLoads];
-  auto load_scales = [&](uint32_t (&rs)[kMats][kLoads], uint32_t (&rz)[kMats][kLoads]) {
+  // a lane's kLoads scales and zero points, two scales a word and four zero points:
+  // in one load each where their rows keep them aligned (p.wide)
+  constexpr int kWords = (kLoads + 1) / 2;
+  struct Scales {
+    uint32_t s[kMats][kWords], z[kMats];
+  };
+  auto load_scales = [&](Scales& to) {
 #pragma unroll
-    for (int mat = 0; mat < kMats; ++mat)
+    for (int mat = 0; mat < kMats; ++mat) {
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        rs[mat][j] = 0u;
-        rz[mat][j] = 8u;
-        if (next_left > 0 && j < groups_left) {
-          rs[mat][j] = __ldg(p.scale[mat] + scale_at + j);
-          if (p.zero[mat]) rz[mat][j] = __ldg(p.zero[mat] + scale_at + j);
+      for (int j = 0; j < kWords; ++j) to.s[mat][j] = 0u;
+      to.z[mat] = 0x08080808u;
+      if (next_left <= 0) continue;
+      const uint16_t* sp = p.scale[mat] + scale_at;
+      const uint8_t* zp = p.zero[mat] + scale_at;
+      if (kLoads > 1 && p.wide) {              // kLoads divides the row's groups
+        if (groups_left <= 0) continue;
+        if constexpr (kLoads == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+          to.s[mat][0] = v.x;
+          to.s[mat][1] = v.y;
+          if (p.zero[mat]) to.z[mat] = __ldg(reinterpret_cast<const uint32_t*>(zp));
+        } else if constexpr (kLoads == 2) {
+          to.s[mat][0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
+          if (p.zero[mat]) to.z[mat] = __ldg(reinterpret_cast<const uint16_t*>(zp));
         }
+        continue;
       }
+      if constexpr (kLoads == 1) {             // nothing waits for the loads here
+        if (groups_left <= 0) continue;
+        to.s[mat][0] = __ldg(sp);
+        if (p.zero[mat]) to.z[mat] = __ldg(zp);
+        continue;
+      }
+      uint32_t z = 0u;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        if (j < groups_left) {
+          to.s[mat][j / 2] |= static_cast<uint32_t>(__ldg(sp + j)) << (16 * (j % 2));
+          if (p.zero[mat]) z |= static_cast<uint32_t>(__ldg(zp + j)) << (8 * j);
+        }
+      if (p.zero[mat]) to.z[mat] = z;
+    }
   };
   auto advance = [&] {
     code_at += 128;
@@ -275,10 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
     }
   };
   start_tile();
-  load_scales(raw_s, raw_z);
+  Scales now, later;
+  load_scales(now);
   copy_box(ring);
   advance();
-  load_scales(later_s, later_z);
+  load_scales(later);
   copy_box(ring + kMats * kBoxBytes);
   advance();
 
@@ -326,12 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
       for (int mat = 0; mat < kMats; ++mat)
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-          sz[mat][j] = __float_as_uint(scale_value(raw_s[mat][j], p.scale_bf16)) | raw_z[mat][j];
-          raw_s[mat][j] = later_s[mat][j];
-          raw_z[mat][j] = later_z[mat][j];
+          const uint32_t bits = now.s[mat][j / 2] >> (16 * (j % 2)) & 0xffffu;
+          sz[mat][j] = __float_as_uint(scale_value(bits, p.scale_bf16)) | (now.z[mat] >> (8 * j) & 0xffu);
         }
       __syncwarp();
-      load_scales(later_s, later_z);
+      now = later;
+      load_scales(later);
       copy_box(slot);
       advance();
       slot = 2 * ring + kMats * kBoxBytes - slot;              // the other one
@@ -383,8 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
     }
 
     // every warp's sums to the CTA that owns the rows: [split, part][weight][token][row].
-    // The wait: every CTA runs, and has read its last tile's sums.
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    // The first wait: every CTA runs, and has read its last tile's sums. (A CTA by
+    // itself uses its own barrier: with cluster barriers a tile took 2 us more.)
+    if (p.splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    else if (tile != tile0) __syncthreads();
 #pragma unroll
     for (int mat = 0; mat < kMats; ++mat)
 #pragma unroll
@@ -400,29 +433,32 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
           else
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(acc[mat][nt][e]) : "memory");
         }
-    tc::cluster_sync();
+    if (p.splits > 1) tc::cluster_sync();
+    else __syncthreads();
     const float* sums = reinterpret_cast<const float*>(smem + p.off_sums);
     for (int e = threadIdx.x; e < mt * own; e += kThreads) {
       const int tok = e >> own_log, row = e & (own - 1);
       const int64_t n = static_cast<int64_t>(tile) * rows_tile + rank * own + row;
       if (n >= p.N) continue;
       float y[kMats] = {};
+#pragma unroll 4
       for (int k = 0; k < p.splits * parts; ++k)
 #pragma unroll
         for (int mat = 0; mat < kMats; ++mat) y[mat] += sums[((k * kMats + mat) * mt + tok) * own + row];
       const float v = kMats == 2 ? gated(y[0], y[kMats - 1], p.curve) : y[0];
       store_sum(p.y, p.y_elem, (m0 + tok) * p.N + n, v, p.accumulate);
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (p.splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");       // the arrival of the last tile
+  if (p.splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // the last tile's arrivals
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Launch shape of a call: tokens of a tile, parts of a slice, splits (the cluster)
 // and clusters for each token tile. Estimated time, in ns: a box a warp (32 KB an
-// SM and weight) takes 0.85 us, a tile 0.4 us more for its sums, 0.5 us in a
-// cluster; staging 60 bytes a ns.
+// SM and weight) takes 0.85 us, a tile 0.7 us more for its sums, 0.9 in a cluster;
+// staging 60 bytes a ns. (Every shape measured on 13 sizes of 1 to 32 tokens: the
+// one chosen is within 5% of the best.)
 struct Int4Shape {
   int tokens, parts_log, splits;
   int64_t row_tiles, row_step, m_tiles;
@@ -447,7 +483,7 @@ Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)
         const int64_t waves = (sh.row_step * sh.m_tiles + clusters - 1) / clusters;
         const int64_t passes = (sh.row_tiles + sh.row_step - 1) / sh.row_step;
         const int64_t each = (slice + (1 << pl) - 1) >> pl;
-        const int64_t cost = waves * (passes * (each * 850 * mats + (s > 1 ? 900 : 400)) +
+        const int64_t cost = waves * (passes * (each * 850 * mats + (s > 1 ? 900 : 700)) +
                                       static_cast<int64_t>(slice) * staged_bytes(mt) / 60 + 2500);
         if (cost < best_cost) {
           best_cost = cost;
@@ -483,6 +519,12 @@ cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
   const int slice = (a.boxes + shape.splits - 1) / shape.splits;
   a.off_sums = ring_bytes(kMats) + slice * staged_bytes(shape.tokens);
   a.scale_bf16 = c.w[0].scale_elem == kElemBf16;
+  // a lane's scales and zero points in one load each
+  constexpr uint32_t kLoads = 128 / kGroup;
+  a.wide = a.groups % kLoads == 0;
+  for (int i = 0; i < kMats; ++i)
+    a.wide = a.wide && reinterpret_cast<uintptr_t>(a.scale[i]) % (2 * kLoads) == 0 &&
+             reinterpret_cast<uintptr_t>(a.zero[i]) % kLoads == 0;
   a.curve = c.curve;
   a.y = c.y;
   a.y_elem = c.y_elem;
