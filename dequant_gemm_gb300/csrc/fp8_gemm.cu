@@ -558,8 +558,13 @@ fp8_pair_kernel(const __grid_constant__ PairMaps<kMode> maps, const __grid_const
           box16(acc + 64, 1);
           send(maps.u, c0, 1);
         }
+        if (p.curve.k1 == 0.0f) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) acc[j] = gated(acc[j], acc[64 + j], p.curve);
+          for (int j = 0; j < 64; ++j) acc[j] = gated<false>(acc[j], acc[64 + j], p.curve);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) acc[j] = gated<true>(acc[j], acc[64 + j], p.curve);
+        }
         if (p.y_scale) {
           float a = 0.0f;
 #pragma unroll

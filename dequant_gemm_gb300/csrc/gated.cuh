@@ -11,31 +11,40 @@
 
 namespace nf4 {
 
+// The exponent of 2 that sigma(p) = 1 / (1 + 2^t) takes: t = g (k0 + k1 g^2),
+// k = -log2(e) c; c = -k / log2(e) for the derivative.
 struct Curve {
+  float k0, k1;            // k1 = 0: SiLU
   float c0, c1;
 };
 inline Curve curve_of(int32_t activation) {
-  constexpr double kGelu = 1.5957691216057308;             // 2 sqrt(2 / pi)
-  return activation == NF4_GELU_TANH
-             ? Curve{static_cast<float>(kGelu), static_cast<float>(kGelu * 0.044715)}
-             : Curve{1.0f, 0.0f};
+  constexpr double kLog2e = 1.4426950408889634, kGelu = 1.5957691216057308;    // 2 sqrt(2 / pi)
+  const double c0 = activation == NF4_GELU_TANH ? kGelu : 1.0;
+  const double c1 = activation == NF4_GELU_TANH ? kGelu * 0.044715 : 0.0;
+  return {static_cast<float>(-kLog2e * c0), static_cast<float>(-kLog2e * c1), static_cast<float>(c0),
+          static_cast<float>(c1)};
 }
 
 // sigma(p(g)), by the base-2 exponential and the reciprocal of PTX (2^-22 and
 // 1 ulp). The exponent's rounding makes the relative error grow with |p|, by
-// 2^-23 a unit, where sigma is small (p < 0). g^2 is kept from infinity, which
-// c1 = 0 would turn into NaN; past 1e30 sigma is 0 or 1 whatever the cubic term.
-__device__ __forceinline__ float gate_sigma(float g, Curve c) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float t = g * (fmaf(c.c1, fminf(g * g, 1e30f), c.c0) * -kLog2e);
+// 2^-23 a unit, where sigma is small (p < 0). kCubic false: k1 is 0, whatever g^2.
+__device__ __forceinline__ float sigma_of(float t) {
   float e, s;
   asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
   asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
   return s;
 }
+template <bool kCubic>
+__device__ __forceinline__ float gate_sigma(float g, Curve c) {
+  return sigma_of(g * (kCubic ? fmaf(c.k1, g * g, c.k0) : c.k0));
+}
 
 // act(g) u
-__device__ __forceinline__ float gated(float g, float u, Curve c) { return g * gate_sigma(g, c) * u; }
+template <bool kCubic>
+__device__ __forceinline__ float gated(float g, float u, Curve c) { return g * gate_sigma<kCubic>(g, c) * u; }
+__device__ __forceinline__ float gated(float g, float u, Curve c) {
+  return c.k1 == 0.0f ? gated<false>(g, u, c) : gated<true>(g, u, c);
+}
 
 // One gated forward as the launcher takes it: y = act(A Wg^T) * (A Wu^T).
 struct GatedFwdCall {
