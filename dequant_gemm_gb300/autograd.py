@@ -14,9 +14,9 @@ the library's kernels. Weights may be NF4, FP4 or int8 ("bitsandbytes", the
 zenbit.int8 bullet).
 
 The second half of the module does the same for the 8-bit floating point
-products and the RMS norm in front of them. Rounding to 8 bits passes its
-gradient through; gradients of a product's output are rounded to 8 bits
-themselves (1 x 128 blocks) before they meet the weight.
+products, the RMS norm in front of them and the gated block between them.
+Rounding to 8 bits passes its gradient through; gradients of a product's output
+are rounded to 8 bits themselves (1 x 128 blocks) before they meet the weight.
 """
 from __future__ import annotations
 
@@ -24,9 +24,9 @@ import functools
 
 import torch
 
-from . import (FP8Tensor, NF4Weight, nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd,
-               nf4_fp8_quantize, nf4_matmul_bwd_dx, nf4_matmul_fwd, nf4_quantize,
-               nf4_rmsnorm_bwd, nf4_rmsnorm_fwd)
+from . import (FP8Tensor, NF4Weight, nf4_fp8_gated_bwd, nf4_fp8_gated_bwd_dx, nf4_fp8_gated_fwd,
+               nf4_fp8_matmul_bwd_dx, nf4_fp8_matmul_fwd, nf4_fp8_quantize, nf4_matmul_bwd_dx,
+               nf4_matmul_fwd, nf4_quantize, nf4_rmsnorm_bwd, nf4_rmsnorm_fwd)
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
@@ -165,8 +165,8 @@ class _Once(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, gg):
-        raise RuntimeError("the RMS norm's gradients can be taken once: they are not differentiable "
-                           "themselves (second-order gradients)")
+        raise RuntimeError("the gradients of the RMS norm and of the gated block can be taken once: they are "
+                           "not differentiable themselves (second-order gradients)")
 
 
 def _once(backward):
@@ -338,3 +338,122 @@ class FP8Linear(_Frozen):
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, fp8"
+
+
+def _gated_mlp(q: FP8Tensor, gate, up, down, activation, out_dtype, keep: bool):
+    """(y, g, u): y of an 8-bit operand, g and u what its gradient needs (None unless keep)."""
+    a, g, u = nf4_fp8_gated_fwd(q, gate, up, activation=activation, save=keep)
+    return nf4_fp8_matmul_fwd(a, down, out_dtype=out_dtype), g, u
+
+
+def _gated_mlp_grad(gy, g, u, gate, up, down, activation, out_dtype):
+    """The gradient of the 8-bit operand's values, [M, cols] of out_dtype (fp32 or bf16)."""
+    da = nf4_fp8_matmul_bwd_dx(nf4_fp8_quantize(_matrix(gy, down.rows)), down, out_dtype=out_dtype)
+    return nf4_fp8_gated_bwd_dx(*nf4_fp8_gated_bwd(da, g, u, activation=activation), gate, up, out_dtype=out_dtype)
+
+
+class FP8GatedMLPFunction(torch.autograd.Function):
+    """y = (act(x gate^T) * (x up^T)) down^T, x [..., cols] (fp32, bf16 or fp16)
+    and the product in front of down rounded to 8 bits, y of `out_dtype` (fp32 or
+    bf16); differentiable in x, once."""
+
+    @staticmethod
+    def forward(ctx, x, gate, up, down, activation="silu", out_dtype=torch.bfloat16):
+        ctx.weights, ctx.activation = (gate, up, down), activation
+        keep = ctx.needs_input_grad[0]
+        q = nf4_fp8_quantize(_matrix(x, x.shape[-1]))
+        y, g, u = _gated_mlp(q, gate, up, down, activation, out_dtype, keep)
+        if keep:
+            ctx.save_for_backward(x, g, u)       # x: for the graph of a gradient that may not be used (_once)
+        return y.reshape(*x.shape[:-1], down.rows)
+
+    @staticmethod
+    @_once
+    def backward(ctx, gy):
+        x, g, u = ctx.saved_tensors
+        out = torch.bfloat16 if x.dtype == torch.bfloat16 else torch.float32
+        dx = _gated_mlp_grad(gy, g, u, *ctx.weights, ctx.activation, out)
+        return dx.reshape(x.shape).to(x.dtype), None, None, None, None, None
+
+
+def fp8_gated_mlp(x: torch.Tensor, gate: FP8Tensor, up: FP8Tensor, down: FP8Tensor, activation: str = "silu",
+                  out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The gated feed-forward block on frozen 8-bit weights; differentiable in x."""
+    return FP8GatedMLPFunction.apply(x, gate, up, down, activation, out_dtype)
+
+
+class NormFP8GatedMLPFunction(torch.autograd.Function):
+    """The norm and the gated block that reads its output, joined: (h, y)."""
+
+    @staticmethod
+    def forward(ctx, x, norm_weight, residual, eps, gate, up, down, activation, out_dtype):
+        shape = x.shape
+        rows = _matrix(x, shape[-1])
+        res = None if residual is None else _aligned(residual.reshape(rows.shape))
+        q, h, rstd = nf4_rmsnorm_fwd(rows, _aligned(norm_weight), res, eps=eps,
+                                     out_dtype=torch.float8_e4m3fn, save_rstd=True)
+        h = x if residual is None else h.reshape(shape)
+        keep = any(ctx.needs_input_grad[:3])
+        y, g, u = _gated_mlp(q, gate, up, down, activation, out_dtype, keep)
+        ctx.weights, ctx.activation, ctx.x_dtype, ctx.shape = (gate, up, down), activation, x.dtype, shape
+        ctx.res_shape = None if residual is None else residual.shape
+        ctx.set_materialize_grads(False)     # an output that nothing used costs no product
+        if keep:
+            ctx.save_for_backward(h, norm_weight, rstd, g, u)    # h: this Function's own input or output (_once)
+        # an output may not be the input itself
+        return (h.clone() if residual is None else h), y.reshape(*shape[:-1], down.rows)
+
+    @staticmethod
+    @_once
+    def backward(ctx, gh, gy):
+        h, norm_weight, rstd, g, u = ctx.saved_tensors
+        h = _matrix(h, h.shape[-1])
+        if gy is None:
+            dy = torch.zeros_like(h)
+        else:
+            out = torch.bfloat16 if h.dtype == torch.bfloat16 else torch.float32
+            dy = _gated_mlp_grad(gy, g, u, *ctx.weights, ctx.activation, out).to(h.dtype)
+        dh = None if gh is None else _aligned(gh.reshape(h.shape).to(h.dtype))
+        dx, dweight = nf4_rmsnorm_bwd(dy, h, _aligned(norm_weight), rstd, dh=dh)
+        dx = dx.reshape(ctx.shape)
+        return (dx.to(ctx.x_dtype), dweight, dx.reshape(ctx.res_shape) if ctx.res_shape else None,
+                *[None] * 6)
+
+
+def norm_fp8_gated_mlp(x: torch.Tensor, norm_weight: torch.Tensor, gate: FP8Tensor, up: FP8Tensor,
+                       down: FP8Tensor, residual=None, eps: float = 1e-6, activation: str = "silu",
+                       out_dtype: torch.dtype = torch.bfloat16):
+    """h = x + residual and the gated block of rms_norm(h): (h, y). Differentiable in
+    x, the residual and the norm's weight."""
+    return NormFP8GatedMLPFunction.apply(x, norm_weight, residual, eps, gate, up, down, activation, out_dtype)
+
+
+class FP8GatedMLP(_Frozen):
+    """A frozen gated feed-forward block (no biases) holding its three weights in
+    8 bits: gate and up [inner, features], down [features_out, inner]."""
+    _frozen = tuple(f"{n}_{part}" for n in ("gate", "up", "down") for part in ("codes", "scale"))
+
+    def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, activation: str = "silu",
+                 out_dtype: torch.dtype = torch.bfloat16):
+        super().__init__()
+        if gate.dim() != 2 or gate.shape != up.shape or down.dim() != 2 or down.shape[1] != gate.shape[0]:
+            raise ValueError("gate and up must be [inner, features] and down [features_out, inner], got "
+                             f"{tuple(gate.shape)}, {tuple(up.shape)} and {tuple(down.shape)}")
+        for name, w in (("gate", gate), ("up", up), ("down", down)):
+            q = nf4_fp8_quantize(_aligned(w.detach()), block_rows=128)
+            self.register_buffer(f"{name}_codes", q.codes)
+            self.register_buffer(f"{name}_scale", q.scale)
+        self.in_features, self.inner_features, self.out_features = gate.shape[1], gate.shape[0], down.shape[0]
+        self.activation, self.out_dtype = activation, out_dtype
+
+    def quantized_weights(self) -> tuple[FP8Tensor, FP8Tensor, FP8Tensor]:
+        """(gate, up, down)"""
+        return tuple(FP8Tensor(getattr(self, f"{n}_codes"), getattr(self, f"{n}_scale"), 128)
+                     for n in ("gate", "up", "down"))
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return fp8_gated_mlp(x, *self.quantized_weights(), self.activation, self.out_dtype)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, inner_features={self.inner_features}, "
+                f"out_features={self.out_features}, {self.activation}, fp8")

@@ -1,6 +1,7 @@
 """A transformer's MLP block on the 8-bit operators: the norm adds the residual
-and writes the 8-bit operand that the gate and up products read, the activation
-is rounded to 8 bits for the down product, and the stream goes on in 32 bits.
+and writes the 8-bit operand that the gate and up products read, one kernel takes
+both, the activation and its product to the down product's 8-bit operand, and the
+stream goes on in 32 bits.
 
     python examples/fp8_mlp_block.py [hidden] [inner] [tokens]
 
@@ -15,7 +16,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import dequant_gemm_gb300 as nf4  # noqa: E402
-from dequant_gemm_gb300.autograd import FP8Linear, norm_fp8_linears  # noqa: E402
+from dequant_gemm_gb300.autograd import FP8GatedMLP, norm_fp8_gated_mlp  # noqa: E402
 
 
 class FP8MLPBlock(torch.nn.Module):
@@ -25,14 +26,13 @@ class FP8MLPBlock(torch.nn.Module):
     def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, eps: float = 1e-6):
         super().__init__()
         self.norm_weight = torch.nn.Parameter(torch.ones(gate.shape[1], device=gate.device))
-        self.gate, self.up, self.down = FP8Linear(gate), FP8Linear(up), FP8Linear(down)
+        self.mlp = FP8GatedMLP(gate, up, down)
         self.eps = eps
 
     def forward(self, x, stream):
-        h, (g, u) = norm_fp8_linears(x, self.norm_weight, [self.gate.quantized_weight(),
-                                                           self.up.quantized_weight()],
-                                     residual=stream, eps=self.eps)
-        return self.down(torch.nn.functional.silu(g) * u), h
+        h, y = norm_fp8_gated_mlp(x, self.norm_weight, *self.mlp.quantized_weights(), residual=stream,
+                                  eps=self.eps)
+        return y, h
 
 
 def torch_block(x, stream, norm_weight, gate, up, down, eps=1e-6):
