@@ -89,7 +89,11 @@ cudaError_t launch_gated_bwd(const void* dy, int dy_elem, const void* g, const v
                              int64_t rows, int64_t cols, Curve curve, uint8_t* dg, float* dg_scale,
                              uint8_t* du, float* du_scale, cudaStream_t st);
 
-// 4-bit weights in groups (include/nf4gemm.h states the format).
+// 4-bit weights in groups (include/nf4gemm.h states the format): a scale's value.
+__device__ __forceinline__ float scale_value(uint32_t bits, bool bf16) {
+  return bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+
 cudaError_t launch_int4_quantize(const void* w, int w_elem, int64_t rows, int64_t cols, int group,
                                  bool scale_bf16, uint8_t* codes, void* scale, uint8_t* zero,
                                  cudaStream_t st);

@@ -1,116 +1,5 @@
-// Uniform 4-bit weights in groups of 32, 64 or 128 along a row, each with a
-// 16-bit scale and (optionally) a zero point: quantization, dequantization and
-// products of few tokens. include/nf4gemm.h states the format.
-#include <algorithm>
-
-#include "gated.cuh"
-#include "tc.cuh"
-
-namespace nf4 {
-namespace {
-
-__device__ __forceinline__ float scale_value(uint32_t bits, bool bf16) {
-  return bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
-}
-
-// A streaming pass. 8 consecutive values a thread and step, a group in kGroup / 8
-// neighbouring lanes; kQuantUnroll steps keep that many loads in flight.
-//
-// rint(w / s) needs the quotient as IEEE division rounds it (a tie of the rounded
-// quotient is a tie). q = RN(w r) with r = RN(1 / s) is within an ulp, its remainder
-// w - q s is exact in one FMA, and RN(q + rem r) is the correctly rounded quotient
-// (Markstein) where nothing leaves the normal range: s >= 2^-64 (smaller scales
-// divide), and quotients near a half or above, which alone matter.
-constexpr int kQuantUnroll = 4;
-constexpr float kSmallScale = 5.421010862427522e-20f;     // 2^-64
-
-template <int kElem, int kGroup, bool kZero>
-__global__ void __launch_bounds__(256)
-int4_quantize_kernel(const void* __restrict__ w, int64_t runs, bool bf16, uint32_t* __restrict__ codes,
-                     uint16_t* __restrict__ scale, uint8_t* __restrict__ zero) {
-  let_next_start();
-  wait_for_previous();
-  constexpr int kLanes = kGroup / 8;
-  constexpr float kMagic = 12582912.0f;                    // 1.5 2^23: x + kMagic holds rint(x) in its low bits
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kQuantUnroll) + threadIdx.x;
-  float v[kQuantUnroll][8];
-#pragma unroll
-  for (int i = 0; i < kQuantUnroll; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    if (first + 256 * i < runs) load8<kElem>(w, 8 * (first + 256 * i), v[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < kQuantUnroll; ++i) {
-    const int64_t run = first + 256 * i;
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo = fminf(lo, kZero ? v[i][j] : -fabsf(v[i][j]));
-      if (kZero) hi = fmaxf(hi, v[i][j]);
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      if (kZero) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const float range = kZero ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(-lo, 7.0f);
-    const uint32_t bits = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(range))
-                               : __half_as_ushort(__float2half_rn(range));
-    const float s = scale_value(bits, bf16);
-    int z = kZero ? 0 : 8;
-    if (kZero && s != 0.0f) z = static_cast<int>(fminf(rintf(__fdiv_rn(-lo, s)), 15.0f));
-    const float r = __frcp_rn(s);
-    uint32_t out = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float q = __fmul_rn(v[i][j], r);
-      q = __fmaf_rn(__fmaf_rn(-q, s, v[i][j]), r, q);
-      if (s < kSmallScale) q = s == 0.0f ? 0.0f : __fdiv_rn(v[i][j], s);
-      const int code = __float_as_int(__fadd_rn(q, kMagic)) - __float_as_int(kMagic) + z;
-      out |= static_cast<uint32_t>(min(max(code, 0), 15)) << (4 * (j ^ 1));     // the even element in the high half
-    }
-    if (run >= runs) continue;
-    codes[run] = out;
-    if (run % kLanes == 0) {
-      scale[run / kLanes] = static_cast<uint16_t>(bits);
-      if (kZero) zero[run / kLanes] = static_cast<uint8_t>(z);
-    }
-  }
-}
-
-// 8 codes a thread and step, so that a warp's stores are whole lines.
-constexpr int kDequantUnroll = 4;
-
-template <int kElem>
-__global__ void __launch_bounds__(256)
-int4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint16_t* __restrict__ scale,
-                       const uint8_t* __restrict__ zero, int64_t runs, int lanes_log, bool bf16,
-                       void* __restrict__ out) {
-  let_next_start();
-  wait_for_previous();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kDequantUnroll) + threadIdx.x;
-  uint32_t q[kDequantUnroll], s[kDequantUnroll], z[kDequantUnroll];
-#pragma unroll
-  for (int i = 0; i < kDequantUnroll; ++i) {
-    const int64_t run = min(first + 256 * i, runs - 1);
-    q[i] = codes[run];
-    s[i] = scale[run >> lanes_log];
-    z[i] = zero ? zero[run >> lanes_log] : 8u;
-  }
-#pragma unroll
-  for (int i = 0; i < kDequantUnroll; ++i) {
-    if (first + 256 * i >= runs) break;
-    const float f = scale_value(s[i], bf16);
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)      // 2^23 + n has the whole number n in its low bits: n - z is exact
-      v[j] = (__uint_as_float(0x4b000000u | (q[i] >> (4 * (j ^ 1)) & 15u)) - __uint_as_float(0x4b000000u | z[i])) * f;
-    store8<kElem>(out, 8 * (first + 256 * i), v);
-  }
-}
-
-// ------------------------------------------------------------- products --
+// Products of few tokens with uniform 4-bit weights in groups of 32, 64 or 128
+// along a row (include/nf4gemm.h states the format):
 // Y[m, n] = sum over groups of s[n, j] sum_{k in j} (q[n, k] - z[n, j]) x[m, k],
 // alone or (kMats = 2) for two weights whose sums meet as act(G) U.
 //
@@ -139,6 +28,14 @@ int4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint16_t* __res
 //    handed to the others by shuffles.
 //  * Every warp leaves its sums of a tile in shared memory of the CTA that owns the
 //    rows, which adds them in a fixed order: repeatable, no workspace.
+#include <algorithm>
+
+#include "gated.cuh"
+#include "tc.cuh"
+
+namespace nf4 {
+namespace {
+
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBoxBytes = 16 * 128;            // 16 rows x 256 codes
@@ -635,12 +532,6 @@ Int4Capacity int4_capacity(const Int4Call& c) {
 }
 
 template <typename F>
-cudaError_t with_elem(int elem, F&& go) {
-  if (elem == kElemF32) return go(std::integral_constant<int, kElemF32>{});
-  if (elem == kElemBf16) return go(std::integral_constant<int, kElemBf16>{});
-  return go(std::integral_constant<int, kElemF16>{});
-}
-template <typename F>
 cudaError_t with_group(int group, F&& go) {
   if (group == 32) return go(std::integral_constant<int, 32>{});
   if (group == 64) return go(std::integral_constant<int, 64>{});
@@ -648,30 +539,6 @@ cudaError_t with_group(int group, F&& go) {
 }
 
 }  // namespace
-
-cudaError_t launch_int4_quantize(const void* w, int w_elem, int64_t rows, int64_t cols, int group,
-                                 bool scale_bf16, uint8_t* codes, void* scale, uint8_t* zero,
-                                 cudaStream_t st) {
-  const int64_t runs = rows * cols / 8;
-  return with_elem(w_elem, [&](auto elem) {
-    return with_group(group, [&](auto g) {
-      return launch_next(zero ? int4_quantize_kernel<decltype(elem)::value, decltype(g)::value, true>
-                              : int4_quantize_kernel<decltype(elem)::value, decltype(g)::value, false>,
-                         (runs + 256 * kQuantUnroll - 1) / (256 * kQuantUnroll), 256, st, w, runs, scale_bf16,
-                         reinterpret_cast<uint32_t*>(codes), static_cast<uint16_t*>(scale), zero);
-    });
-  });
-}
-
-cudaError_t launch_int4_dequantize(const nf4_int4_weight& w, void* out, int out_elem, cudaStream_t st) {
-  const int64_t runs = w.rows * w.cols / 8;
-  return with_elem(out_elem, [&](auto elem) {
-    return launch_next(int4_dequantize_kernel<decltype(elem)::value>,
-                       (runs + 256 * kDequantUnroll - 1) / (256 * kDequantUnroll), 256, st,
-                       reinterpret_cast<const uint32_t*>(w.codes), static_cast<const uint16_t*>(w.scale), w.zero,
-                       runs, w.group == 32 ? 2 : w.group == 64 ? 3 : 4, w.scale_elem == kElemBf16, out);
-  });
-}
 
 cudaError_t launch_int4_matmul(const Int4Call& c) {
   const Int4Shape shape = plan_int4(c.M, c.w[0].rows, static_cast<int>((c.w[0].cols + kBoxCodes - 1) / kBoxCodes),
