@@ -13,7 +13,10 @@
 //  * One CTA of 16 warps an SM, persistent: the tokens' slice of the reduction is
 //    staged in shared memory once, then row tiles pass by. Of a tile, a warp has
 //    16 rows and one of 2^parts_log parts of the slice; a cluster of up to 8 CTAs
-//    splits the reduction where the rows are few or the tokens' slice is large.
+//    splits the reduction where the rows are few or the tokens' slice is large. A
+//    tile may have fewer rows than the warps could take, so that every SM has the
+//    same share (3584 x 18944 at 16 tokens, 14 tiles of 16 row groups on 18 clusters
+//    or 18 of 13).
 //  * A warp streams its own codes, boxes of 16 rows x 256 values, by asynchronous
 //    copies into two slots of its own: no warp waits for another. A box goes into
 //    registers whole (ldmatrix: word t of row g is lane (g, t)'s, which is the
@@ -54,7 +57,8 @@ struct Int4Args {
   int groups;                    // of a row
   int boxes;                     // of a row
   int tokens, m_tiles;           // of a tile; tiles
-  int parts_log, splits;
+  int parts_log, splits, splits_log;
+  int row_groups;                // 16 rows each, of a tile: row_groups * parts warps work
   int row_tiles, row_step;       // all; clusters that share a token tile
   int off_sums;                  // byte offset in shared memory
   bool scale_bf16, wide;
@@ -134,7 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int parts = 1 << p.parts_log, part = warp & (parts - 1);
-  const int rows_tile = 16 * (kWarps >> p.parts_log), row_warp = 16 * (warp >> p.parts_log);
+  const int rows_tile = 16 * p.row_groups, row_warp = 16 * (warp >> p.parts_log);
+  const bool works = row_warp < rows_tile;
   const int rank = static_cast<int>(blockIdx.x) % p.splits, cluster = static_cast<int>(blockIdx.x) / p.splits;
   const int64_t m0 = static_cast<int64_t>(cluster % p.m_tiles) * p.tokens;
   const int mt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.M - m0));
@@ -142,7 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   // this CTA's boxes of a row, and this warp's
   const int s0 = static_cast<int>(static_cast<int64_t>(p.boxes) * rank / p.splits);
   const int s1 = static_cast<int>(static_cast<int64_t>(p.boxes) * (rank + 1) / p.splits);
-  const int b0 = s0 + (s1 - s0) * part / parts, nb = s0 + (s1 - s0) * (part + 1) / parts - b0;
+  const int b0 = s0 + (s1 - s0) * part / parts;
+  const int nb = works ? s0 + (s1 - s0) * (part + 1) / parts - b0 : 0;
   const uint32_t ring = tc::smem_addr(smem) + warp * (2 * kMats * kBoxBytes);
   let_next_start();
   if (p.splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -262,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   }
   __syncthreads();
 
-  const int own = rows_tile / p.splits, own_log = 31 - __clz(own);
+  // of each 16 rows, CTA r of the cluster owns the run of 16 / splits from r 16 / splits
+  const int own = rows_tile >> p.splits_log, run_log = 4 - p.splits_log, run = 1 << run_log;
   const uint32_t inbox = tc::smem_addr(smem) + p.off_sums;
   // lanes 8 j .. 8 j + 7 give the rows of matrix j, chunk 4 c + j of a box's rows
   const uint32_t lm = (lane & 7) * 128 + 16 * ((lane >> 3) ^ (lane & 7));
@@ -359,10 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = 8 * nt + 2 * t + (e & 1), row = row_warp + g + 8 * (e >> 1);
-          if (tok >= mt) continue;
-          const uint32_t at = inbox + 4u * ((((rank * parts + part) * kMats + mat) * mt + tok) * own + (row & (own - 1)));
+          if (tok >= mt || !works) continue;
+          const int local = (row >> 4 << run_log) + (row & (run - 1));
+          const uint32_t at = inbox + 4u * ((((rank * parts + part) * kMats + mat) * mt + tok) * own + local);
           if (p.splits > 1)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, row >> own_log)), "f"(acc[mat][nt][e])
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, (row & 15) >> run_log)),
+                         "f"(acc[mat][nt][e])
                          : "memory");
           else
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(acc[mat][nt][e]) : "memory");
@@ -371,8 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
     else __syncthreads();
     const float* sums = reinterpret_cast<const float*>(smem + p.off_sums);
     for (int e = threadIdx.x; e < mt * own; e += kThreads) {
-      const int tok = e >> own_log, row = e & (own - 1);
-      const int64_t n = static_cast<int64_t>(tile) * rows_tile + rank * own + row;
+      const int tok = e / own, row = e - tok * own;
+      const int64_t n = static_cast<int64_t>(tile) * rows_tile + ((row >> run_log) << 4) + (rank << run_log) +
+                        (row & (run - 1));
       if (n >= p.N) continue;
       float y[kMats] = {};
 #pragma unroll 4
@@ -388,44 +398,49 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Launch shape of a call: tokens of a tile, parts of a slice, splits (the cluster)
-// and clusters for each token tile. Estimated time, in ns: a box a warp (32 KB an
-// SM and weight) takes 0.85 us, a tile 0.7 us more for its sums, 0.9 in a cluster;
-// staging 60 bytes a ns. (Every shape measured on 13 sizes of 1 to 32 tokens: the
-// one chosen is within 5% of the best.)
+// Launch shape of a call: tokens of a tile, parts of a slice, splits (the cluster),
+// row groups of a tile and clusters for each token tile. Estimated time, in us: a
+// box a warp takes 0.85 us and weight where all 16 warps work (1.6 above 8 tokens),
+// less where fewer do, as the SM's issue slots bound it, down to half; a tile 0.7 us
+// more for its sums, 0.9 in a cluster; staging 60 bytes a ns.
 struct Int4Shape {
-  int tokens, parts_log, splits;
-  int64_t row_tiles, row_step, m_tiles;
+  int tokens, parts_log, splits_log, row_groups;
+  int row_tiles, row_step, m_tiles;
 };
 
 Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)[4]) {
   Int4Shape best = {};
-  int64_t best_cost = INT64_MAX;
+  float best_cost = 3e38f;
+  const int groups = static_cast<int>((N + 15) / 16);
   for (int tokens = 16; tokens >= 1; tokens /= 2) {
     if (tokens > 1 && tokens / 2 >= M) continue;            // a smaller tile holds them all
     const int mt = M >= tokens || tokens == 16 ? tokens : static_cast<int>(M);   // two column tiles hold 16
     const int room = (kMostSmem - ring_bytes(mats) - sums_bytes(mats, mt)) / staged_bytes(mt);
-    for (int i = 0; i < 4 && (1 << i) <= boxes; ++i) {
-      const int s = 1 << i, slice = (boxes + s - 1) / s;
-      if (slice > room || ctas[i] < s) continue;
+    const int m_tiles = static_cast<int>((M + mt - 1) / mt);
+    const float box = (mt > 8 ? 1.6f : 0.85f) * static_cast<float>(mats);
+    for (int sl = 0; sl < 4 && (1 << sl) <= boxes; ++sl) {
+      const int slice = (boxes + (1 << sl) - 1) >> sl, clusters = ctas[sl] >> sl;
+      if (slice > room || clusters == 0) continue;
+      const int step = std::max(1, clusters / m_tiles);
+      const float fixed = static_cast<float>(slice) * static_cast<float>(staged_bytes(mt)) / 60000.0f + 2.5f;
       for (int pl = 0; pl <= 4; ++pl) {
-        const int64_t rows = 16 * (kWarps >> pl);
-        if (rows < s) continue;
-        Int4Shape sh = {mt, pl, s, (N + rows - 1) / rows, 0, (M + mt - 1) / mt};
-        const int64_t clusters = ctas[i] / s;
-        sh.row_step = std::min(sh.row_tiles, std::max<int64_t>(1, clusters / sh.m_tiles));
-        const int64_t waves = (sh.row_step * sh.m_tiles + clusters - 1) / clusters;
-        const int64_t passes = (sh.row_tiles + sh.row_step - 1) / sh.row_step;
-        const int64_t each = (slice + (1 << pl) - 1) >> pl;
-        const int64_t cost = waves * (passes * (each * 850 * mats + (s > 1 ? 900 : 700)) +
-                                      static_cast<int64_t>(slice) * staged_bytes(mt) / 60 + 2500);
+        // the passes that full tiles take, then the smallest tile that takes no more
+        const int full = kWarps >> pl, tiles = (groups + full - 1) / full, passes = (tiles + step - 1) / step;
+        const int spread = passes * step;
+        const int rg = groups <= spread ? 1 : (groups - 1) / spread + 1;
+        const int row_tiles = (groups + rg - 1) / rg, row_step = std::min(row_tiles, step);
+        const int64_t all = static_cast<int64_t>(row_step) * m_tiles;
+        const float waves = static_cast<float>((all + clusters - 1) / clusters);
+        const float busy = std::max(0.5f, static_cast<float>(rg << pl) / kWarps);
+        const float each = static_cast<float>((slice + (1 << pl) - 1) >> pl);
+        const float cost = waves * (static_cast<float>(passes) * (each * box * busy + (sl > 0 ? 0.9f : 0.7f)) + fixed);
         if (cost < best_cost) {
           best_cost = cost;
-          best = sh;
+          best = {mt, pl, sl, rg, row_tiles, row_step, m_tiles};
         }
       }
     }
-    if (best_cost < INT64_MAX) break;                       // fewer tokens read the weight more often
+    if (best_cost < 3e38f) break;                           // fewer tokens read the weight more often
   }
   return best;
 }
@@ -445,12 +460,14 @@ cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
   a.groups = static_cast<int>(a.K / kGroup);
   a.boxes = static_cast<int>((a.K + kBoxCodes - 1) / kBoxCodes);
   a.tokens = shape.tokens;
-  a.m_tiles = static_cast<int>(shape.m_tiles);
+  a.m_tiles = shape.m_tiles;
   a.parts_log = shape.parts_log;
-  a.splits = shape.splits;
-  a.row_tiles = static_cast<int>(shape.row_tiles);
-  a.row_step = static_cast<int>(shape.row_step);
-  const int slice = (a.boxes + shape.splits - 1) / shape.splits;
+  a.splits = 1 << shape.splits_log;
+  a.splits_log = shape.splits_log;
+  a.row_groups = shape.row_groups;
+  a.row_tiles = shape.row_tiles;
+  a.row_step = shape.row_step;
+  const int slice = (a.boxes + a.splits - 1) / a.splits;
   a.off_sums = ring_bytes(kMats) + slice * staged_bytes(shape.tokens);
   a.scale_bf16 = c.w[0].scale_elem == kElemBf16;
   // a lane's scales and zero points in one load each
@@ -468,7 +485,7 @@ cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
     cudaFuncSetAttribute(int4_matmul_kernel<kF16, kGroup, kMats, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          kMostSmem);
   });
-  const int64_t grid = shape.row_step * shape.m_tiles * shape.splits;
+  const int64_t grid = static_cast<int64_t>(shape.row_step) * shape.m_tiles * a.splits;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -479,7 +496,7 @@ cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(shape.splits);
+  attr[1].val.clusterDim.x = static_cast<unsigned>(a.splits);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -543,7 +560,7 @@ cudaError_t with_group(int group, F&& go) {
 cudaError_t launch_int4_matmul(const Int4Call& c) {
   const Int4Shape shape = plan_int4(c.M, c.w[0].rows, static_cast<int>((c.w[0].cols + kBoxCodes - 1) / kBoxCodes),
                                     c.gated ? 2 : 1, int4_capacity(c).ctas);
-  if (shape.splits == 0) return cudaErrorInvalidConfiguration;
+  if (shape.row_groups == 0) return cudaErrorInvalidConfiguration;
   return with_group(c.w[0].group, [&](auto g) {
     constexpr int kGroup = decltype(g)::value;
     auto go = [&](auto f16, auto mats) {
