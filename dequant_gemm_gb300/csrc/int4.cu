@@ -253,18 +253,32 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   copy_box(ring + kMats * kBoxBytes);
   advance();
 
-  // the slice's tokens, [run of 8 / 4][token][run % 4]
+  // The slice's tokens, [run of 8 / 4][token][run % 4], zeros past the ends: every
+  // warp a share of one token's runs, four loads in flight a lane.
   {
-    const int runs = (s1 - s0) * (kBoxCodes / 8);
-    for (int i = threadIdx.x; i < runs * p.tokens; i += kThreads) {
-      const int tok = i / runs, run = i - tok * runs;
-      const int64_t k = static_cast<int64_t>(s0) * kBoxCodes + 8 * run;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (k < p.K && tok < mt) v = __ldg(reinterpret_cast<const uint4*>(p.x + (m0 + tok) * p.K + k));
-      reinterpret_cast<uint4*>(smem + ring_bytes(kMats))[((run >> 2) * p.tokens + tok) * 4 + (run & 3)] =
-          make_uint4(__byte_perm(v.x, v.z, 0x7632), __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.y, v.w, 0x7632),
-                     __byte_perm(v.y, v.w, 0x5410));
-    }
+    const int runs = (s1 - s0) * (kBoxCodes / 8), tok = warp % p.tokens, shares = kWarps / p.tokens;
+    const int64_t k0 = static_cast<int64_t>(s0) * kBoxCodes;
+    const int valid = tok < mt ? static_cast<int>(min(static_cast<int64_t>(runs), (p.K - k0) / 8)) : 0;
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + (m0 + (tok < mt ? tok : 0)) * p.K + k0);
+    uint4* dst = reinterpret_cast<uint4*>(smem + ring_bytes(kMats)) + 4 * tok + (lane & 3);
+    if (warp / p.tokens < shares)
+      for (int r0 = warp / p.tokens * 32 + lane; r0 < runs; r0 += 4 * 32 * shares) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + i * 32 * shares;
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < valid) v[i] = __ldg(src + r);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + i * 32 * shares;
+          if (r < runs)
+            dst[(r >> 2) * p.tokens * 4] = make_uint4(
+                __byte_perm(v[i].x, v[i].z, 0x7632), __byte_perm(v[i].x, v[i].z, 0x5410),
+                __byte_perm(v[i].y, v[i].w, 0x7632), __byte_perm(v[i].y, v[i].w, 0x5410));
+        }
+      }
   }
   __syncthreads();
 
