@@ -568,7 +568,7 @@ fp8_pair_kernel(const __grid_constant__ PairMaps<kMode> maps, const __grid_const
         if (p.y_scale) {
           float a = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 64; ++j) a = max_nan(a, fabsf(acc[j]));   // columns past the end are 0
+          for (int j = 0; j < 64; j += 2) a = max_abs(a, acc[j], acc[j + 1]);   // columns past the end are 0
           // the other half of the block; slots by parity, since this warp may be a
           // tile ahead of the partner's read
           const uint32_t slot = base + kPairOffMax + (joined & 1) * kMaxBytes + 4 * lane;
@@ -974,7 +974,7 @@ fp8_rows_kernel(const __grid_constant__ RowsMaps<kMode> maps, const __grid_const
             make_uint2(pack2<kElemBf16>(u.x, u.y), pack2<kElemBf16>(u.z, u.w));
       }
       if (p.y_scale) {
-        float a = max_nan(max_nan(fabsf(y.x), fabsf(y.y)), max_nan(fabsf(y.z), fabsf(y.w)));   // 0 past the end
+        float a = max_abs(max_abs(0.0f, y.x, y.y), y.z, y.w);   // 0 past the end
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, k));
         const float s = fp8_scale(a), inv = fp8_inverse(s);

@@ -24,21 +24,32 @@ __device__ __forceinline__ void load_run(Run<kElem>& r, const void* p, int64_t i
   if constexpr (kElem == kElemF32) r.v[1] = __ldcs(q + 1);
 }
 template <int kElem>
-__device__ __forceinline__ void widen(const Run<kElem>& r, float (&v)[8]) {
+__device__ __forceinline__ void widen(const Run<kElem>& r, uint64_t (&v)[4]) {
   if constexpr (kElem == kElemF32) {
-    v[0] = __uint_as_float(r.v[0].x); v[1] = __uint_as_float(r.v[0].y);
-    v[2] = __uint_as_float(r.v[0].z); v[3] = __uint_as_float(r.v[0].w);
-    v[4] = __uint_as_float(r.v[1].x); v[5] = __uint_as_float(r.v[1].y);
-    v[6] = __uint_as_float(r.v[1].z); v[7] = __uint_as_float(r.v[1].w);
+    v[0] = pair_of(__uint_as_float(r.v[0].x), __uint_as_float(r.v[0].y));
+    v[1] = pair_of(__uint_as_float(r.v[0].z), __uint_as_float(r.v[0].w));
+    v[2] = pair_of(__uint_as_float(r.v[1].x), __uint_as_float(r.v[1].y));
+    v[3] = pair_of(__uint_as_float(r.v[1].z), __uint_as_float(r.v[1].w));
   } else {
     const uint32_t u[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = unpack2<kElem>(u[j]);
-      v[2 * j] = f.x;
-      v[2 * j + 1] = f.y;
+      v[j] = pair_of(f.x, f.y);
     }
   }
+}
+
+// 8 values times `inverse` as e4m3 codes.
+__device__ __forceinline__ uint2 codes_of(const uint64_t (&v)[4], float inverse) {
+  const uint64_t i2 = pair_of(inverse, inverse);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = both(mul2(v[j], i2));
+    w[j] = e4m3x2(f.x, f.y);
+  }
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
 template <int kElem, bool kCubic>
@@ -65,33 +76,40 @@ gated_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ g, const 
   }
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
-    float d[8], gv[8], uv[8];
+    uint64_t d[4], gv[4], uv[4];
     widen<kElem>(rd[i], d);
     widen<kElemBf16>(rg[i], gv);
     widen<kElemBf16>(ru[i], uv);
     float ag = 0.0f, au = 0.0f;
+    const uint64_t one = pair_of(1.0f, 1.0f), minus = pair_of(-1.0f, -1.0f);
+    const uint64_t k0 = pair_of(c.k0, c.k0), k1 = pair_of(c.k1, c.k1), c0 = pair_of(c.c0, c.c0);
+    const uint64_t c13 = pair_of(3.0f * c.c1, 3.0f * c.c1);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float g2 = kCubic ? fminf(gv[j] * gv[j], 1e30f) : 0.0f;    // p' stays finite where s (1 - s) is 0
-      const float s = sigma_of(gv[j] * (kCubic ? fmaf(c.k1, g2, c.k0) : c.k0)), f = gv[j] * s;
-      const float slope = fmaf(f * (1.0f - s), kCubic ? fmaf(3.0f * c.c1, g2, c.c0) : 1.0f, s);
-      uv[j] = d[j] * uv[j] * slope;
-      d[j] *= f;
-      ag = max_nan(ag, fabsf(uv[j]));
-      au = max_nan(au, fabsf(d[j]));
+    for (int j = 0; j < 4; ++j) {
+      uint64_t g2 = 0;
+      if (kCubic) {                       // p' stays finite where s (1 - s) is 0
+        const float2 q = both(mul2(gv[j], gv[j]));
+        g2 = pair_of(fminf(q.x, 1e30f), fminf(q.y, 1e30f));
+      }
+      const float2 t = both(mul2(gv[j], kCubic ? fma2(k1, g2, k0) : k0));
+      const uint64_t s = pair_of(sigma_of(t.x), sigma_of(t.y)), f = mul2(gv[j], s);
+      uint64_t slope = mul2(f, fma2(s, minus, one));
+      slope = kCubic ? fma2(slope, fma2(c13, g2, c0), s) : add2(slope, s);
+      uv[j] = mul2(mul2(d[j], uv[j]), slope);
+      d[j] = mul2(d[j], f);
+      const float2 x = both(uv[j]), y = both(d[j]);
+      ag = max_abs(ag, x.x, x.y);
+      au = max_abs(au, y.x, y.y);
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) {
       ag = max_nan(ag, __shfl_xor_sync(0xffffffffu, ag, o));
       au = max_nan(au, __shfl_xor_sync(0xffffffffu, au, o));
     }
-    const float sg = fp8_scale(ag), su = fp8_scale(au), ig = fp8_inverse(sg), iu = fp8_inverse(su);
+    const float sg = fp8_scale(ag), su = fp8_scale(au);
     if (at[i] >= 0) {
-      *reinterpret_cast<uint2*>(dg + at[i]) =
-          make_uint2(e4m3x4(uv[0] * ig, uv[1] * ig, uv[2] * ig, uv[3] * ig),
-                     e4m3x4(uv[4] * ig, uv[5] * ig, uv[6] * ig, uv[7] * ig));
-      *reinterpret_cast<uint2*>(du + at[i]) = make_uint2(e4m3x4(d[0] * iu, d[1] * iu, d[2] * iu, d[3] * iu),
-                                                         e4m3x4(d[4] * iu, d[5] * iu, d[6] * iu, d[7] * iu));
+      *reinterpret_cast<uint2*>(dg + at[i]) = codes_of(uv, fp8_inverse(sg));
+      *reinterpret_cast<uint2*>(du + at[i]) = codes_of(d, fp8_inverse(su));
     }
     if ((threadIdx.x & 15) == 0 && b0 + i < blocks) {
       dg_scale[b0 + i] = sg;

@@ -514,7 +514,7 @@ cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, int4_matmul_kernel<kF16, kGroup, kMats, kNT>, a);
 }
 

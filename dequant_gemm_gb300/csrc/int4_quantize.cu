@@ -22,28 +22,6 @@ namespace {
 constexpr int kQuantUnroll = 2;
 constexpr float kSmallScale = 5.421010862427522e-20f;     // 2^-64
 
-// Two fp32 operations at once, each rounded by itself.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 template <int kElem, int kGroup, bool kZero>
 __global__ void __launch_bounds__(256)
 int4_quantize_kernel(const void* __restrict__ w, int64_t runs, bool bf16, uint32_t* __restrict__ codes,
@@ -88,10 +66,10 @@ int4_quantize_kernel(const void* __restrict__ w, int64_t runs, bool bf16, uint32
     };
     if (s >= kSmallScale) {
       const float inverse = __frcp_rn(s);
-      const uint64_t r = pair(inverse, inverse), minus_s = pair(-s, -s), magic = pair(kMagic, kMagic);
+      const uint64_t r = pair_of(inverse, inverse), minus_s = pair_of(-s, -s), magic = pair_of(kMagic, kMagic);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        const uint64_t x = pair(v[i][j], v[i][j + 1]), q = mul2(x, r);
+        const uint64_t x = pair_of(v[i][j], v[i][j + 1]), q = mul2(x, r);
         const uint64_t m = add2(fma2(fma2(q, minus_s, x), r, q), magic);
         put(j, static_cast<uint32_t>(m));
         put(j + 1, static_cast<uint32_t>(m >> 32));
