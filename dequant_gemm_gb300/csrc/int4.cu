@@ -46,7 +46,10 @@ constexpr int kBoxCodes = 256;
 constexpr int kMostSmem = 227 * 1024;
 constexpr int ring_bytes(int mats) { return kWarps * 2 * kBoxBytes * mats; }
 constexpr int sums_bytes(int mats, int tokens) { return kWarps * 16 * 4 * mats * tokens; }
-constexpr int staged_bytes(int tokens) { return kBoxCodes * 2 * tokens; }            // a box's tokens
+// a box's values of a token, [word][lane], at a pitch that puts two neighbouring
+// tokens, which are read together, on different banks
+constexpr int kTokenBytes = kBoxCodes * 2 + 64;
+constexpr int staged_bytes(int tokens) { return kTokenBytes * tokens; }
 
 struct Int4Args {
   const uint16_t* x;             // [M, K]
@@ -160,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   // are numbers, which meet zero scales and tokens or are dropped with their rows.
   int next_tile = tile0, next_left = 0;        // boxes left in the tile
   int64_t code_at = 0, scale_at = 0;           // this lane's first byte and scale
-  int rows_left = 0, bytes_left = 0, groups_left = 0;
-  const int64_t pitch = p.K / 2;
+  int rows_left = 0, codes_left = 0;           // of this lane's rows; of the row from the box on
+  const uint32_t pitch = static_cast<uint32_t>(p.K / 2);
   // lanes t = 0, 1 load the scales of row g, 2, 3 those of row g + 8, half a box's each
   const int lane_group = kLoads * (t & 1);
   const uint32_t copy_to = (lane >> 3) * 128;
@@ -172,13 +175,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
     const int64_t row0 = static_cast<int64_t>(next_tile) * rows_tile + row_warp;
     code_at = (row0 + (lane >> 3)) * pitch + static_cast<int64_t>(b0) * 128 + 16 * (lane & 7);
     rows_left = static_cast<int>(min(p.N - row0, static_cast<int64_t>(16))) - (lane >> 3);
-    bytes_left = static_cast<int>(pitch) - b0 * 128 - 16 * (lane & 7);
-    groups_left = p.groups - b0 * kBoxGroups - lane_group;
+    codes_left = static_cast<int>(p.K) - b0 * kBoxCodes;
     scale_at = min(row0 + g + 8 * (t >> 1), p.N - 1) * p.groups + b0 * kBoxGroups + lane_group;
   };
   auto copy_box = [&](uint32_t slot) {         // (address of the slot)
     if (next_left > 0) {
-      const int rows = bytes_left > 0 ? rows_left : 0;
+      const int rows = codes_left > 32 * (lane & 7) ? rows_left : 0;
 #pragma unroll
       for (int mat = 0; mat < kMats; ++mat) {
         const uint8_t* src = p.codes[mat] + code_at;
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
       if (next_left <= 0) continue;
       const uint16_t* sp = p.scale[mat] + scale_at;
       const uint8_t* zp = p.zero[mat] + scale_at;
+      const int groups_left = codes_left / kGroup - lane_group;
       if (kLoads > 1 && p.wide) {              // kLoads divides the row's groups
         if (groups_left <= 0) continue;
         if constexpr (kLoads == 4) {
@@ -236,8 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   };
   auto advance = [&] {
     code_at += 128;
-    bytes_left -= 128;
-    groups_left -= kBoxGroups;
+    codes_left -= kBoxCodes;
     scale_at += kBoxGroups;
     if (--next_left == 0) {
       next_tile += p.row_step;
@@ -253,31 +255,22 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   copy_box(ring + kMats * kBoxBytes);
   advance();
 
-  // The slice's tokens, [run of 8 / 4][token][run % 4], zeros past the ends: every
-  // warp a share of one token's runs, four loads in flight a lane.
+  // The slice's tokens, [box][token][run of 8], zeros past the ends: every warp a
+  // share of one token's runs.
   {
     const int runs = (s1 - s0) * (kBoxCodes / 8), tok = warp % p.tokens, shares = kWarps / p.tokens;
     const int64_t k0 = static_cast<int64_t>(s0) * kBoxCodes;
     const int valid = tok < mt ? static_cast<int>(min(static_cast<int64_t>(runs), (p.K - k0) / 8)) : 0;
     const uint4* src = reinterpret_cast<const uint4*>(p.x + (m0 + (tok < mt ? tok : 0)) * p.K + k0);
-    uint4* dst = reinterpret_cast<uint4*>(smem + ring_bytes(kMats)) + 4 * tok + (lane & 3);
+    uint8_t* dst = smem + ring_bytes(kMats) + kTokenBytes * tok + 16 * lane;
     if (warp / p.tokens < shares)
-      for (int r0 = warp / p.tokens * 32 + lane; r0 < runs; r0 += 4 * 32 * shares) {
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + i * 32 * shares;
-          v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < valid) v[i] = __ldg(src + r);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + i * 32 * shares;
-          if (r < runs)
-            dst[(r >> 2) * p.tokens * 4] = make_uint4(
-                __byte_perm(v[i].x, v[i].z, 0x7632), __byte_perm(v[i].x, v[i].z, 0x5410),
-                __byte_perm(v[i].y, v[i].w, 0x7632), __byte_perm(v[i].y, v[i].w, 0x5410));
-        }
+#pragma unroll 4
+      for (int r = warp / p.tokens * 32 + lane; r < runs; r += 32 * shares) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < valid) v = __ldg(src + r);
+        *reinterpret_cast<uint4*>(dst + (r >> 5) * (kTokenBytes * p.tokens)) =
+            make_uint4(__byte_perm(v.x, v.z, 0x7632), __byte_perm(v.x, v.z, 0x5410),
+                       __byte_perm(v.y, v.w, 0x7632), __byte_perm(v.y, v.w, 0x5410));
       }
   }
   __syncthreads();
@@ -289,13 +282,15 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   const uint32_t lm = (lane & 7) * 128 + 16 * ((lane >> 3) ^ (lane & 7));
   // A lane whose column of the MMA has no token reads another's: the column's sums
   // are dropped.
-  const uint32_t x_lane = tc::smem_addr(smem) + ring_bytes(kMats) + 16 * (4 * (g % min(p.tokens, 8)) + t);
-  const uint32_t x_word = 64u * p.tokens;
+  const uint32_t x_box = kTokenBytes * p.tokens;
+  const uint32_t x_first = tc::smem_addr(smem) + ring_bytes(kMats) + kTokenBytes * (g % min(p.tokens, 8)) + 16 * t +
+                           (b0 - s0) * x_box;
   uint32_t slot = ring;
   for (int tile = tile0; tile < p.row_tiles; tile += p.row_step) {
     float acc[kMats][kNT][4] = {};
+    uint32_t xb = x_first;
 #pragma unroll 1
-    for (int b = 0; b < nb; ++b) {
+    for (int b = 0; b < nb; ++b, xb += x_box) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
       uint32_t q[kMats][2][2][4];              // [weight][chunk][row half][word]
@@ -321,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
       copy_box(slot);
       advance();
       slot = 2 * ring + kMats * kBoxBytes - slot;              // the other one
-      const uint32_t xb = x_lane + (b0 - s0 + b) * (8 * x_word);
 #pragma unroll
       for (int j = 0; j < kBoxGroups; ++j) {
         uint32_t za[kMats], zb[kMats];
@@ -343,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
           const int w = j * (8 / kBoxGroups) + i;              // of the box's 8 words a lane
           uint4 x[kNT];
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) x[nt] = lds_words(xb + w * x_word + 512 * nt);
+          for (int nt = 0; nt < kNT; ++nt) x[nt] = lds_words(xb + 64 * w + 8 * kTokenBytes * nt);
 #pragma unroll
           for (int mat = 0; mat < kMats; ++mat) {
             const uint32_t wa = q[mat][w >> 2][0][w & 3], wb = q[mat][w >> 2][1][w & 3];
