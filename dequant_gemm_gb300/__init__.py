@@ -114,9 +114,10 @@ def lib() -> ctypes.CDLL:
                 "nf4_rmsnorm_fwd": [vp, i32, vp, i32, vp, i32, i64, i64, f32, vp, vp, i32, vp, vp,
                                     vp],
                 "nf4_rmsnorm_bwd": [vp, vp, vp, i32, vp, i32, vp, i64, i64, vp, vp, vp, i64, vp],
-                "nf4_fp8_gated_fwd": [Q, Q, Q, i32, vp, i32, vp, vp, vp, vp],
+                # (addresses of nf4_fp8_tensor structs)
+                "nf4_fp8_gated_fwd": [vp, vp, vp, i32, vp, i32, vp, vp, vp, vp],
                 "nf4_fp8_gated_bwd": [vp, i32, vp, vp, i64, i64, i32, vp, vp, vp, vp, vp],
-                "nf4_fp8_gated_bwd_dx": [Q, Q, Q, Q, vp, i32, i32, vp],
+                "nf4_fp8_gated_bwd_dx": [vp, vp, vp, vp, vp, i32, i32, vp],
                 "nf4_int4_quantize": [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp],
                 "nf4_int4_dequantize": [I, vp, i32, vp],
                 "nf4_int4_matmul_fwd": [vp, i32, i64, I, vp, i32, i32, vp],
