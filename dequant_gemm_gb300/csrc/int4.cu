@@ -117,13 +117,17 @@ __device__ __forceinline__ void mma_16(float (&d)[4], const uint32_t (&a)[4], ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
+__device__ __forceinline__ uint32_t or_masked(uint32_t w, uint32_t mask, uint32_t one) {
+  uint32_t v;                                  // (w & mask) | one: written out, it takes two instructions
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w), "r"(mask), "r"(one));
+  return v;
+}
+
 // Codes 4 bits wide in bits 0-3 and 16-19 of w as two numbers less the zero
 // point's (zz: the same two numbers made of it).
 template <bool kF16>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zz) {
-  constexpr uint32_t kOne = kF16 ? 0x64006400u : 0x43004300u;     // 1024, 128
-  uint32_t v;                                  // (w & mask) | one: written out, it takes two instructions
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w), "n"(0x000f000f), "r"(kOne));
+  const uint32_t v = or_masked(w, 0x000f000fu, kF16 ? 0x64006400u : 0x43004300u);     // 1024, 128
   if constexpr (kF16) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&zz));
     return *reinterpret_cast<const uint32_t*>(&d);
@@ -132,6 +136,24 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t zz) {
         __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&zz));
     return *reinterpret_cast<const uint32_t*>(&d);
   }
+}
+
+// The same of bits 4-7 and 20-23 in fp16, whose mantissa has room for 1024 + 16 q:
+// one exact FMA with -(64 + z) makes q - z without a shift, for a constant more a
+// row and group. 8 tokens x 18944 x 3584 in groups of 128: 12.1 us for 12.8; 16 x
+// 3584 x 18944 in groups of 64: 19.7 for 20.1; two weights of 18944 x 3584 at one
+// token 18.9 for 20.1. Not in groups of 32 (two of 11008 x 4096 at 7 tokens: 22.5
+// for 21.8) and not with two weights and two token tiles, where registers run out
+// (two of 18944 x 3584 at 16: 32.0 for 31.5).
+__device__ __forceinline__ uint32_t minus_64_z(uint32_t zz) {      // of twice 1024 + z
+  const __half2 d = __hsub2(__float2half2_rn(960.0f), *reinterpret_cast<const __half2*>(&zz));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t high_pair(uint32_t w, uint32_t far) {
+  const uint32_t v = or_masked(w, 0x00f000f0u, 0x64006400u);
+  const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.0625f),
+                            *reinterpret_cast<const __half2*>(&far));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 template <bool kF16, int kGroup, int kMats, int kNT>
@@ -318,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
       slot = 2 * ring + kMats * kBoxBytes - slot;              // the other one
 #pragma unroll
       for (int j = 0; j < kBoxGroups; ++j) {
-        uint32_t za[kMats], zb[kMats];
+        constexpr bool kHigh = kF16 && kGroup > 32 && kMats * kNT < 4;
+        uint32_t za[kMats], zb[kMats], far_a[kMats], far_b[kMats];
         float sa[kMats], sb[kMats];
 #pragma unroll
         for (int mat = 0; mat < kMats; ++mat) {
@@ -328,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
           constexpr uint32_t kOne = kF16 ? 0x64u : 0x43u;
           za[mat] = __byte_perm(va, kOne, 0x4040);
           zb[mat] = __byte_perm(vb, kOne, 0x4040);
+          far_a[mat] = kHigh ? minus_64_z(za[mat]) : 0u;
+          far_b[mat] = kHigh ? minus_64_z(zb[mat]) : 0u;
           sa[mat] = __uint_as_float(va & 0xffffff00u);
           sb[mat] = __uint_as_float(vb & 0xffffff00u);
         }
@@ -344,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t a[4] = {code_pair<kF16>(wa >> (8 * h), za[mat]), code_pair<kF16>(wb >> (8 * h), zb[mat]),
-                                     code_pair<kF16>(wa >> (8 * h + 4), za[mat]),
-                                     code_pair<kF16>(wb >> (8 * h + 4), zb[mat])};
+                                     kHigh ? high_pair(wa >> (8 * h), far_a[mat])
+                                           : code_pair<kF16>(wa >> (8 * h + 4), za[mat]),
+                                     kHigh ? high_pair(wb >> (8 * h), far_b[mat])
+                                           : code_pair<kF16>(wb >> (8 * h + 4), zb[mat])};
 #pragma unroll
               for (int nt = 0; nt < kNT; ++nt)
                 mma_16<kF16>(sum[mat][nt], a, h ? x[nt].z : x[nt].x, h ? x[nt].w : x[nt].y, i + h > 0);
