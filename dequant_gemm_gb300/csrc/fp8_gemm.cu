@@ -1038,6 +1038,11 @@ struct LaunchAttrs {
 // us, start-up left out. Measured at 128 tokens a tile on the decoder shapes:
 // 0.46 us a block, 1.5 us a round for the last block and the reduction (up to 64
 // tokens a block takes 0.37 us, which the estimate does not tell apart).
+// The gated block's kernels: a block takes the longer of its own latency and its
+// share of HBM among the CTAs that run, and joining costs more the more CTAs share
+// a tile. Two weights of 11008 x 4096 at 64 tokens: 25.8, 31.7, 34.1, 54.9 us in 1,
+// 2, 4, 8 splits (estimated 22.6, 30.0, 29.5, 43.6 with 3 us to start); 4112 x 3600
+// at one token 15.8, 11.0, 9.8, 18.2 (15.9, 10.3, 10.0, 13.5).
 struct RowsPlan {
   int splits;
   int64_t cost;
@@ -1107,13 +1112,23 @@ template <int kMode, int kBT>
 RowsPlan plan_rows(const Operands& c, const MatmulArgs& a) {
   const RowsCapacity cap = rows_capacity<kMode, kBT>(c);
   const int64_t tiles = (a.cols + 127) / 128 * ((c.M + kBT - 1) / kBT);
-  constexpr int64_t kBlockCost = kMode == kGatedForward ? 80 : 46;
   RowsPlan best = {1, INT64_MAX};
   for (int i = 0; i < 4 && (1 << i) <= a.rb; ++i) {
     const int s = 1 << i;
     if (cap.ctas[i] < s) break;
     const int64_t rounds = (tiles * s + cap.ctas[i] - 1) / cap.ctas[i];
-    const int64_t cost = rounds * ((a.rb + s - 1) / s * kBlockCost + 150);
+    const int64_t blocks = (a.rb + s - 1) / s;
+    int64_t cost;
+    if constexpr (kMode >= kGatedForward) {
+      constexpr bool kBoth = kMode == kGatedForward;             // two weights a block
+      constexpr int64_t kLeast = kBoth ? (kBT <= 32 ? 43 : 60) : (kBT <= 32 ? 25 : kBT == 64 ? 31 : 48);
+      constexpr int64_t kFull = kBoth ? 78 : kBT == 128 ? 52 : 39;
+      constexpr int64_t kJoin[2][4] = {{40, 80, 160, 250}, {40, 100, 300, 400}};
+      const int64_t busy = std::min<int64_t>(tiles * s, cap.ctas[i]);
+      cost = rounds * (blocks * std::max(kLeast, kFull * busy / c.num_sms) + kJoin[kBT > 32][i]);
+    } else {
+      cost = rounds * (blocks * 46 + 150);
+    }
     if (cost < best.cost) best = {s, cost};
   }
   return best;
@@ -1192,6 +1207,7 @@ cudaError_t launch_any(const Operands& c, const MatmulArgs& a) {
   // forward's take 64 tokens at most
   constexpr int64_t kMostTiles = 65535;
   constexpr int kMostTokens = kMode == kGatedForward ? 64 : 128;
+  constexpr int64_t kPairBlock = kMode == kGatedForward ? 51 : kMode == kGatedInputGrad ? 44 : 39;
   if ((a.cols + 127) / 128 <= kMostTiles && (c.M + kMostTokens - 1) / kMostTokens <= kMostTiles) {
     if (c.M <= 16) return launch_rows<kMode, 16>(c, a);
     if (c.M <= 32) return launch_rows<kMode, 32>(c, a);
@@ -1200,10 +1216,14 @@ cudaError_t launch_any(const Operands& c, const MatmulArgs& a) {
     // more tokens: pairs, unless their tiles leave most SMs idle for a long
     // reduction, which the rows kernel splits (512 x 3584 forward at 250
     // tokens 16.2 us on pairs, 7.8 in rows; 4096 x 4096 at 512 tokens 18.8 and
-    // 20.4). Pairs: 0.39 us a block, 1 us a tile.
+    // 20.4). Pairs: 0.39 us a block, 1 us a tile; 0.44 a block of the
+    // gradient over two reductions (two of 4096 x 5504 at 256 tokens: 31.5 us on
+    // pairs, 38.3 in rows); 0.51 a block of two weights (two of
+    // 4112 x 3600 forward at 128 tokens: 19.0 us on pairs, 15.3 in rows; at 256 19.6
+    // and 23.0; two of 11008 x 4096 at 128 37.0 and 54.3).
     const int64_t units = (c.M + 255) / 256 * ((a.cols + pair_cols(kMode) - 1) / pair_cols(kMode));
     const int64_t rounds = (units + c.num_sms / 2 - 1) / std::max(1, c.num_sms / 2);
-    if (plan_rows<kMode, kMostTokens>(c, a).cost < rounds * (a.rb * 39 + 100))
+    if (plan_rows<kMode, kMostTokens>(c, a).cost < rounds * (a.rb * kPairBlock + 100))
       return launch_rows<kMode, kMostTokens>(c, a);
   }
   return launch_pair<kMode>(c, a);
