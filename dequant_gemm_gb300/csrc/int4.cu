@@ -435,9 +435,14 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
 
 // Launch shape of a call: tokens of a tile, parts of a slice, splits (the cluster),
 // row groups of a tile and clusters for each token tile. Estimated time, in us: a
-// box a warp takes 0.85 us and weight where all 16 warps work (1.6 above 8 tokens),
-// less where fewer do, as the SM's issue slots bound it, down to half; a tile 0.7 us
-// more for its sums, 0.9 in a cluster; staging 60 bytes a ns.
+// box a warp takes 1.1 us and weight where all 16 warps work (1.55 above 8 tokens),
+// less where fewer do, as the SM's issue slots bound it, down to 0.55 of it; a tile
+// 1.1 us more for its sums, 0.02 a token and weight, 0.2 to 0.6 in clusters of 2 to
+// 8; staging 45 bytes a ns. Fitted to every shape of 93 calls (1 to 32 tokens, 512 x
+// 3584 to 18944 x 3584, alone and gated), of which it takes one within 1% of the
+// fastest on average, 10% at worst: 4096 x 11008 at one token 10.1 us in rows of a
+// CTA (11.0 in clusters of 4), 6000 x 1024 at 8 tokens 4.0 (4.7), gated 11008 x
+// 4096 at 7 tokens 18.9 in clusters of 2 (19.9 in rows of a CTA).
 struct Int4Shape {
   int tokens, parts_log, splits_log, row_groups;
   int row_tiles, row_step, m_tiles;
@@ -452,12 +457,14 @@ Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)
     const int mt = M >= tokens || tokens == 16 ? tokens : static_cast<int>(M);   // two column tiles hold 16
     const int room = (kMostSmem - ring_bytes(mats) - sums_bytes(mats, mt)) / staged_bytes(mt);
     const int m_tiles = static_cast<int>((M + mt - 1) / mt);
-    const float box = (mt > 8 ? 1.6f : 0.85f) * static_cast<float>(mats);
+    const float box = (mt > 8 ? 1.55f : 1.1f) * static_cast<float>(mats);
     for (int sl = 0; sl < 4 && (1 << sl) <= boxes; ++sl) {
       const int slice = (boxes + (1 << sl) - 1) >> sl, clusters = ctas[sl] >> sl;
       if (slice > room || clusters == 0) continue;
       const int step = std::max(1, clusters / m_tiles);
-      const float fixed = static_cast<float>(slice) * static_cast<float>(staged_bytes(mt)) / 60000.0f + 2.5f;
+      const float staged = static_cast<float>(slice) * static_cast<float>(staged_bytes(mt));
+      const float fixed = staged / 45000.0f + (sl > 0 ? 1.9f : 1.5f);
+      const float sums = 1.1f + 0.02f * static_cast<float>(mt * mats) + 0.2f * static_cast<float>(sl);
       for (int pl = 0; pl <= 4; ++pl) {
         // the passes that full tiles take, then the smallest tile that takes no more
         const int full = kWarps >> pl, tiles = (groups + full - 1) / full, passes = (tiles + step - 1) / step;
@@ -466,9 +473,9 @@ Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)
         const int row_tiles = (groups + rg - 1) / rg, row_step = std::min(row_tiles, step);
         const int64_t all = static_cast<int64_t>(row_step) * m_tiles;
         const float waves = static_cast<float>((all + clusters - 1) / clusters);
-        const float busy = std::max(0.5f, static_cast<float>(rg << pl) / kWarps);
+        const float busy = std::max(0.55f, static_cast<float>(rg << pl) / kWarps);
         const float each = static_cast<float>((slice + (1 << pl) - 1) >> pl);
-        const float cost = waves * (static_cast<float>(passes) * (each * box * busy + (sl > 0 ? 0.9f : 0.7f)) + fixed);
+        const float cost = waves * (static_cast<float>(passes) * (each * box * busy + sums) + fixed);
         if (cost < best_cost) {
           best_cost = cost;
           best = {mt, pl, sl, rg, row_tiles, row_step, m_tiles};
