@@ -3,8 +3,16 @@
 // Y[m, n] = sum over groups of s[n, j] sum_{k in j} (q[n, k] - z[n, j]) x[m, k],
 // alone or (kMats = 2) for two weights whose sums meet as act(G) U.
 //
-// The weight's bytes bound it: half a byte a weight, read once for every 16
-// tokens. The weight's rows are the 16 rows of mma.sync.m16n8k16, the tokens
+// The weight's bytes are its floor: half a byte a weight, read once for every 16
+// tokens. What it takes is issue slots: a box of 16 x 256 codes costs a warp ~360
+// instructions (16 tokens 540), half of them to make operands of codes. Measured
+// (CUDA graph, bf16, groups of 128): one token, 4096 x 4096 5.6 us, 18944 x 3584 11.2
+// us (3.2 TB/s), two of them 19.7 (3.6 TB/s); 16 tokens 15.7 and 31.4. The legacy
+// mma.sync takes its operands from registers, where the codes are widened; for
+// tcgen05 they would go through shared or tensor memory first, and the tensor pipe
+// is 15% busy.
+//
+// The weight's rows are the 16 rows of mma.sync.m16n8k16, the tokens
 // its 8 columns (one or two tiles). Nothing is rounded on the way: a code
 // becomes the number 128 + q (bf16) or 1024 + q (fp16) by putting its four bits
 // into the mantissa, the same number with the zero point is subtracted, and
