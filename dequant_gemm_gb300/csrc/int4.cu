@@ -68,6 +68,7 @@ struct Int4Args {
   int groups;                    // of a row
   int boxes;                     // of a row
   int tokens, m_tiles;           // of a tile; tiles
+  int shares, per_share;         // warps that stage a token; 256 / shares, rounded up
   int parts_log, splits, splits_log;
   int row_groups;                // 16 rows each, of a tile: row_groups * parts warps work
   int row_tiles, row_step;       // all; clusters that share a token tile
@@ -164,6 +165,20 @@ __device__ __forceinline__ uint32_t high_pair(uint32_t w, uint32_t far) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
+// Sums to the shared memory of the cluster's CTA `owner` (of one: its own), at the
+// address that they have in this one's.
+__device__ __forceinline__ void store1(uint32_t at, uint32_t owner, bool cluster, float v) {
+  if (cluster) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, owner)), "f"(v) : "memory");
+  else asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void store4(uint32_t at, uint32_t owner, bool cluster, float a, float b, float c, float d) {
+  if (cluster)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(tc::mapa(at, owner)), "f"(a), "f"(b),
+                 "f"(c), "f"(d)
+                 : "memory");
+  else asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
 template <bool kF16, int kGroup, int kMats, int kNT>
 __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_constant__ Int4Args p) {
   constexpr int kBoxGroups = kBoxCodes / kGroup;               // 2, 4 or 8
@@ -173,15 +188,14 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   const int parts = 1 << p.parts_log, part = warp & (parts - 1);
   const int rows_tile = 16 * p.row_groups, row_warp = 16 * (warp >> p.parts_log);
   const bool works = row_warp < rows_tile;
-  const int rank = static_cast<int>(blockIdx.x) % p.splits, cluster = static_cast<int>(blockIdx.x) / p.splits;
+  const int rank = static_cast<int>(blockIdx.x) & (p.splits - 1), cluster = static_cast<int>(blockIdx.x) >> p.splits_log;
   const int64_t m0 = static_cast<int64_t>(cluster % p.m_tiles) * p.tokens;
   const int mt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.M - m0));
   const int tile0 = cluster / p.m_tiles;
   // this CTA's boxes of a row, and this warp's
-  const int s0 = static_cast<int>(static_cast<int64_t>(p.boxes) * rank / p.splits);
-  const int s1 = static_cast<int>(static_cast<int64_t>(p.boxes) * (rank + 1) / p.splits);
-  const int b0 = s0 + (s1 - s0) * part / parts;
-  const int nb = works ? s0 + (s1 - s0) * (part + 1) / parts - b0 : 0;
+  const int s0 = p.boxes * rank >> p.splits_log, s1 = p.boxes * (rank + 1) >> p.splits_log;
+  const int b0 = s0 + ((s1 - s0) * part >> p.parts_log);
+  const int nb = works ? s0 + ((s1 - s0) * (part + 1) >> p.parts_log) - b0 : 0;
   const uint32_t ring = tc::smem_addr(smem) + warp * (2 * kMats * kBoxBytes);
   let_next_start();
   if (p.splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -276,33 +290,50 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
       start_tile();
     }
   };
-  start_tile();
-  Scales now, later;
-  load_scales(now);
-  copy_box(ring);
-  advance();
-  load_scales(later);
-  copy_box(ring + kMats * kBoxBytes);
-  advance();
-
   // The slice's tokens, [box][token][run of 8], zeros past the ends: every warp a
-  // share of one token's runs.
+  // share of one token's runs. The first box's codes are asked for before them, or
+  // after the first of 16 tokens' loads, and the second's once they are here: asked
+  // for at once, all SMs' boxes delay the tokens and each other (two of 18944 x 3584
+  // at one token 19.3 us for 18.5, 3584 x 18944 at 16 19.5 for 18.7).
+  constexpr int kFirst = kNT == 2 ? 4 : 0;
+  Scales now, later;
+  auto first_box = [&] {
+    start_tile();
+    load_scales(now);
+    copy_box(ring);
+    advance();
+  };
+  if (kFirst == 0) first_box();
   {
-    const int runs = (s1 - s0) * (kBoxCodes / 8), tok = warp % p.tokens, shares = kWarps / p.tokens;
+    // warp = share + shares tok
+    const int tok = kNT == 2 ? warp : warp * p.per_share >> 8, shares = kNT == 2 ? 1 : p.shares;
+    const int share = tok < p.tokens ? warp - tok * shares : shares;
+    const int runs = (s1 - s0) * (kBoxCodes / 8);
     const int64_t k0 = static_cast<int64_t>(s0) * kBoxCodes;
     const int valid = tok < mt ? static_cast<int>(min(static_cast<int64_t>(runs), (p.K - k0) / 8)) : 0;
     const uint4* src = reinterpret_cast<const uint4*>(p.x + (m0 + (tok < mt ? tok : 0)) * p.K + k0);
     uint8_t* dst = smem + ring_bytes(kMats) + kTokenBytes * tok + 16 * lane;
-    if (warp / p.tokens < shares)
+    const int step = 32 * shares;
+    auto load = [&](int r) { return r < valid ? __ldg(src + r) : make_uint4(0u, 0u, 0u, 0u); };
+    auto stage = [&](int r, const uint4& v) {
+      *reinterpret_cast<uint4*>(dst + (r >> 5) * (kTokenBytes * p.tokens)) =
+          make_uint4(__byte_perm(v.x, v.z, 0x7632), __byte_perm(v.x, v.z, 0x5410),
+                     __byte_perm(v.y, v.w, 0x7632), __byte_perm(v.y, v.w, 0x5410));
+    };
+    int r = share < shares ? share * 32 + lane : runs;
+    uint4 first[kFirst + 1];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) first[i] = load(r + i * step);
+    if (kFirst > 0) first_box();
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i, r += step)
+      if (r < runs) stage(r, first[i]);
 #pragma unroll 4
-      for (int r = warp / p.tokens * 32 + lane; r < runs; r += 32 * shares) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < valid) v = __ldg(src + r);
-        *reinterpret_cast<uint4*>(dst + (r >> 5) * (kTokenBytes * p.tokens)) =
-            make_uint4(__byte_perm(v.x, v.z, 0x7632), __byte_perm(v.x, v.z, 0x5410),
-                       __byte_perm(v.y, v.w, 0x7632), __byte_perm(v.y, v.w, 0x5410));
-      }
+    for (; r < runs; r += step) stage(r, load(r));
   }
+  load_scales(later);
+  copy_box(ring + kMats * kBoxBytes);
+  advance();
   __syncthreads();
 
   // of each 16 rows, CTA r of the cluster owns the run of 16 / splits from r 16 / splits
@@ -313,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   // A lane whose column of the MMA has no token reads another's: the column's sums
   // are dropped.
   const uint32_t x_box = kTokenBytes * p.tokens;
-  const uint32_t x_first = tc::smem_addr(smem) + ring_bytes(kMats) + kTokenBytes * (g % min(p.tokens, 8)) + 16 * t +
+  const uint32_t x_first = tc::smem_addr(smem) + ring_bytes(kMats) + kTokenBytes * (g < p.tokens ? g : 0) + 16 * t +
                            (b0 - s0) * x_box;
   uint32_t slot = ring;
   for (int tile = tile0; tile < p.row_tiles; tile += p.row_step) {
@@ -397,47 +428,71 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
       }
     }
 
-    // every warp's sums to the CTA that owns the rows: [split, part][weight][token][row].
+    // every warp's sums to the CTA that owns the rows: [split, part][weight][token][row],
+    // or with 16 tokens [split, part][weight][row][token], where a lane's four of a row
+    // (tokens 2 t, 2 t + 1, 8 more) are one store and one load, swizzled so that eight
+    // rows' are on different banks (sum by sum, two of 18944 x 3584 at 16 tokens took
+    // 29.2 us for 23.8).
     // The first wait: every CTA runs, and has read its last tile's sums. (A CTA by
     // itself uses its own barrier: with cluster barriers a tile took 2 us more.)
     if (p.splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     else if (tile != tile0) __syncthreads();
+    const int from = (rank * parts + part) * kMats;
 #pragma unroll
     for (int mat = 0; mat < kMats; ++mat)
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = 8 * nt + 2 * t + (e & 1), row = row_warp + g + 8 * (e >> 1);
-          if (tok >= mt || !works) continue;
-          const int local = (row >> 4 << run_log) + (row & (run - 1));
-          const uint32_t at = inbox + 4u * ((((rank * parts + part) * kMats + mat) * mt + tok) * own + local);
-          if (p.splits > 1)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, (row & 15) >> run_log)),
-                         "f"(acc[mat][nt][e])
-                         : "memory");
-          else
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(acc[mat][nt][e]) : "memory");
+      for (int e = 0; e < 4; ++e) {
+        const int row = row_warp + g + 8 * (e >> 1), local = (row >> 4 << run_log) + (row & (run - 1));
+        const uint32_t owner = (row & 15) >> run_log;
+        if (!works) continue;
+        if constexpr (kNT == 2) {
+          if (e & 1) continue;
+          const uint32_t at = inbox + 16u * (((from + mat) * own + local) * 4 + (t ^ (local >> 1 & 3)));
+          const float *lo = acc[mat][0] + e, *hi = acc[mat][kNT - 1] + e;
+          store4(at, owner, p.splits > 1, lo[0], lo[1], hi[0], hi[1]);
+        } else {
+          const int tok = 2 * t + (e & 1);
+          if (tok < mt) store1(inbox + 4u * (((from + mat) * mt + tok) * own + local), owner, p.splits > 1, acc[mat][0][e]);
         }
+      }
     if (p.splits > 1) tc::cluster_sync();
     else __syncthreads();
     const float* sums = reinterpret_cast<const float*>(smem + p.off_sums);
-    for (int e = threadIdx.x; e < mt * own; e += kThreads) {
-      const int tok = e / own, row = e - tok * own;
+    constexpr int kEach = kNT == 2 ? 4 : 1;    // tokens a thread adds up at once
+    const int items = kNT == 2 ? 4 * own : mt * own;
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+      const int col = kNT == 2 ? (i >= own) + (i >= 2 * own) + (i >= 3 * own) : mt == 1 ? 0 : i / own;
+      const int row = i - col * own;
       const int64_t n = static_cast<int64_t>(tile) * rows_tile + ((row >> run_log) << 4) + (rank << run_log) +
                         (row & (run - 1));
       if (n >= p.N) continue;
-      float y[kMats] = {};
+      float y[kMats][kEach] = {};
 #pragma unroll 4
       for (int k = 0; k < p.splits * parts; ++k)
 #pragma unroll
-        for (int mat = 0; mat < kMats; ++mat) y[mat] += sums[((k * kMats + mat) * mt + tok) * own + row];
-      const float v = kMats == 2 ? gated(y[0], y[kMats - 1], p.curve) : y[0];
-      store_sum(p.y, p.y_elem, (m0 + tok) * p.N + n, v, p.accumulate);
+        for (int mat = 0; mat < kMats; ++mat) {
+          if constexpr (kNT == 2) {
+            const float4 v =
+                reinterpret_cast<const float4*>(sums)[((k * kMats + mat) * own + row) * 4 + (col ^ (row >> 1 & 3))];
+            y[mat][0] += v.x;
+            y[mat][1] += v.y;
+            y[mat][2] += v.z;
+            y[mat][3] += v.w;
+          } else {
+            y[mat][0] += sums[((k * kMats + mat) * mt + col) * own + row];
+          }
+        }
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int tok = kNT == 2 ? 2 * col + (e & 1) + 8 * (e >> 1) : col;
+        if (tok >= mt) continue;
+        const float v = kMats == 2 ? gated(y[0][e], y[kMats - 1][e], p.curve) : y[0][e];
+        store_sum(p.y, p.y_elem, (m0 + tok) * p.N + n, v, p.accumulate);
+      }
     }
-    if (p.splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (p.splits > 1 && tile + p.row_step < p.row_tiles)
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
-  if (p.splits > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // the last tile's arrivals
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
@@ -511,6 +566,8 @@ cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
   a.boxes = static_cast<int>((a.K + kBoxCodes - 1) / kBoxCodes);
   a.tokens = shape.tokens;
   a.m_tiles = shape.m_tiles;
+  a.shares = kWarps / shape.tokens;
+  a.per_share = (256 + a.shares - 1) / a.shares;
   a.parts_log = shape.parts_log;
   a.splits = 1 << shape.splits_log;
   a.splits_log = shape.splits_log;
