@@ -20,7 +20,7 @@
 // in fp32 and added to the row's.
 //  * One CTA of 16 warps an SM, persistent: the tokens' slice of the reduction is
 //    staged in shared memory once, then row tiles pass by. Of a tile, a warp has
-//    16 rows and one of 2^parts_log parts of the slice; a cluster of up to 8 CTAs
+//    16 rows and one of up to 16 parts of the slice; a cluster of up to 8 CTAs
 //    splits the reduction where the rows are few or the tokens' slice is large. A
 //    tile may have fewer rows than the warps could take, so that every SM has the
 //    same share (3584 x 18944 at 16 tokens, 14 tiles of 16 row groups on 18 clusters
@@ -68,8 +68,9 @@ struct Int4Args {
   int groups;                    // of a row
   int boxes;                     // of a row
   int tokens, m_tiles;           // of a tile; tiles
-  int shares, per_share;         // warps that stage a token; 256 / shares, rounded up
-  int parts_log, splits, splits_log;
+  int shares, per_share;         // warps that stage a token; 2^16 / shares, rounded up
+  int parts, per_part;           // likewise
+  int splits, splits_log;
   int row_groups;                // 16 rows each, of a tile: row_groups * parts warps work
   int row_tiles, row_step;       // all; clusters that share a token tile
   int off_sums;                  // byte offset in shared memory
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   constexpr int kLoads = kBoxGroups / 2;                       // scales a lane loads of a box
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int parts = 1 << p.parts_log, part = warp & (parts - 1);
-  const int rows_tile = 16 * p.row_groups, row_warp = 16 * (warp >> p.parts_log);
+  const int parts = p.parts, row_group = warp * p.per_part >> 16, part = warp - row_group * parts;
+  const int rows_tile = 16 * p.row_groups, row_warp = 16 * row_group;
   const bool works = row_warp < rows_tile;
   const int rank = static_cast<int>(blockIdx.x) & (p.splits - 1), cluster = static_cast<int>(blockIdx.x) >> p.splits_log;
   const int64_t m0 = static_cast<int64_t>(cluster % p.m_tiles) * p.tokens;
@@ -194,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   const int tile0 = cluster / p.m_tiles;
   // this CTA's boxes of a row, and this warp's
   const int s0 = p.boxes * rank >> p.splits_log, s1 = p.boxes * (rank + 1) >> p.splits_log;
-  const int b0 = s0 + ((s1 - s0) * part >> p.parts_log);
-  const int nb = works ? s0 + ((s1 - s0) * (part + 1) >> p.parts_log) - b0 : 0;
+  const int b0 = s0 + ((s1 - s0) * part * p.per_part >> 16);
+  const int nb = works ? s0 + ((s1 - s0) * (part + 1) * p.per_part >> 16) - b0 : 0;
   const uint32_t ring = tc::smem_addr(smem) + warp * (2 * kMats * kBoxBytes);
   let_next_start();
   if (p.splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   if (kFirst == 0) first_box();
   {
     // warp = share + shares tok
-    const int tok = kNT == 2 ? warp : warp * p.per_share >> 8, shares = kNT == 2 ? 1 : p.shares;
+    const int tok = kNT == 2 ? warp : warp * p.per_share >> 16, shares = kNT == 2 ? 1 : p.shares;
     const int share = tok < p.tokens ? warp - tok * shares : shares;
     const int runs = (s1 - s0) * (kBoxCodes / 8);
     const int64_t k0 = static_cast<int64_t>(s0) * kBoxCodes;
@@ -498,16 +499,16 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
 
 // Launch shape of a call: tokens of a tile, parts of a slice, splits (the cluster),
 // row groups of a tile and clusters for each token tile. Estimated time, in us: a
-// box a warp takes 1.1 us and weight where all 16 warps work (1.55 above 8 tokens),
-// less where fewer do, as the SM's issue slots bound it, down to 0.55 of it; a tile
-// 1.1 us more for its sums, 0.02 a token and weight, 0.2 to 0.6 in clusters of 2 to
-// 8; staging 45 bytes a ns. Fitted to every shape of 93 calls (1 to 32 tokens, 512 x
-// 3584 to 18944 x 3584, alone and gated), of which it takes one within 1% of the
-// fastest on average, 10% at worst: 4096 x 11008 at one token 10.1 us in rows of a
-// CTA (11.0 in clusters of 4), 6000 x 1024 at 8 tokens 4.0 (4.7), gated 11008 x
-// 4096 at 7 tokens 18.9 in clusters of 2 (19.9 in rows of a CTA).
+// box a warp takes 1.15 us and weight where all 16 warps work (1.2 above 8 tokens),
+// less where fewer do, as the issue slots of the SM's four schedulers bound it, down
+// to 0.55 of it; a tile 1 us more for its sums, 0.015 a token and weight, 0.01 a part,
+// 0.05 to 0.15 in clusters of 2 to 8; staging 65 bytes a ns. Fitted to every shape of
+// 109 calls (1 to 32 tokens, 512 x 3584 to 18944 x 3584, alone and gated), of which
+// it takes one within 1.2% of the fastest on average, 11% at worst: 11008 x 4096 at
+// one token 8.6 us in three parts (9.3 in two), 4096 x 11008 9.1 in rows of a CTA (9.4
+// in clusters of 2), 3584 x 18944 at 16 tokens 16.2 in clusters of 8 (20 of 4).
 struct Int4Shape {
-  int tokens, parts_log, splits_log, row_groups;
+  int tokens, parts, splits_log, row_groups;
   int row_tiles, row_step, m_tiles;
 };
 
@@ -520,28 +521,28 @@ Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)
     const int mt = M >= tokens || tokens == 16 ? tokens : static_cast<int>(M);   // two column tiles hold 16
     const int room = (kMostSmem - ring_bytes(mats) - sums_bytes(mats, mt)) / staged_bytes(mt);
     const int m_tiles = static_cast<int>((M + mt - 1) / mt);
-    const float box = (mt > 8 ? 1.55f : 1.1f) * static_cast<float>(mats);
+    const float box = (mt > 8 ? 1.2f : 1.15f) * static_cast<float>(mats);
     for (int sl = 0; sl < 4 && (1 << sl) <= boxes; ++sl) {
       const int slice = (boxes + (1 << sl) - 1) >> sl, clusters = ctas[sl] >> sl;
       if (slice > room || clusters == 0) continue;
       const int step = std::max(1, clusters / m_tiles);
       const float staged = static_cast<float>(slice) * static_cast<float>(staged_bytes(mt));
-      const float fixed = staged / 45000.0f + (sl > 0 ? 1.9f : 1.5f);
-      const float sums = 1.1f + 0.02f * static_cast<float>(mt * mats) + 0.2f * static_cast<float>(sl);
-      for (int pl = 0; pl <= 4; ++pl) {
+      const float fixed = staged / 65000.0f + (sl > 0 ? 1.3f : 0.9f);
+      const float sums = 1.0f + 0.015f * static_cast<float>(mt * mats) + 0.05f * static_cast<float>(sl);
+      for (const int parts : {1, 2, 3, 4, 5, 8, 16}) {
         // the passes that full tiles take, then the smallest tile that takes no more
-        const int full = kWarps >> pl, tiles = (groups + full - 1) / full, passes = (tiles + step - 1) / step;
+        const int full = kWarps / parts, tiles = (groups + full - 1) / full, passes = (tiles + step - 1) / step;
         const int spread = passes * step;
         const int rg = groups <= spread ? 1 : (groups - 1) / spread + 1;
         const int row_tiles = (groups + rg - 1) / rg, row_step = std::min(row_tiles, step);
         const int64_t all = static_cast<int64_t>(row_step) * m_tiles;
         const float waves = static_cast<float>((all + clusters - 1) / clusters);
-        const float busy = std::max(0.55f, static_cast<float>(rg << pl) / kWarps);
-        const float each = static_cast<float>((slice + (1 << pl) - 1) >> pl);
-        const float cost = waves * (static_cast<float>(passes) * (each * box * busy + sums) + fixed);
+        const float busy = std::max(0.55f, static_cast<float>((rg * parts + 3) / 4) / 4.0f);   // a scheduler has each fourth
+        const float each = std::max(1.0f, static_cast<float>(slice) / static_cast<float>(parts));
+        const float cost = waves * (static_cast<float>(passes) * (each * box * busy + sums + 0.01f * static_cast<float>(parts << sl)) + fixed);
         if (cost < best_cost) {
           best_cost = cost;
-          best = {mt, pl, sl, rg, row_tiles, row_step, m_tiles};
+          best = {mt, parts, sl, rg, row_tiles, row_step, m_tiles};
         }
       }
     }
@@ -567,8 +568,9 @@ cudaError_t launch_int4_as(const Int4Call& c, const Int4Shape& shape) {
   a.tokens = shape.tokens;
   a.m_tiles = shape.m_tiles;
   a.shares = kWarps / shape.tokens;
-  a.per_share = (256 + a.shares - 1) / a.shares;
-  a.parts_log = shape.parts_log;
+  a.per_share = (65536 + a.shares - 1) / a.shares;
+  a.parts = shape.parts;
+  a.per_part = (65536 + a.parts - 1) / a.parts;
   a.splits = 1 << shape.splits_log;
   a.splits_log = shape.splits_log;
   a.row_groups = shape.row_groups;
