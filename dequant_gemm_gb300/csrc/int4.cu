@@ -5,12 +5,13 @@
 //
 // The weight's bytes are its floor: half a byte a weight, read once for every 16
 // tokens. What it takes is issue slots: a box of 16 x 256 codes costs a warp ~360
-// instructions (16 tokens 540), half of them to make operands of codes. Measured
-// (CUDA graph, bf16, groups of 128): one token, 4096 x 4096 5.6 us, 18944 x 3584 11.2
-// us (3.2 TB/s), two of them 19.7 (3.6 TB/s); 16 tokens 15.7 and 31.4. The legacy
-// mma.sync takes its operands from registers, where the codes are widened; for
-// tcgen05 they would go through shared or tensor memory first, and the tensor pipe
-// is 15% busy.
+// instructions (16 tokens 540), half of them to make operands of codes, and the
+// SM's four schedulers issue them at 85% of their rate while boxes go by; the first
+// box is there 3 us after the launch. Measured (CUDA graph, bf16, groups of 128): one
+// token, 4096 x 4096 5.1 us, 18944 x 3584 10.4 us (3.5 TB/s), two of them 18.2 (3.9
+// TB/s); 16 tokens 12.9 and 24.1. The legacy mma.sync takes its operands from
+// registers, where the codes are widened; for tcgen05 they would go through shared
+// or tensor memory first, and the tensor pipe is 15% busy.
 //
 // The weight's rows are the 16 rows of mma.sync.m16n8k16, the tokens
 // its 8 columns (one or two tiles). Nothing is rounded on the way: a code
@@ -23,8 +24,8 @@
 //    16 rows and one of up to 16 parts of the slice; a cluster of up to 8 CTAs
 //    splits the reduction where the rows are few or the tokens' slice is large. A
 //    tile may have fewer rows than the warps could take, so that every SM has the
-//    same share (3584 x 18944 at 16 tokens, 14 tiles of 16 row groups on 18 clusters
-//    or 18 of 13).
+//    same share (3584 x 18944 at 16 tokens, 14 tiles of 16 row groups or, on 15
+//    clusters, 15 of 15).
 //  * A warp streams its own codes, boxes of 16 rows x 256 values, by asynchronous
 //    copies into two slots of its own: no warp waits for another. A box goes into
 //    registers whole (ldmatrix: word t of row g is lane (g, t)'s, which is the
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
   const int parts = p.parts, row_group = warp * p.per_part >> 16, part = warp - row_group * parts;
   const int rows_tile = 16 * p.row_groups, row_warp = 16 * row_group;
   const bool works = row_warp < rows_tile;
-  const int rank = static_cast<int>(blockIdx.x) & (p.splits - 1), cluster = static_cast<int>(blockIdx.x) >> p.splits_log;
+  const int cta = static_cast<int>(blockIdx.x), rank = cta & (p.splits - 1), cluster = cta >> p.splits_log;
   const int64_t m0 = static_cast<int64_t>(cluster % p.m_tiles) * p.tokens;
   const int mt = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.M - m0));
   const int tile0 = cluster / p.m_tiles;
@@ -453,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
           store4(at, owner, p.splits > 1, lo[0], lo[1], hi[0], hi[1]);
         } else {
           const int tok = 2 * t + (e & 1);
-          if (tok < mt) store1(inbox + 4u * (((from + mat) * mt + tok) * own + local), owner, p.splits > 1, acc[mat][0][e]);
+          if (tok >= mt) continue;
+          store1(inbox + 4u * (((from + mat) * mt + tok) * own + local), owner, p.splits > 1, acc[mat][0][e]);
         }
       }
     if (p.splits > 1) tc::cluster_sync();
@@ -502,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
 // box a warp takes 1.15 us and weight where all 16 warps work (1.2 above 8 tokens),
 // less where fewer do, as the issue slots of the SM's four schedulers bound it, down
 // to 0.55 of it; a tile 1 us more for its sums, 0.015 a token and weight, 0.01 a part,
-// 0.05 to 0.15 in clusters of 2 to 8; staging 65 bytes a ns. Fitted to every shape of
-// 109 calls (1 to 32 tokens, 512 x 3584 to 18944 x 3584, alone and gated), of which
+// 0.05 to 0.15 in clusters of 2 to 8; staging 50 bytes a ns. Fitted to every shape of
+// 136 calls (1 to 32 tokens, 512 x 3584 to 18944 x 3584, alone and gated), of which
 // it takes one within 1.2% of the fastest on average, 11% at worst: 11008 x 4096 at
 // one token 8.6 us in three parts (9.3 in two), 4096 x 11008 9.1 in rows of a CTA (9.4
 // in clusters of 2), 3584 x 18944 at 16 tokens 16.2 in clusters of 8 (20 of 4).
@@ -527,7 +529,7 @@ Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)
       if (slice > room || clusters == 0) continue;
       const int step = std::max(1, clusters / m_tiles);
       const float staged = static_cast<float>(slice) * static_cast<float>(staged_bytes(mt));
-      const float fixed = staged / 65000.0f + (sl > 0 ? 1.3f : 0.9f);
+      const float fixed = staged / 50000.0f + (sl > 0 ? 1.3f : 0.9f);
       const float sums = 1.0f + 0.015f * static_cast<float>(mt * mats) + 0.05f * static_cast<float>(sl);
       for (const int parts : {1, 2, 3, 4, 5, 8, 16}) {
         // the passes that full tiles take, then the smallest tile that takes no more
@@ -537,9 +539,11 @@ Int4Shape plan_int4(int64_t M, int64_t N, int boxes, int mats, const int (&ctas)
         const int row_tiles = (groups + rg - 1) / rg, row_step = std::min(row_tiles, step);
         const int64_t all = static_cast<int64_t>(row_step) * m_tiles;
         const float waves = static_cast<float>((all + clusters - 1) / clusters);
-        const float busy = std::max(0.55f, static_cast<float>((rg * parts + 3) / 4) / 4.0f);   // a scheduler has each fourth
+        // of the fullest of four schedulers
+        const float busy = std::max(0.55f, static_cast<float>((rg * parts + 3) / 4) / 4.0f);
         const float each = std::max(1.0f, static_cast<float>(slice) / static_cast<float>(parts));
-        const float cost = waves * (static_cast<float>(passes) * (each * box * busy + sums + 0.01f * static_cast<float>(parts << sl)) + fixed);
+        const float tile = each * box * busy + sums + 0.01f * static_cast<float>(parts << sl);
+        const float cost = waves * (static_cast<float>(passes) * tile + fixed);
         if (cost < best_cost) {
           best_cost = cost;
           best = {mt, parts, sl, rg, row_tiles, row_step, m_tiles};

@@ -220,3 +220,24 @@ def test_offsets_beyond_32_bits():
         ref, bound = product(x, tail)
         assert_near(y[:, -40:], ref, bound + U24 * ref.abs())
         assert not y[:, :-40].any()
+
+
+@pytest.mark.parametrize("M, N, K", [
+    (1, 24, 1056), (1, 1240, 4096), (1, 2888, 4096), (1, 40, 4096), (2, 2928, 4096), (1, 2504, 4096), (2, 64, 3200),
+    (1, 16, 6400), (3, 24, 3200), (1, 760, 8192), (1, 16, 12800), (8, 24, 2048), (7, 2464, 2048), (5, 2496, 2048),
+    (17, 3664, 1056), (11, 2328, 1056), (100, 648, 3200), (33, 2312, 2048), (17, 936, 3200), (17, 376, 6400),
+    (11, 24, 12800), (160, 3872, 32), (160, 3848, 512), (64, 272, 18944), (160, 296, 8192)])
+def test_clusters_and_parts(M, N, K):
+    """Reductions split over clusters of 1 to 8 and over 1 to 16 warps of a CTA, in
+    numbers that divide neither, with one row tile or several."""
+    x = make(M, K, M + N, dtype=BF16).to(DEV)
+    a, b = weight(N, K, 32), weight(N, K, 32, seed=6)
+    (g, eg), (u, eu) = product(x, a), product(x, b)
+    y = nf4.nf4_int4_matmul_fwd(x, a)
+    assert_near(y, g, eg + U24 * g.abs())
+    assert torch.equal(y, nf4.nf4_int4_matmul_fwd(x, a))
+    f, _ = on_gpu(o.act, g, "silu")
+    e = u.abs() * 1.13 * eg + (f.abs() + 1.13 * eg) * eu + relative(g, "silu") * 1.01 * (f * u).abs()
+    y = nf4.nf4_int4_gated_fwd(x, a, b, out_dtype=F32)
+    assert_near(y, f * u, e * (1 + U24) + U24 * (f * u).abs() + 1e-38)
+    assert torch.equal(y, nf4.nf4_int4_gated_fwd(x, a, b, out_dtype=F32))
