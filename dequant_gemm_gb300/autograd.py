@@ -17,6 +17,10 @@ The second half of the module does the same for the 8-bit floating point
 products, the RMS norm in front of them and the gated block between them.
 Rounding to 8 bits passes its gradient through; gradients of a product's output
 are rounded to 8 bits themselves (1 x 128 blocks) before they meet the weight.
+
+A backward pass can be captured into a CUDA graph. PyTorch ties a leaf's
+accumulation to the stream of the graph that used it first: capture on leaves of
+which no eager graph still lives (drop its outputs, or detach the leaves).
 """
 from __future__ import annotations
 
