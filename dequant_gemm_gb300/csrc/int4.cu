@@ -9,7 +9,7 @@
 // SM's four schedulers issue them at 85% of their rate while boxes go by; the first
 // box is there 3 us after the launch. Measured (CUDA graph, bf16, groups of 128): one
 // token, 4096 x 4096 5.1 us, 18944 x 3584 10.4 us (3.5 TB/s), two of them 18.2 (3.9
-// TB/s); 16 tokens 12.9 and 24.1. The legacy mma.sync takes its operands from
+// TB/s); 16 tokens 12.9 and 23.9. The legacy mma.sync takes its operands from
 // registers, where the codes are widened; for tcgen05 they would go through shared
 // or tensor memory first, and the tensor pipe is 15% busy.
 //
@@ -36,8 +36,8 @@
 //    (e2, e6) for elements e0 to e7 of 4 bytes, and the tokens are staged in that
 //    order, 16 bytes a lane.
 //  * Scales and zero points are loaded two boxes ahead, each by one lane of a row's
-//    four, packed into a word (the scale's fp32 bits leave the low 13 free) and
-//    handed to the others by shuffles.
+//    four, and handed to the others by shuffles, in one word (the scale's fp32 bits
+//    leave the low 13 free) or two.
 //  * Every warp leaves its sums of a tile in shared memory of the CTA that owns the
 //    rows, which adds them in a fixed order: repeatable, no workspace.
 #include <algorithm>
@@ -364,14 +364,21 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             ldmatrix4(slot + mat * kBoxBytes + h * 1024 + (c ? lm ^ 64u : lm), q[mat][c][h]);
-      // this box's scales as fp32 bits with the zero point below
-      uint32_t sz[kMats][kLoads];
+      // this box's scales as fp32 bits, and twice 128 + z or 1024 + z (a code's numbers
+      // less q); in groups of 32, where registers run out, z in the scale's low bits.
+      // Apart against together: two of 18944 x 3584 at one token 18.2 us for 18.4, at
+      // 16 23.9 for 24.2; groups of 32, two of 11008 x 4096 at 7 22.2 for 21.6.
+      constexpr uint32_t kOne = kF16 ? 0x64u : 0x43u;
+      constexpr bool kApart = kGroup > 32;
+      uint32_t sz[kMats][kLoads], zz[kMats][kLoads];
 #pragma unroll
       for (int mat = 0; mat < kMats; ++mat)
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           const uint32_t bits = now.s[mat][j / 2] >> (16 * (j % 2)) & 0xffffu;
-          sz[mat][j] = __float_as_uint(scale_value(bits, p.scale_bf16)) | (now.z[mat] >> (8 * j) & 0xffu);
+          sz[mat][j] = __float_as_uint(scale_value(bits, p.scale_bf16));
+          if (kApart) zz[mat][j] = __byte_perm(now.z[mat], kOne, 0x4040 + 0x0101 * j);
+          else sz[mat][j] |= now.z[mat] >> (8 * j) & 0xffu;
         }
       __syncwarp();
       now = later;
@@ -389,13 +396,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
           const int from = (lane & 28) + j / kLoads;
           const uint32_t va = __shfl_sync(0xffffffffu, sz[mat][j % kLoads], from);
           const uint32_t vb = __shfl_sync(0xffffffffu, sz[mat][j % kLoads], from + 2);
-          constexpr uint32_t kOne = kF16 ? 0x64u : 0x43u;
-          za[mat] = __byte_perm(va, kOne, 0x4040);
-          zb[mat] = __byte_perm(vb, kOne, 0x4040);
+          za[mat] = kApart ? __shfl_sync(0xffffffffu, zz[mat][j % kLoads], from) : __byte_perm(va, kOne, 0x4040);
+          zb[mat] = kApart ? __shfl_sync(0xffffffffu, zz[mat][j % kLoads], from + 2) : __byte_perm(vb, kOne, 0x4040);
           far_a[mat] = kHigh ? minus_64_z(za[mat]) : 0u;
           far_b[mat] = kHigh ? minus_64_z(zb[mat]) : 0u;
-          sa[mat] = __uint_as_float(va & 0xffffff00u);
-          sb[mat] = __uint_as_float(vb & 0xffffff00u);
+          sa[mat] = __uint_as_float(kApart ? va : va & 0xffffff00u);
+          sb[mat] = __uint_as_float(kApart ? vb : vb & 0xffffff00u);
         }
         float sum[kMats][kNT][4];
 #pragma unroll
