@@ -95,7 +95,6 @@ def lib() -> ctypes.CDLL:
             vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
             W = ctypes.POINTER(nf4_weight)
             Q = ctypes.POINTER(nf4_fp8_tensor)
-            I = ctypes.POINTER(nf4_int4_weight)
             f32 = ctypes.c_float
             sig = {
                 "nf4_quantize": [vp, i64, i64, i32, vp, vp, vp, vp],
@@ -114,14 +113,14 @@ def lib() -> ctypes.CDLL:
                 "nf4_rmsnorm_fwd": [vp, i32, vp, i32, vp, i32, i64, i64, f32, vp, vp, i32, vp, vp,
                                     vp],
                 "nf4_rmsnorm_bwd": [vp, vp, vp, i32, vp, i32, vp, i64, i64, vp, vp, vp, i64, vp],
-                # (addresses of nf4_fp8_tensor structs)
+                # (addresses of nf4_fp8_tensor and nf4_int4_weight structs)
                 "nf4_fp8_gated_fwd": [vp, vp, vp, i32, vp, i32, vp, vp, vp, vp],
                 "nf4_fp8_gated_bwd": [vp, i32, vp, vp, i64, i64, i32, vp, vp, vp, vp, vp],
                 "nf4_fp8_gated_bwd_dx": [vp, vp, vp, vp, vp, i32, i32, vp],
                 "nf4_int4_quantize": [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp],
-                "nf4_int4_dequantize": [I, vp, i32, vp],
-                "nf4_int4_matmul_fwd": [vp, i32, i64, I, vp, i32, i32, vp],
-                "nf4_int4_gated_fwd": [vp, i32, i64, I, I, i32, vp, i32, vp],
+                "nf4_int4_dequantize": [vp, vp, i32, vp],
+                "nf4_int4_matmul_fwd": [vp, i32, i64, vp, vp, i32, i32, vp],
+                "nf4_int4_gated_fwd": [vp, i32, i64, vp, vp, i32, vp, i32, vp],
                 "nf4_poll_device_status": [vp],
                 "nf4_poll_device_status_site": [vp, vp],
                 "nf4_codebook": [vp],

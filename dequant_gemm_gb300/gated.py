@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import sys
+from array import array
 
 import torch
 
@@ -32,12 +33,10 @@ def _activation(name: str) -> int:
 
 
 # Two to four nf4_fp8_tensor in a row, built at once: five 64-bit words each (the
-# low half of the last is block_rows), whose addresses the calls take. One struct
-# after the other took the host 0.6 us each.
-_WORDS = 5
+# low half of the last is block_rows), whose addresses the calls take. One ctypes
+# struct after the other took the host 0.6 us each.
 _STRUCT = ctypes.sizeof(nf4_fp8_tensor)
-assert _STRUCT == 8 * _WORDS and sys.byteorder == "little"
-_Three, _Four = ctypes.c_int64 * (3 * _WORDS), ctypes.c_int64 * (4 * _WORDS)
+assert _STRUCT == 8 * 5 and array("q").itemsize == 8 and sys.byteorder == "little"
 
 
 def _plain_pair(gate, up):
@@ -132,8 +131,8 @@ def nf4_fp8_gated_fwd(X: FP8Tensor, gate: FP8Tensor, up: FP8Tensor, activation: 
     g = u = None
     if save:
         g, u = (_empty((M, rows), dtype=_BF16, device=device) for _ in range(2))
-    structs = _Three(*left, *words)
-    at = ctypes.addressof(structs)
+    structs = array("q", left + words)
+    at = structs.buffer_info()[0]
     _call_on(device.index, "nf4_fp8_gated_fwd", at, at + _STRUCT, at + 2 * _STRUCT, act, y_ptr, elem,
              scale_ptr, None if g is None else g.data_ptr(), None if u is None else u.data_ptr())
     return y, g, u
@@ -211,8 +210,8 @@ def nf4_fp8_gated_bwd_dx(dG: FP8Tensor, dU: FP8Tensor, gate: FP8Tensor, up: FP8T
         raise ValueError("accumulate=True needs the output tensor to add to (out=)")
     _require_cuda_device(device)
     dx = _empty((M, cols), dtype=out_dtype, device=device) if out is None else out
-    structs = _Four(*left, *right, *words)
-    at = ctypes.addressof(structs)
+    structs = array("q", left + right + words)
+    at = structs.buffer_info()[0]
     _call_on(device.index, "nf4_fp8_gated_bwd_dx", at, at + _STRUCT, at + 2 * _STRUCT, at + 3 * _STRUCT,
              dx.data_ptr(), elem, ACCUMULATE if accumulate else 0)
     if out is not None:

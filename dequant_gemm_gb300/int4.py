@@ -9,6 +9,7 @@ allocate outputs with PyTorch and pass the current stream.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -21,7 +22,13 @@ from .norm import _refused, _require_matrix
 INT4_GROUPS = (32, 64, 128)
 INT4_MAX_COLS = 262144         # NF4_INT4_MAX_COLS
 _SCALES = {torch.bfloat16: ELEM[torch.bfloat16], torch.float16: ELEM[torch.float16]}
-_U8, _empty, _byref = torch.uint8, torch.empty, ctypes.byref
+_U8, _empty = torch.uint8, torch.empty
+
+# An nf4_int4_weight as six 64-bit words (little-endian: the group, and the scales'
+# type above it), whose address the calls take: as a ctypes struct it took the host
+# 1 us more.
+_STRUCT = ctypes.sizeof(nf4_int4_weight)
+assert _STRUCT == 8 * 6
 
 
 @dataclass(slots=True)
@@ -55,10 +62,10 @@ class Int4Weight:
         n = self.codes.numel() + 2 * self.scale.numel()
         return n + (0 if self.zero is None else self.zero.numel())
 
-    def c_struct(self) -> nf4_int4_weight:
-        return nf4_int4_weight(self.codes.data_ptr(), self.scale.data_ptr(),
-                               None if self.zero is None else self.zero.data_ptr(), self.rows, self.cols,
-                               self.group, _SCALES[self.scale.dtype])
+    def words(self) -> tuple:
+        """The fields of the C struct, a word each."""
+        return (self.codes.data_ptr(), self.scale.data_ptr(), 0 if self.zero is None else self.zero.data_ptr(),
+                self.rows, self.cols, self.group | _SCALES[self.scale.dtype] << 32)
 
 
 def _check_group(group: int):
@@ -87,8 +94,8 @@ def _check_int4(w: Int4Weight, name: str, device):
 
 
 def _plain_int4(w, device):
-    """The C struct of a weight that passes _check_int4, in one pass; None where
-    it does not."""
+    """The words of a weight that passes _check_int4, in one pass; None where it
+    does not."""
     try:
         codes, scale, zero = w.codes, w.scale, w.zero
         rows, half = codes.shape
@@ -99,8 +106,8 @@ def _plain_int4(w, device):
                 and scale.is_contiguous() and codes.device == device and scale.device == device
                 and (zero is None or zero.dtype is _U8 and zero.shape == scale.shape and zero.is_contiguous()
                      and zero.device == device)):
-            return nf4_int4_weight(codes.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
-                                   rows, 2 * half, group, _SCALES[scale.dtype])
+            return (codes.data_ptr(), scale.data_ptr(), 0 if zero is None else zero.data_ptr(), rows, 2 * half,
+                    group | _SCALES[scale.dtype] << 32)
     except (AttributeError, TypeError, ValueError, IndexError, ZeroDivisionError):
         pass
     return None
@@ -164,7 +171,8 @@ def nf4_int4_dequantize(w: Int4Weight, out: torch.Tensor | None = None,
     _require_cuda_device(w.device)
     y = out if out is not None else _empty(shape, dtype=out_dtype, device=w.device)
     try:
-        _call_on(w.device.index, "nf4_int4_dequantize", _byref(w.c_struct()), y.data_ptr(), ELEM[out_dtype])
+        struct = array("q", w.words())
+        _call_on(w.device.index, "nf4_int4_dequantize", struct.buffer_info()[0], y.data_ptr(), ELEM[out_dtype])
     except NF4Error as error:
         _refused(error, out=out, **{"w.codes": w.codes})
     if out is not None:
@@ -196,11 +204,11 @@ def nf4_int4_matmul_fwd(X: torch.Tensor, w: Int4Weight, out: torch.Tensor | None
     """Y = X * value(w)^T (+ out when accumulate): X bf16 or fp16 [M, cols] -> Y
     fp32, bf16 or fp16 [M, rows]. For few tokens: the weight is read once for
     every 16."""
-    struct = _plain_int4(w, X.device) if _plain_x(X) else None
-    if struct is None or X.shape[1] != struct.cols or struct.cols > INT4_MAX_COLS:
+    words = _plain_int4(w, X.device) if _plain_x(X) else None
+    if words is None or X.shape[1] != words[4] or words[4] > INT4_MAX_COLS:
         _check_x(X, w=w)
-        struct = w.c_struct()
-    M = X.shape[0]
+        words = w.words()
+    M, rows = X.shape[0], words[3]
     if out is not None:
         if not isinstance(out, torch.Tensor):
             raise ValueError("out must be a tensor")
@@ -209,15 +217,16 @@ def nf4_int4_matmul_fwd(X: torch.Tensor, w: Int4Weight, out: torch.Tensor | None
     if elem is None:
         raise ValueError(f"the output must be float32, bfloat16 or float16, got {out_dtype}")
     if out is not None:
-        _require(out, "out", out_dtype, shape=(M, struct.rows))
+        _require(out, "out", out_dtype, shape=(M, rows))
         _same_device(X.device, out=out)
     elif accumulate:
         raise ValueError("accumulate=True needs the output tensor to add to (out=)")
     device = X.device
     _require_cuda_device(device)
-    y = _empty((M, struct.rows), dtype=out_dtype, device=device) if out is None else out
+    y = _empty((M, rows), dtype=out_dtype, device=device) if out is None else out
     try:
-        _call_on(device.index, "nf4_int4_matmul_fwd", X.data_ptr(), _SCALES[X.dtype], M, _byref(struct),
+        struct = array("q", words)
+        _call_on(device.index, "nf4_int4_matmul_fwd", X.data_ptr(), _SCALES[X.dtype], M, struct.buffer_info()[0],
                  y.data_ptr(), elem, ACCUMULATE if accumulate else 0)
     except NF4Error as error:
         _refused(error, X=X, **{"w.codes": w.codes})
@@ -235,11 +244,11 @@ def nf4_int4_gated_fwd(X: torch.Tensor, gate: Int4Weight, up: Int4Weight, activa
     a = b = None
     if _plain_x(X):
         a, b = _plain_int4(gate, X.device), _plain_int4(up, X.device)
-    if a is None or b is None or X.shape[1] != a.cols or a.cols > INT4_MAX_COLS:
+    if a is None or b is None or X.shape[1] != a[4] or a[4] > INT4_MAX_COLS:
         _check_x(X, gate=gate)
         _check_int4(up, "up", X.device)
-        a, b = gate.c_struct(), up.c_struct()
-    if (a.rows, a.cols, a.group, a.scale_elem) != (b.rows, b.cols, b.group, b.scale_elem):
+        a, b = gate.words(), up.words()
+    if a[3:] != b[3:]:
         raise ValueError("gate and up must have the same shape, group and scale type")
     act = _activation(activation)
     out_dtype = X.dtype if out_dtype is None else out_dtype
@@ -249,9 +258,11 @@ def nf4_int4_gated_fwd(X: torch.Tensor, gate: Int4Weight, up: Int4Weight, activa
     device = X.device
     _require_cuda_device(device)
     M = X.shape[0]
-    y = _empty((M, a.rows), dtype=out_dtype, device=device)
+    y = _empty((M, a[3]), dtype=out_dtype, device=device)
     try:
-        _call_on(device.index, "nf4_int4_gated_fwd", X.data_ptr(), _SCALES[X.dtype], M, _byref(a), _byref(b), act,
+        structs = array("q", a + b)
+        at = structs.buffer_info()[0]
+        _call_on(device.index, "nf4_int4_gated_fwd", X.data_ptr(), _SCALES[X.dtype], M, at, at + _STRUCT, act,
                  y.data_ptr(), elem)
     except NF4Error as error:
         _refused(error, X=X, **{"gate.codes": gate.codes, "up.codes": up.codes})
