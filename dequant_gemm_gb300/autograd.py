@@ -344,6 +344,12 @@ class FP8Linear(_Frozen):
         return f"in_features={self.in_features}, out_features={self.out_features}, fp8"
 
 
+# The block keeps its projections for the backward pass (4 bytes a value of theirs)
+# where a graph is recorded. A Function cannot see that: in its forward the gradient
+# mode is off, and needs_input_grad says what its inputs require in any mode. The
+# wrappers hand it in as `graph`.
+
+
 def _gated_mlp(q: FP8Tensor, gate, up, down, activation, out_dtype, keep: bool):
     """(y, g, u): y of an 8-bit operand, g and u what its gradient needs (None unless keep)."""
     a, g, u = nf4_fp8_gated_fwd(q, gate, up, activation=activation, save=keep)
@@ -362,9 +368,9 @@ class FP8GatedMLPFunction(torch.autograd.Function):
     bf16); differentiable in x, once."""
 
     @staticmethod
-    def forward(ctx, x, gate, up, down, activation="silu", out_dtype=torch.bfloat16):
+    def forward(ctx, x, gate, up, down, activation="silu", out_dtype=torch.bfloat16, graph=True):
         ctx.weights, ctx.activation = (gate, up, down), activation
-        keep = ctx.needs_input_grad[0]
+        keep = graph and ctx.needs_input_grad[0]
         q = nf4_fp8_quantize(_matrix(x, x.shape[-1]))
         y, g, u = _gated_mlp(q, gate, up, down, activation, out_dtype, keep)
         if keep:
@@ -377,27 +383,27 @@ class FP8GatedMLPFunction(torch.autograd.Function):
         x, g, u = ctx.saved_tensors
         out = torch.bfloat16 if x.dtype == torch.bfloat16 else torch.float32
         dx = _gated_mlp_grad(gy, g, u, *ctx.weights, ctx.activation, out)
-        return dx.reshape(x.shape).to(x.dtype), None, None, None, None, None
+        return dx.reshape(x.shape).to(x.dtype), *[None] * 6
 
 
 def fp8_gated_mlp(x: torch.Tensor, gate: FP8Tensor, up: FP8Tensor, down: FP8Tensor, activation: str = "silu",
                   out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The gated feed-forward block on frozen 8-bit weights; differentiable in x."""
-    return FP8GatedMLPFunction.apply(x, gate, up, down, activation, out_dtype)
+    return FP8GatedMLPFunction.apply(x, gate, up, down, activation, out_dtype, torch.is_grad_enabled())
 
 
 class NormFP8GatedMLPFunction(torch.autograd.Function):
     """The norm and the gated block that reads its output, joined: (h, y)."""
 
     @staticmethod
-    def forward(ctx, x, norm_weight, residual, eps, gate, up, down, activation, out_dtype):
+    def forward(ctx, x, norm_weight, residual, eps, gate, up, down, activation, out_dtype, graph=True):
         shape = x.shape
         rows = _matrix(x, shape[-1])
         res = None if residual is None else _aligned(residual.reshape(rows.shape))
         q, h, rstd = nf4_rmsnorm_fwd(rows, _aligned(norm_weight), res, eps=eps,
                                      out_dtype=torch.float8_e4m3fn, save_rstd=True)
         h = x if residual is None else h.reshape(shape)
-        keep = any(ctx.needs_input_grad[:3])
+        keep = graph and any(ctx.needs_input_grad[:3])
         y, g, u = _gated_mlp(q, gate, up, down, activation, out_dtype, keep)
         ctx.weights, ctx.activation, ctx.x_dtype, ctx.shape = (gate, up, down), activation, x.dtype, shape
         ctx.res_shape = None if residual is None else residual.shape
@@ -421,7 +427,7 @@ class NormFP8GatedMLPFunction(torch.autograd.Function):
         dx, dweight = nf4_rmsnorm_bwd(dy, h, _aligned(norm_weight), rstd, dh=dh)
         dx = dx.reshape(ctx.shape)
         return (dx.to(ctx.x_dtype), dweight, dx.reshape(ctx.res_shape) if ctx.res_shape else None,
-                *[None] * 6)
+                *[None] * 7)
 
 
 def norm_fp8_gated_mlp(x: torch.Tensor, norm_weight: torch.Tensor, gate: FP8Tensor, up: FP8Tensor,
@@ -429,7 +435,8 @@ def norm_fp8_gated_mlp(x: torch.Tensor, norm_weight: torch.Tensor, gate: FP8Tens
                        out_dtype: torch.dtype = torch.bfloat16):
     """h = x + residual and the gated block of rms_norm(h): (h, y). Differentiable in
     x, the residual and the norm's weight."""
-    return NormFP8GatedMLPFunction.apply(x, norm_weight, residual, eps, gate, up, down, activation, out_dtype)
+    return NormFP8GatedMLPFunction.apply(x, norm_weight, residual, eps, gate, up, down, activation, out_dtype,
+                                         torch.is_grad_enabled())
 
 
 class FP8GatedMLP(_Frozen):

@@ -144,3 +144,42 @@ def test_checkpointed(calls):
     want, = torch.autograd.grad(ag.fp8_gated_mlp(x, *weights()).float().sum(), x)
     y = torch.utils.checkpoint.checkpoint(lambda x: ag.fp8_gated_mlp(x, *weights()), x, use_reentrant=False)
     assert torch.equal(torch.autograd.grad(y.float().sum(), x)[0], want)
+
+
+def test_nothing_is_kept_where_no_graph_is_recorded(calls, monkeypatch):
+    """Under no_grad and inference_mode a parameter still requires a gradient, and so
+    may an input: the projections are not asked for all the same. A checkpoint that
+    runs its first pass under no_grad asks for them in the second alone."""
+    saves, fwd = [], ag.nf4_fp8_gated_fwd
+
+    def recorded(*args, save=False, **kw):
+        saves.append(save)
+        return fwd(*args, save=save, **kw)
+
+    monkeypatch.setattr(ag, "nf4_fp8_gated_fwd", recorded)
+    x, nw = rand(5, 16, seed=4).requires_grad_(), torch.nn.Parameter(rand(16, seed=5))
+    w, r = weights(), rand(5, 16, seed=6)
+
+    def forms(x):
+        return [lambda: ag.fp8_gated_mlp(x, *w), lambda: ag.norm_fp8_gated_mlp(x, nw, *w)[1],
+                lambda: ag.norm_fp8_gated_mlp(x, nw, *w, residual=r)[1]]
+
+    want = [f() for f in forms(x)]
+    assert saves == [True] * 3 and all(y.requires_grad for y in want)
+    for mode in (torch.no_grad, torch.inference_mode):
+        for leaf in (x, x.detach()):
+            saves.clear()
+            with mode():
+                got = [f() for f in forms(leaf)]
+            assert saves == [False] * 3
+            assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
+    for f in forms(x):
+        saves.clear()
+        y = torch.utils.checkpoint.checkpoint(lambda _: f(), x, use_reentrant=True)
+        assert saves == [False]
+        y.float().sum().backward()
+        assert saves == [False, True]
+    with torch.no_grad():                                # and a graph that is recorded inside
+        saves.clear()
+        with torch.enable_grad():
+            assert ag.fp8_gated_mlp(x, *w).requires_grad and saves == [True]
