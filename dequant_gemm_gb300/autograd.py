@@ -365,7 +365,9 @@ def _gated_mlp_grad(gy, g, u, gate, up, down, activation, out_dtype):
 class FP8GatedMLPFunction(torch.autograd.Function):
     """y = (act(x gate^T) * (x up^T)) down^T, x [..., cols] (fp32, bf16 or fp16)
     and the product in front of down rounded to 8 bits, y of `out_dtype` (fp32 or
-    bf16); differentiable in x, once."""
+    bf16); differentiable in x, once. Returns (y, tie): the gradient does not read x,
+    which is not kept (it may change in place); an output without elements, `tie`,
+    takes its place in the graph that raises (_once)."""
 
     @staticmethod
     def forward(ctx, x, gate, up, down, activation="silu", out_dtype=torch.bfloat16, graph=True):
@@ -373,23 +375,25 @@ class FP8GatedMLPFunction(torch.autograd.Function):
         keep = graph and ctx.needs_input_grad[0]
         q = nf4_fp8_quantize(_matrix(x, x.shape[-1]))
         y, g, u = _gated_mlp(q, gate, up, down, activation, out_dtype, keep)
+        ctx.x_dtype, ctx.shape = x.dtype, x.shape
+        tie = y.new_empty(0)
         if keep:
-            ctx.save_for_backward(x, g, u)       # x: for the graph of a gradient that may not be used (_once)
-        return y.reshape(*x.shape[:-1], down.rows)
+            ctx.save_for_backward(g, u, tie)
+        return y.reshape(*x.shape[:-1], down.rows), tie
 
     @staticmethod
     @_once
-    def backward(ctx, gy):
-        x, g, u = ctx.saved_tensors
-        out = torch.bfloat16 if x.dtype == torch.bfloat16 else torch.float32
+    def backward(ctx, gy, _):
+        g, u, _ = ctx.saved_tensors
+        out = torch.bfloat16 if ctx.x_dtype == torch.bfloat16 else torch.float32
         dx = _gated_mlp_grad(gy, g, u, *ctx.weights, ctx.activation, out)
-        return dx.reshape(x.shape).to(x.dtype), *[None] * 6
+        return dx.reshape(ctx.shape).to(ctx.x_dtype), *[None] * 6
 
 
 def fp8_gated_mlp(x: torch.Tensor, gate: FP8Tensor, up: FP8Tensor, down: FP8Tensor, activation: str = "silu",
                   out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The gated feed-forward block on frozen 8-bit weights; differentiable in x."""
-    return FP8GatedMLPFunction.apply(x, gate, up, down, activation, out_dtype, torch.is_grad_enabled())
+    return FP8GatedMLPFunction.apply(x, gate, up, down, activation, out_dtype, torch.is_grad_enabled())[0]
 
 
 class NormFP8GatedMLPFunction(torch.autograd.Function):

@@ -183,3 +183,38 @@ def test_nothing_is_kept_where_no_graph_is_recorded(calls, monkeypatch):
         saves.clear()
         with torch.enable_grad():
             assert ag.fp8_gated_mlp(x, *w).requires_grad and saves == [True]
+
+
+def test_the_input_is_not_kept(calls):
+    """The gradient takes the two projections alone: nothing of the input's size is
+    saved, it may change in place before the backward pass (a residual added to it),
+    and a second order is refused all the same."""
+    seen, w = [], weights()
+    leaf, gy = rand(5, 16, seed=4).requires_grad_(), rand(5, 32, seed=7)
+    down = types.SimpleNamespace(rows=16, cols=24, dense=rand(16, 24, seed=3, dtype=F64))
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: seen.append(t) or t, lambda t: t):
+        y = ag.fp8_gated_mlp(leaf * 1.0, *w)             # (the product's factor is no tensor)
+    assert sum(t.numel() for t in seen) == 2 * 5 * 24 and all(t.dtype == F64 for t in seen if t.numel())
+    y.float().backward(gy)
+    kept = leaf.grad.clone()
+    leaf.grad = None
+    ag.fp8_gated_mlp(leaf, *w).float().backward(gy)
+    assert torch.equal(leaf.grad, kept)
+
+    def step(inplace):
+        h = leaf * 1.0
+        y = ag.fp8_gated_mlp(h, w[0], w[1], down, "silu", torch.float32)
+        if inplace:
+            h += y
+        else:
+            h = h + y
+        return h
+
+    g = rand(5, 16, seed=8)
+    want, = torch.autograd.grad(step(False), leaf, g)
+    got, = torch.autograd.grad(step(True), leaf, g)
+    assert torch.equal(got, want)
+    once, = torch.autograd.grad(step(True), leaf, g, create_graph=True)
+    assert torch.equal(once, want)
+    with pytest.raises(RuntimeError, match="once"):
+        torch.autograd.grad(once.square().sum(), leaf)
