@@ -365,9 +365,9 @@ def _gated_mlp_grad(gy, g, u, gate, up, down, activation, out_dtype):
 class FP8GatedMLPFunction(torch.autograd.Function):
     """y = (act(x gate^T) * (x up^T)) down^T, x [..., cols] (fp32, bf16 or fp16)
     and the product in front of down rounded to 8 bits, y of `out_dtype` (fp32 or
-    bf16); differentiable in x, once. Returns (y, tie): the gradient does not read x,
-    which is not kept (it may change in place); an output without elements, `tie`,
-    takes its place in the graph that raises (_once)."""
+    bf16); differentiable in x, once. Returns (y, g): the gradient does not read x,
+    which is not kept (it may change in place); the projection g, an output for that
+    reason alone, ties the graph that raises to x (_once)."""
 
     @staticmethod
     def forward(ctx, x, gate, up, down, activation="silu", out_dtype=torch.bfloat16, graph=True):
@@ -376,15 +376,17 @@ class FP8GatedMLPFunction(torch.autograd.Function):
         q = nf4_fp8_quantize(_matrix(x, x.shape[-1]))
         y, g, u = _gated_mlp(q, gate, up, down, activation, out_dtype, keep)
         ctx.x_dtype, ctx.shape = x.dtype, x.shape
-        tie = y.new_empty(0)
+        ctx.set_materialize_grads(False)     # (g's is None)
         if keep:
-            ctx.save_for_backward(g, u, tie)
-        return y.reshape(*x.shape[:-1], down.rows), tie
+            ctx.save_for_backward(g, u)
+        return y.reshape(*x.shape[:-1], down.rows), g
 
     @staticmethod
     @_once
     def backward(ctx, gy, _):
-        g, u, _ = ctx.saved_tensors
+        g, u = ctx.saved_tensors
+        if gy is None:
+            return torch.zeros(ctx.shape, dtype=ctx.x_dtype, device=g.device), *[None] * 6
         out = torch.bfloat16 if ctx.x_dtype == torch.bfloat16 else torch.float32
         dx = _gated_mlp_grad(gy, g, u, *ctx.weights, ctx.activation, out)
         return dx.reshape(ctx.shape).to(ctx.x_dtype), *[None] * 6

@@ -194,7 +194,7 @@ def test_the_input_is_not_kept(calls):
     down = types.SimpleNamespace(rows=16, cols=24, dense=rand(16, 24, seed=3, dtype=F64))
     with torch.autograd.graph.saved_tensors_hooks(lambda t: seen.append(t) or t, lambda t: t):
         y = ag.fp8_gated_mlp(leaf * 1.0, *w)             # (the product's factor is no tensor)
-    assert sum(t.numel() for t in seen) == 2 * 5 * 24 and all(t.dtype == F64 for t in seen if t.numel())
+    assert sum(t.numel() for t in seen) == 2 * 5 * 24 and all(t.dtype == F64 for t in seen)
     y.float().backward(gy)
     kept = leaf.grad.clone()
     leaf.grad = None
@@ -218,3 +218,19 @@ def test_the_input_is_not_kept(calls):
     assert torch.equal(once, want)
     with pytest.raises(RuntimeError, match="once"):
         torch.autograd.grad(once.square().sum(), leaf)
+
+
+def test_no_gradient_is_zeros(calls):
+    """Where nothing comes back for y, x gets zeros and no kernel runs."""
+    class Cut(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, y):
+            return y.clone()
+
+        @staticmethod
+        def backward(ctx, gy):
+            return None
+
+    x = rand(2, 3, 16, seed=4, dtype=torch.bfloat16).requires_grad_()
+    Cut.apply(ag.fp8_gated_mlp(x, *weights())).float().sum().backward()
+    assert torch.equal(x.grad, torch.zeros_like(x)) and "nf4_fp8_gated_bwd" not in calls
