@@ -284,6 +284,58 @@ def test_gradients_against_differences(name):
     assert abs(got - want) <= bound + 1e-3 * abs(want)
 
 
+@pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
+def test_gradients_along_themselves(name):
+    """The derivative of sum(Y * c) along the 64-bit gradient v itself, by central
+    differences, against <dX, v>: no cancellation hides a lost part, since each of
+    both reductions makes up more than twice the bound.
+    G and U are off by their products' e and bf16's 2^-8 (moved); |act''| < 0.81, so
+    dG = c U act'(G) is off by |c| (0.81 |U| moved(G) + |act'| moved(U) + the product of
+    both), dU = c act(G) by 1.13 |c| moved(G), the arithmetic of either by 2^-12 of its
+    terms (|p| < 160: r < 2^-14, above). In 8 bits 2^-4 of the value or 2^-10 of the
+    scale, three roundings in fp32. Then the input gradient's own bound."""
+    M, N, K = 12, 272, 2048
+    x = nf4.nf4_fp8_quantize(make(M, K, 1))
+    wg, wu = weights(N, K)
+    X, Wg, Wu = values64(x), values64(wg), values64(wu)
+    (G, eG), (U, eU) = project(x, wg), project(x, wu)
+    c = make(M, N, 7, 0.1)
+    C = c.double()
+    f, slope = on_gpu(o.act, G, name)
+    p, dp = on_gpu(o.exponent, G, name)
+    assert float(p.abs().max()) < 160
+    tG, tU = C * U * slope, C * f
+    v = tG @ Wg + tU @ Wu
+    v *= M * K / float(v.abs().sum())
+    parts = float((tG * (v @ Wg.t())).sum()), float((tU * (v @ Wu.t())).sum())
+
+    def total(t):
+        A, B = (X + t * v) @ Wg.t(), (X + t * v) @ Wu.t()
+        return float((on_gpu(o.act, A, name)[0] * B * C).sum())
+
+    h = 1e-5
+    want = (total(h) - total(-h)) / (2 * h)
+    assert abs(want - sum(parts)) <= 1e-6 * abs(want)     # the formulas' own gradient
+    _, g, u = nf4.nf4_fp8_gated_fwd(x, wg, wu, activation=name, save=True)
+    dg, du = nf4.nf4_fp8_gated_bwd(c, g, u, activation=name)
+    got = float((nf4.nf4_fp8_gated_bwd_dx(dg, du, wg, wu).double() * v).sum())
+    mG, mU = (e + 2.0 ** -8 * (t.abs() + e) for t, e in ((G, eG), (U, eU)))
+    each = 2.0 ** -12 * C.abs() * (1 + (G * dp).abs())
+    bG = C.abs() * (0.81 * U.abs() * mG + slope.abs() * mU + 0.81 * mG * mU) + each * (U.abs() + mU)
+    bU = 1.13 * C.abs() * mG + each * G.abs()
+
+    def eight(q, t, b):
+        s = q.scale.double().repeat_interleave(128, 1)[:, :N]
+        return b + torch.maximum((t.abs() + b) * 2.0 ** -4, s * 2.0 ** -10) * (1 + 2.0 ** -20)
+
+    bG, bU = eight(dg, tG, bG), eight(du, tU, bU)
+    terms = (tG.abs() + bG) @ Wg.abs() + (tU.abs() + bU) @ Wu.abs()
+    own = (128 * 2.0 ** -23 + (4 + 2 * -(-N // 128)) * U24) * float((terms * v.abs()).sum())
+    bound = float((bG * (v @ Wg.t()).abs()).sum() + (bU * (v @ Wu.t()).abs()).sum()) + own + 1e-6 * abs(want)
+    assert all(q > 2 * bound for q in parts)
+    assert abs(got - want) <= bound
+
+
 def test_row_slices_and_another_stream():
     wg, wu = weights(256, 400)
     q = nf4.nf4_fp8_quantize(make(200, 400, 6))
