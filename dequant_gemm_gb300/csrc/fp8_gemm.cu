@@ -174,9 +174,9 @@ struct MatmulArgs {
 // other 64 columns are in the partner warp. Its gradient runs through the two
 // operand pairs' blocks one after the other. Both are bound as the plain products,
 // by a block's way through tensor memory and back. Measured (CUDA graph): forward,
-// 4096 tokens, two of 11008 x 4096, 8-bit output, both projections kept, 298 us, 2.48
-// PFLOP/s (two plain products 292); gradient, 2048 tokens, the same weights, 141 us,
-// 2.62 PFLOP/s.
+// 4096 tokens, two of 11008 x 4096, 8-bit output, both projections kept, 301 us, 2.45
+// PFLOP/s (two plain products 284; at the power limit 316 and 293); gradient, 2048
+// tokens, the same weights, 141 us, 2.61 PFLOP/s.
 // Persistent: a pair takes the tiles c, c + G, ... in turn, tokens fastest,
 // and the copies and MMAs of the next tile start while one is written out.
 //
@@ -671,8 +671,8 @@ fp8_pair_kernel(const __grid_constant__ PairMaps<kMode> maps, const __grid_const
 // MMAs a block, into neighbouring columns; each has its own totals warps, and
 // the totals of both meet in the inbox, where act(G) U is taken. A warp then
 // holds a token's 128 columns: the block of an 8-bit output. Bound by HBM: two of
-// 18944 x 3584, 8-bit output, 24.7 us at one token (5.5 TB/s), 29.3 at 64; two of
-// 11008 x 4096 19.2 and 25.6 (4.7 and 3.5 TB/s: 86 of 152 SMs).
+// 18944 x 3584, 8-bit output, 24.0 us at one token (5.7 TB/s), 28.8 at 64; two of
+// 11008 x 4096 19.1 and 24.9 (4.7 and 3.7 TB/s: 86 of 152 SMs).
 template <int kBT, int kMats>
 struct RowsCfg {
   static constexpr int kGroups = kBT >= 64 ? 2 : 1;      // token groups, four warps each and weight

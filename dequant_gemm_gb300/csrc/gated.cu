@@ -10,8 +10,8 @@ namespace {
 // dG and dU: a streaming pass (6 or 8 bytes read and 2 written per value). 16
 // lanes hold a 1 x 128 block, 8 values each; both gradients are taken from one
 // sigma, in pairs of fp32 operations, and their blocks' largest magnitudes meet by
-// shuffles. 2048 x 11008 bf16: 31.8 us, 5.7 TB/s (with two blocks a half-warp in
-// flight, 58 registers instead of 40, 32.3).
+// shuffles. 2048 x 11008 bf16: 30.9 us, 5.8 TB/s (with two blocks a half-warp in
+// flight, 58 registers instead of 40, 0.5 us more).
 template <int kElem>
 struct Run {               // 8 values as they lie in memory
   uint4 v[kElem == kElemF32 ? 2 : 1];

@@ -7,11 +7,12 @@
 // tokens. What it takes is issue slots: a box of 16 x 256 codes costs a warp ~360
 // instructions (16 tokens 540), half of them to make operands of codes, and the
 // SM's four schedulers issue them at 85% of their rate while boxes go by; the first
-// box is there 3 us after the launch. Measured (CUDA graph, bf16, groups of 128): one
-// token, 4096 x 4096 5.1 us, 18944 x 3584 10.4 us (3.5 TB/s), two of them 18.2 (3.9
-// TB/s); 16 tokens 12.9 and 23.9. The legacy mma.sync takes its operands from
-// registers, where the codes are widened; for tcgen05 they would go through shared
-// or tensor memory first, and the tensor pipe is 15% busy.
+// box is there 3 us after the launch. Measured (CUDA graph of 24 calls, weights rotated
+// through more than L2, bf16, groups of 128): one token, 4096 x 4096 5.1 us, 18944 x
+// 3584 9.9 us (3.6 TB/s), two of them 17.7 (4.0 TB/s); 16 tokens 12.7 and 23.2. The
+// legacy mma.sync takes its operands from registers, where the codes are widened; for
+// tcgen05 they would go through shared or tensor memory first, and the tensor pipe is
+// 17 to 18% busy.
 //
 // The weight's rows are the 16 rows of mma.sync.m16n8k16, the tokens
 // its 8 columns (one or two tiles). Nothing is rounded on the way: a code
@@ -513,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_matmul_kernel(const __grid_c
 // 0.05 to 0.15 in clusters of 2 to 8; staging 50 bytes a ns. Fitted to every shape of
 // 136 calls (1 to 32 tokens, 512 x 3584 to 18944 x 3584, alone and gated), of which
 // it takes one within 1.2% of the fastest on average, 11% at worst: 11008 x 4096 at
-// one token 8.6 us in three parts (9.3 in two), 4096 x 11008 9.1 in rows of a CTA (9.4
-// in clusters of 2), 3584 x 18944 at 16 tokens 16.2 in clusters of 8 (20 of 4).
+// one token 8.4 us in three parts (8.9 in two), 4096 x 11008 8.8 in rows of a CTA (9.1
+// in clusters of 2), 3584 x 18944 at 16 tokens 16.1 in clusters of 8 (21.7 of 4).
 struct Int4Shape {
   int tokens, parts, splits_log, row_groups;
   int row_tiles, row_step, m_tiles;

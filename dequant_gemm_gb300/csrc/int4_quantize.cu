@@ -16,9 +16,9 @@ namespace {
 // w - q s is exact in one FMA, and RN(q + rem r) is the correctly rounded quotient
 // (Markstein) where nothing leaves the normal range: s >= 2^-64 (smaller scales
 // divide), and quotients near a half or above, which alone matter.
-// Measured at 11008 x 4096 with zero points, 1, 2, 3 and 4 steps: fp32 35.5, 33.8, 34.2
-// and 34.8 us (6.0 TB/s), bf16 28.2, 26.9, 25.8 and 27.4 (the arithmetic). Back: bf16
-// 21 us, fp32 32 (6.4 TB/s).
+// Measured at 11008 x 4096, 1, 2, 3 and 4 steps: fp32 with zero points 34.2, 32.6, 33.0
+// and 33.4 us (two: 6.3 TB/s), bf16 32.3, 29.9, 30.0 and 30.9 (the arithmetic), without
+// zero points 27.0, 25.9, 24.9 and 26.6. Back: bf16 19.8 us, fp32 34.0 (6.0 TB/s).
 constexpr int kQuantUnroll = 2;
 constexpr float kSmallScale = 5.421010862427522e-20f;     // 2^-64
 

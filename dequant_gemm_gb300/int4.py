@@ -1,9 +1,12 @@
 """Uniform 4-bit weights with a 16-bit scale, and a zero point, for each group of
-32, 64 or 128 values along a row, and products of few tokens with them: the
-layout that most 4-bit checkpoints come in, for decoding.
+32, 64 or 128 values along a row, and products of few tokens with them, for
+decoding.
 
 A value is (code - zero point) * scale; ``include/nf4gemm.h`` states the
-format. As everywhere in the package, the functions check their arguments,
+format: two codes a byte in the order of the row, scales and zero points not
+packed. Checkpoints that hold such weights otherwise (eight codes an int32,
+transposed or interleaved columns, packed or shifted zero points) have to be
+brought into this order first; nothing here does. As everywhere in the package, the functions check their arguments,
 allocate outputs with PyTorch and pass the current stream.
 """
 from __future__ import annotations
